@@ -12,6 +12,11 @@ Steps (TensorFold PR #903, "Step-5-Preview on one 256 GB Mac", CSA-indexer commi
   step5_sparse_attn       -- attention over the picked regions plus the row's own region
   step5_sparse_attn_gated -- the same, followed by the per-head sigmoid output gate
   step5_indexer_front     -- decode front end: q/k norms, k/z cache write, summary on completion
+
+The paged KV cache that step (4) can read in 8 bits (``PagedCache``):
+  step5_kv_append, step5_kv_append_e4m3 -- rotate and append the rows' keys and values
+  step5_paged_attn_e4m3   -- causal (or sliding-window) attention over the e4m3 pages
+  step5_sparse_attn_e4m3  -- step (4) over the e4m3 pages
 """
 from __future__ import annotations
 
@@ -36,6 +41,8 @@ __all__ = [
     "step5_workspace_bytes", "step5_workspace_init", "step5_device_status",
     "step5_set_select_path", "step5_set_wait_polls", "step5_set_attention_path", "step5_select_path_for", "step5_set_prologue_overlap", "step5_decode_step", "step5_status_string", "step5_convert_bf16_to_e4m3",
     "Workspace", "decode_step",
+    "Pages", "PagedCache", "PagedWorkspace", "step5_kv_append", "step5_kv_append_e4m3", "step5_paged_attn_e4m3",
+    "step5_sparse_attn_e4m3", "step5_paged_workspace_bytes", "decode_step_paged",
 ]
 
 STATUS = {0: "STEP5_OK", 1: "STEP5_ERR_INVALID_ARGUMENT", 2: "STEP5_ERR_UNSUPPORTED",
@@ -91,6 +98,7 @@ def load():
     lib = ctypes.CDLL(LIB)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     G = ctypes.POINTER(Geometry)
+    PG = ctypes.POINTER(Pages)
     sigs = {
         "step5_region_summarize": (i32, [G, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P]),
         "step5_index_score_topk": (i32, [G, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P,
@@ -112,6 +120,12 @@ def load():
         "step5_rows_layout_for": (i32, [G, i32, i32, ctypes.POINTER(RowsLayout)]),
         "step5_decode_step_host": (i32, [G, i32, i32, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P,
                                          P, sz, P]),
+        "step5_kv_append": (i32, [G, PG, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P]),
+        "step5_kv_append_e4m3": (i32, [G, PG, i32, i32, i32, i32, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P,
+                                       P, P]),
+        "step5_paged_attn_e4m3": (i32, [G, PG, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "step5_sparse_attn_e4m3": (i32, [G, PG, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "step5_paged_workspace_bytes": (sz, [G]),
         "step5_workspace_bytes": (sz, [G, i32, i32]),
         "step5_workspace_init": (i32, [P, sz, P]),
         "step5_device_status": (i32, [ctypes.POINTER(ctypes.c_uint32), P]),
@@ -479,3 +493,196 @@ def decode_step(geom, t: dict, ws: Workspace, sel_ids, sel_count, out, max_regio
         step5_set_prologue_overlap(prev)
     step5_sparse_attn(geom, t["q"], t["k_cache"], t["v_cache"], t["row_seq"], t["row_pos"],
                       sel_ids, sel_count, out, ws.tensor, stream=stream)
+
+
+class Pages(ctypes.Structure):
+    """Shape of a paged pool (step5_pages)."""
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("table_len", ctypes.c_int32)]
+
+
+class PagedCache:
+    """A paged KV cache: pools ``k``, ``v`` [num_pages][G][page_tokens][128] (bf16, or uint8
+    e4m3 codes with fp32 ``k_scales``, ``v_scales`` [num_pages][G][page_tokens / 8]) and the
+    int32 ``block_table`` [B][table_len] of page numbers.  ``block_table`` None: sequence b owns
+    page b, so that contiguous caches [B][G][t_cap][128] are a PagedCache as they are.  The
+    tensors belong to the caller, who may change the table's entries between calls; give a
+    table of another shape to a new PagedCache."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: Optional[torch.Tensor] = None,
+                 k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be pools [num_pages][G][page_tokens][128] of one shape and type")
+        if k.dtype not in (torch.bfloat16, torch.uint8):
+            raise ValueError("pools are bf16 or e4m3 codes (uint8)")
+        self.e4m3 = k.dtype == torch.uint8
+        pages, groups, tokens, _ = k.shape
+        want = (pages, groups, tokens // 8)
+        for s in (k_scales, v_scales):
+            if self.e4m3 != (s is not None):
+                raise ValueError("e4m3 pools come with k_scales and v_scales, bf16 pools without")
+            if s is not None and (tuple(s.shape) != want or s.dtype != torch.float32):
+                raise ValueError(f"scales must be fp32 {want}")
+        if block_table is not None and (block_table.dim() != 2 or block_table.dtype != torch.int32):
+            raise ValueError("block_table must be int32 [B][table_len]")
+        self.k, self.v, self.block_table, self.k_scales, self.v_scales = k, v, block_table, k_scales, v_scales
+        self.B = pages if block_table is None else block_table.shape[0]
+        self.pages = Pages(pages, tokens, 1 if block_table is None else block_table.shape[1])
+
+    @classmethod
+    def create(cls, geom, num_pages: int, page_tokens: int, block_table: torch.Tensor, e4m3: bool = True,
+               device="cuda") -> "PagedCache":
+        """An empty cache (codes 0, scales 1)."""
+        g = Geometry.of(geom)
+        shape = (num_pages, g.num_kv_groups, page_tokens, g.head_dim)
+        k, v = (torch.zeros(shape, dtype=torch.uint8 if e4m3 else torch.bfloat16, device=device) for _ in range(2))
+        if not e4m3:
+            return cls(k, v, block_table)
+        ks, vs = (torch.ones((num_pages, g.num_kv_groups, page_tokens // 8), dtype=torch.float32, device=device)
+                  for _ in range(2))
+        return cls(k, v, block_table, ks, vs)
+
+    def _args(self, geom):
+        """(pages, k, v, k_scales, v_scales, table) as the C calls take them."""
+        if self.k.shape[1] != geom.num_kv_groups or self.k.shape[3] != geom.head_dim:
+            raise ValueError("the cache's groups and head dim are not the geometry's")
+        return (ctypes.byref(self.pages), _ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales),
+                _ptr(self.block_table))
+
+
+def step5_paged_workspace_bytes(geom) -> int:
+    return load().step5_paged_workspace_bytes(ctypes.byref(Geometry.of(geom)))
+
+
+@dataclass
+class PagedWorkspace:
+    """Device workspace of the attention calls over e4m3 pages, zeroed once on creation."""
+    tensor: torch.Tensor
+
+    @classmethod
+    def create(cls, geom, device="cuda") -> "PagedWorkspace":
+        nbytes = step5_paged_workspace_bytes(geom)
+        if nbytes == 0:
+            raise Step5Error("step5_paged_workspace_bytes", 2, "unsupported geometry")
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.device(t.device):
+            step5_workspace_init(t)
+        return cls(t)
+
+
+def _rows_ptr(t: torch.Tensor, what: str, N: int, heads: int, dim: int):
+    """Pointer and row stride of a bf16 [N][heads][dim] tensor whose rows may lie apart."""
+    if tuple(t.shape) != (N, heads, dim) or t.dtype != torch.bfloat16:
+        raise ValueError(f"{what} must be bf16 [{N}][{heads}][{dim}], got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("tensors passed to libstep5sa must be on the GPU")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a row of {what} must lie together")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if N > 1 else heads * dim
+
+
+def _same_device(dev: torch.device, **tensors):
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _int32_rows(N: int, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != torch.int32 or t.shape[0] != N:
+            raise ValueError(f"{name} must be int32 with {N} rows, got {t.dtype} {tuple(t.shape)}")
+
+
+def _kv_append(fn: str, geom, k, v, cache: PagedCache, row_seq, row_pos, cos, sin, q, q_out, stream):
+    g = Geometry.of(geom)
+    N = k.shape[0]
+    if cache.e4m3 != (fn == "step5_kv_append_e4m3"):
+        raise ValueError(f"{fn} does not write this kind of pool")
+    _same_device(k.device, v=v, cache=cache.k, row_seq=row_seq, row_pos=row_pos, cos=cos, sin=sin, q=q, q_out=q_out)
+    _int32_rows(N, row_seq=row_seq, row_pos=row_pos)
+    kp, ks = _rows_ptr(k, "k", N, g.num_kv_groups, g.head_dim)
+    vp, vs = _rows_ptr(v, "v", N, g.num_kv_groups, g.head_dim)
+    qp, qs = (None, 0) if q is None else _rows_ptr(q, "q", N, g.num_q_heads, g.head_dim)
+    if q_out is not None and (q_out.dtype != torch.bfloat16 or q_out.numel() != N * g.num_q_heads * g.head_dim):
+        raise ValueError("q_out must be bf16 [N][num_q_heads][128]")
+    if cos is not None and (sin is None or cos.shape != sin.shape or cos.dtype != torch.bfloat16 or
+                            sin.dtype != torch.bfloat16):
+        raise ValueError("cos and sin must be bf16 tables of one shape")
+    t_cap, half = (1, 0) if cos is None else cos.shape
+    pages, kc, vc, ksc, vsc, table = cache._args(g)
+    scales = (ksc, vsc) if cache.e4m3 else ()
+    _check(fn, getattr(load(), fn)(ctypes.byref(g), pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
+                                   _ptr(row_seq), _ptr(row_pos), _ptr(cos), _ptr(sin), _ptr(q_out), kc, vc, *scales,
+                                   table, _stream(stream)))
+
+
+def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
+                    stream=None):
+    """Rotates the rows' k [N][G][128] (cos/sin [t_cap][rot / 2] bf16; None: no rotation) and
+    writes it and v into the bf16 cache at (row_seq, row_pos) [N] int32; with q
+    [N][Hq][128], its rotation into q_out.  q, k and v may be slices of one [N][heads][128]
+    tensor (rows apart, heads together)."""
+    _kv_append("step5_kv_append", geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+
+
+def step5_kv_append_e4m3(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
+                         stream=None):
+    """step5_kv_append into an e4m3 cache: codes and the power-of-two scale of each region
+    and group.  A sequence's rows stand together at ascending positions (see the header)."""
+    _kv_append("step5_kv_append_e4m3", geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+
+
+def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, before=(), after=()):
+    g = Geometry.of(geom)
+    N = q.shape[0]
+    if not cache.e4m3:
+        raise ValueError(f"{fn} reads e4m3 pools")
+    ws_t = ws.tensor if isinstance(ws, PagedWorkspace) else ws
+    _same_device(q.device, cache=cache.k, row_seq=row_seq, row_pos=row_pos, out=out, workspace=ws_t, gate=gate)
+    _int32_rows(N, row_seq=row_seq, row_pos=row_pos)
+    for name, t in (("q", q), ("out", out)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, g.num_q_heads, g.head_dim):
+            raise ValueError(f"{name} must be bf16 [N][{g.num_q_heads}][{g.head_dim}]")
+    if gate is not None and (gate.dtype != torch.bfloat16 or tuple(gate.shape) != (N, g.num_q_heads)):
+        raise ValueError("gate must be bf16 [N][num_q_heads]")
+    pages, kc, vc, ksc, vsc, table = cache._args(g)
+    _check(fn, getattr(load(), fn)(ctypes.byref(g), pages, N, cache.B, *before, _ptr(q), kc, vc, ksc, vsc, table,
+                                   _ptr(row_seq), _ptr(row_pos), *after, _ptr(gate), _ptr(out), _ptr(ws_t),
+                                   0 if ws_t is None else ws_t.numel() * ws_t.element_size(), _stream(stream)))
+
+
+def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
+                          stream=None):
+    """Causal attention of rows q [N][Hq][128] bf16 at (row_seq, row_pos) over the e4m3
+    cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
+    sigmoid gate [N][Hq] when given."""
+    _attend_e4m3("step5_paged_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                 before=(int(window),))
+
+
+def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
+                           gate=None, stream=None):
+    """step5_sparse_attn over the e4m3 cache: the picked regions sel_ids [N][G][top_k],
+    sel_count [N][G] and the row's own region."""
+    g, N = Geometry.of(geom), q.shape[0]
+    _int32_rows(N, sel_ids=sel_ids, sel_count=sel_count)
+    if tuple(sel_ids.shape) != (N, g.num_kv_groups, g.top_k) or tuple(sel_count.shape) != (N, g.num_kv_groups):
+        raise ValueError("sel_ids must be [N][G][top_k], sel_count [N][G]")
+    _same_device(q.device, sel_ids=sel_ids, sel_count=sel_count)
+    _attend_e4m3("step5_sparse_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                 after=(_ptr(sel_ids), _ptr(sel_count)))
+
+
+def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws: PagedWorkspace, k, v, sel_ids,
+                      sel_count, q_rot, out, max_regions_per_seq, cos=None, sin=None, gate=None, stream=None):
+    """One pass of the whole path over an e4m3 paged cache: the rows' k and v appended (and
+    t["q"] rotated into q_rot by cos/sin), then summarise, score + select over the indexer
+    tensors of ``t`` as decode_step does, and attend over the picked regions of the cache."""
+    step5_kv_append_e4m3(geom, k, v, cache, t["row_seq"], t["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)
+    step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], t["sum_begin"], t["sum_end"],
+                           t["summaries"], max_regions_per_seq=max_regions_per_seq, stream=stream)
+    step5_index_score_topk(geom, t["idx_q"], t["w"], t["row_seq"], t["row_pos"], t["cos"], t["sin"], t["summaries"],
+                           sel_ids, sel_count, ws.tensor, t_cap=t["idx_k"].shape[2], stream=stream)
+    step5_sparse_attn_e4m3(geom, q_rot, cache, t["row_seq"], t["row_pos"], sel_ids, sel_count, out, paged_ws, gate=gate,
+                           stream=stream)

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "api.cuh"
 #include "kernels.cuh"
 #include "step5_sparse_attn.h"
 
@@ -23,7 +24,7 @@ int32_t g_host_copies = 0;  // step5_decode_step_host: 1 = always through copies
 uint32_t g_wait_polls = 0;  // split path's waits on other blocks: 0 = kBarrierPolls
 int32_t g_attn_path = 0;    // step (4): 0 auto (split: cluster; one block per pair: tensor cores), 1 warp MMA kernel, 2 tensor cores
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
 // Geometry check after the vLLM Step5 DSA validation (provider groups = KV groups,
 // indexer heads divisible into them, 4/8/16 query heads per KV group) plus the shapes
@@ -68,6 +69,8 @@ int num_sms() {
     }
     return cached[dev];
 }
+
+namespace {
 
 // ------------------------------------------------------------------ workspace layout
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -139,6 +142,8 @@ Layout layout(const step5_geometry* g, int N, int r_cap) {
     return L;
 }
 
+}  // namespace
+
 // ------------------------------------------------------------------ TMA descriptors
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -153,6 +158,8 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
     });
     return fn;
 }
+
+namespace {
 
 // 3-D view of a [B][G][t_cap][128] bf16 cache as (64 dims, rows, 2 halves of a row):
 // one box (64 x 8 x 2) is a whole 8-token region, landing in shared memory as two

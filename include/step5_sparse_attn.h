@@ -363,6 +363,108 @@ step5_status step5_decode_step_host(const step5_geometry* geom, int32_t N, int32
                                     int32_t* sel_count, void* workspace, size_t workspace_bytes,
                                     step5_stream_t stream);
 
+/* ------------------------------------------------------------------------------------
+ * The paged KV cache (no counterpart in the pages: where the K/V that step (4) reads live
+ * in a serving program).  A pool holds num_pages pages of page_tokens tokens each,
+ * [num_pages][G][page_tokens][head_dim], K and V apart, and block_table [B][table_len]
+ * (device int32) names sequence b's page of tokens page_tokens * i .. in its entry i.
+ * page_tokens is a multiple of region_tokens, so a region lies in one page; num_pages * G *
+ * page_tokens and table_len * page_tokens are at most 2^31 - 1.  block_table NULL (with
+ * table_len 1 and num_pages >= B): sequence b owns page b, so that the contiguous
+ * [B][G][t_cap][head_dim] caches of the calls above are pools with page_tokens = t_cap.
+ * Two kinds of pool:
+ *  - bf16 values;
+ *  - e4m3 codes with one fp32 scale for each region and KV group (k_scales, v_scales
+ *    [num_pages][G][page_tokens / region_tokens]): value = code * scale.  Half the bytes.
+ * A row with row_seq -1 is padding: nothing is read or written for it.  A row whose
+ * sequence or position is out of range, and a table entry outside [0, num_pages), set
+ * STEP5_DEV_RANGE.  Entries of pages that no row of a call touches may hold anything. */
+typedef struct {
+    int32_t num_pages;    /* pages of the pool                                          */
+    int32_t page_tokens;  /* tokens per page, a multiple of region_tokens               */
+    int32_t table_len;    /* block-table entries per sequence                           */
+} step5_pages;
+
+/* Appends the rows' keys and values to a bf16 pool, with the rotary rotation applied on
+ * the way.  For every row n (b = row_seq[n], p = row_pos[n]) and KV group g:
+ *   k_pages[b, g, p] = NEOX rotation of k[n][g] over its first rot_dims dims (pairs
+ *           (i, i + rot_dims / 2), cos/sin [t_cap][rot_dims / 2] at row p; the exact sum
+ *           of each pair rounded once to bf16), the other dims as they are;
+ *   v_pages[b, g, p] = v[n][g];
+ *   q_out[n][h] = the same rotation of q[n][h] (q and q_out both NULL: left out; they may
+ *           be the same buffer when q_stride is num_q_heads * head_dim).
+ * rot_dims is a multiple of 16 in [0, head_dim]; rope_cos_bf16 and rope_sin_bf16 both
+ * NULL: no rotation (rot_dims and t_cap are then unused, t_cap still positive).  q, k and
+ * v rows are q_stride, k_stride and v_stride elements apart (multiples of 8, at least a
+ * row's heads), each row's heads dense: slices of one projection's output will do.
+ * q_out [N][num_q_heads][head_dim].  Rows are independent; two rows of a call with the
+ * same sequence and position leave one of the two behind.  A row out of range, or at or past
+ * min(t_cap, table_len * page_tokens), writes nothing.  Pointers 16-byte aligned. */
+step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                             int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
+                             const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                             const int32_t* row_seq, const int32_t* row_pos, const void* rope_cos_bf16,
+                             const void* rope_sin_bf16, void* q_out_bf16_or_null, void* k_pages_bf16,
+                             void* v_pages_bf16, const int32_t* block_table_or_null, step5_stream_t stream);
+
+/* step5_kv_append into an e4m3 pool.  With x the bf16 values that step5_kv_append would
+ * write, and the call's tokens of region r in group g being t0 .. t1 (K and V apart):
+ *   s = max(the scale held, if t0 is not the region's first token;
+ *           the smallest power of two >= max |x| / 448;  2^-126)
+ *   scales[r] = s;  codes[t] = e4m3(x[t] / s) for t0 <= t <= t1 (round to nearest even)
+ * and, when s is larger than the scale held, the codes of the region's tokens before t0 are
+ * requantised: e4m3(code * held / s).  Tokens behind t1 are taken as absent (a position
+ * may be written again after tokens were rolled back; the scale then shrinks only when the
+ * region's first token is written).  Infinities saturate, NaN stays NaN; neither moves the scale
+ * past 2^120.  A scale held that is not finite and positive is ignored (STEP5_DEV_RANGE).
+ * The rows of one sequence must stand together in a call, at consecutive ascending
+ * positions (a chunk, or one decode row); a row that follows one of its own sequence at
+ * any other position sets STEP5_DEV_RANGE and nothing is written for it and its region. */
+step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                                  int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
+                                  const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,
+                                  const int32_t* row_seq, const int32_t* row_pos, const void* rope_cos_bf16,
+                                  const void* rope_sin_bf16, void* q_out_bf16_or_null, uint8_t* k_pages_e4m3,
+                                  uint8_t* v_pages_e4m3, float* k_scales_f32, float* v_scales_f32,
+                                  const int32_t* block_table_or_null, step5_stream_t stream);
+
+/* Causal attention over an e4m3 pool.  For every row n (b = row_seq[n], p = row_pos[n]) and
+ * query head h of KV group g = h / (num_q_heads / G):
+ *   keys  = tokens max(0, p - window + 1) .. p  (window 0: 0 .. p)
+ *   out[n][h] = sigmoid(gate[n][h]) * softmax(softmax_scale * q[n][h] . K^T) V
+ * with K and V the values code * scale, every score, weight and sum in fp32 (weights meet
+ * V with at least 11 significant bits), one rounding to bf16; the factor is 1 with gate NULL
+ * (gate [N][num_q_heads] bf16 logits).  q, out: [N][num_q_heads][head_dim] bf16.  Tokens
+ * outside a row's keys never reach its result, whatever their codes, scales and table entries hold (a
+ * region that a row sees in part has one scale).  A region of the keys whose table entry
+ * or scale is bad (a scale must be finite and positive) is left out and sets
+ * STEP5_DEV_RANGE; a row without keys, or out of range, gets zeros; a padding row's output
+ * is left as it was.  N <= 65535.  Any order of rows; rows of one sequence that stand
+ * together share its keys.
+ * workspace: step5_paged_workspace_bytes(geom) bytes, 16-byte aligned, zeroed once
+ * (step5_workspace_init); any number of calls with geometries of no more query heads per
+ * group may use it one after another, captured or not, but not two at once. */
+step5_status step5_paged_attn_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                                   int32_t window, const void* q_bf16, const uint8_t* k_pages_e4m3,
+                                   const uint8_t* v_pages_e4m3, const float* k_scales_f32, const float* v_scales_f32,
+                                   const int32_t* block_table_or_null, const int32_t* row_seq, const int32_t* row_pos,
+                                   const void* gate_bf16_or_null, void* out_bf16, void* workspace,
+                                   size_t workspace_bytes, step5_stream_t stream);
+
+/* Step (4) over an e4m3 pool: step5_paged_attn_e4m3 with the keys of step5_sparse_attn, the
+ * regions sel_ids[n][g][0 .. sel_count[n][g]) (distinct candidates of the row) and the
+ * own-region tokens up to p. */
+step5_status step5_sparse_attn_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                                    const void* q_bf16, const uint8_t* k_pages_e4m3, const uint8_t* v_pages_e4m3,
+                                    const float* k_scales_f32, const float* v_scales_f32,
+                                    const int32_t* block_table_or_null, const int32_t* row_seq, const int32_t* row_pos,
+                                    const int32_t* sel_ids, const int32_t* sel_count, const void* gate_bf16_or_null,
+                                    void* out_bf16, void* workspace, size_t workspace_bytes, step5_stream_t stream);
+
+/* Bytes of device workspace that the attention calls over an e4m3 pool need, whatever N,
+ * the pool and the lengths.  Returns 0 for an unsupported geometry. */
+size_t step5_paged_workspace_bytes(const step5_geometry* geom);
+
 /* Bytes of device workspace that step5_index_score_topk and step5_sparse_attn need for
  * N rows and r_cap summary slots (one buffer serves both: step (4)'s part comes first
  * and depends on the geometry and N only).  Returns 0 for an unsupported geometry. */

@@ -1,0 +1,563 @@
+"""The paged KV cache on the GPU against its definitions in 64 bits: appending with rotation
+(bf16 and e4m3), attention over the e4m3 pages, over picked regions, and a run of them together."""
+import numpy as np
+import pytest
+import torch
+
+import paged_reference as R
+import synthetic as S
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def s5():
+    import block_sparse_attention_step5_gb300 as s5
+    s5.build()
+    s5.load()
+    return s5
+
+
+def geometry(s5, G=4, hq=8, **over):
+    return s5.Geometry.step5(num_q_heads=G * hq, num_kv_groups=G, idx_heads=4 * G, **over)
+
+
+def normal(gen, *shape, scale=1.0):
+    return (torch.randn(*shape, generator=gen) * scale).bfloat16()
+
+
+def tables(gen, B, length, spare=3):
+    """A block table over a pool of B * length + spare pages in a random order."""
+    return torch.randperm(B * length + spare, generator=gen)[:B * length].int().view(B, length).contiguous()
+
+
+def rows_of(*runs):
+    """(row_seq, row_pos) of runs (sequence, first position, rows)."""
+    seq = [b for b, p, n in runs for _ in range(n)]
+    pos = [p + i for b, p, n in runs for i in range(n)]
+    return torch.tensor(seq, dtype=torch.int32), torch.tensor(pos, dtype=torch.int32)
+
+
+def random_pool(gen, P, G, pt, lo=-9, hi=-4):
+    codes = (torch.randn((P, G, pt, 128), generator=gen) * 100).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    return codes, torch.exp2(torch.randint(lo, hi, (P, G, pt // 8), generator=gen).float())
+
+
+def dev(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def status(s5):
+    torch.cuda.synchronize()
+    return s5.step5_device_status()
+
+
+# ------------------------------------------------------------------------------ append
+
+RUNS = {
+    "one": [(0, 5, 1)],
+    "first": [(0, 0, 1)],
+    "last_of_region": [(1, 15, 1)],
+    "decode": [(0, 5, 1), (2, 8, 1), (1, 31, 1)],
+    "chunk": [(0, 3, 27)],
+    "chunks": [(1, 0, 8), (0, 7, 2), (-1, 0, 3), (2, 12, 20)],
+    "long": [(0, 1, 200)],
+}
+
+
+@pytest.mark.parametrize("runs", list(RUNS))
+@pytest.mark.parametrize("G, hq, pt, rot", [(4, 8, 16, 128), (1, 4, 8, 32), (8, 16, 24, 96), (2, 8, 64, 0)])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append(s5, runs, G, hq, pt, rot, e4m3):
+    gen = torch.Generator().manual_seed(len(runs) * 100 + rot)
+    geom = geometry(s5, G, hq)
+    seq, pos = rows_of(*RUNS[runs])
+    N, B, length = len(seq), 3, -(-208 // pt)
+    table = tables(gen, B, length)
+    P = B * length + 3
+    # one projection's rows, magnitudes over many binades
+    qkv = (torch.randn((N, G * (hq + 2), 128), generator=gen) *
+           torch.exp2(torch.randint(-20, 12, (N, G * (hq + 2), 1), generator=gen).float())).bfloat16()
+    q, k, v = qkv.split((G * hq, G, G), dim=1)
+    cos, sin = S.rope_tables(length * pt, rot) if rot else (None, None)
+    dq, dseq, dpos, dtab, dcos, dsin = dev(qkv, seq, pos, table, cos, sin)
+    gq, gk, gv = dq.split((G * hq, G, G), dim=1)
+    q_out = torch.full((N, G * hq, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    at = pos.long().clamp(min=0)
+    want_q = R.rotate(q.double(), cos, sin, at)
+    want = {"k": R.rotate(k.double(), cos, sin, at), "v": v.double()}
+    real = (seq >= 0)
+    if e4m3:
+        pools = [random_pool(gen, P, G, pt, -12, 4) for _ in "kv"]
+        (kc, ks), (vc, vs) = [tuple(x.cuda() for x in pl) for pl in pools]
+        s5.step5_kv_append_e4m3(geom, gk, gv, s5.PagedCache(kc, vc, dtab, ks, vs), dseq, dpos, dcos, dsin, q=gq,
+                                q_out=q_out)
+    else:
+        pools = [(normal(gen, P, G, pt, 128), None) for _ in "kv"]
+        kc, vc = (pl[0].cuda() for pl in pools)
+        s5.step5_kv_append(geom, gk, gv, s5.PagedCache(kc, vc, dtab), dseq, dpos, dcos, dsin, q=gq, q_out=q_out)
+    assert status(s5) == 0
+    assert torch.equal(q_out.cpu().double()[real], want_q[real])
+    assert bool((q_out.cpu()[~real] == 7.0).all())
+    for name, got, got_s, (base, base_s) in (("k", kc, ks if e4m3 else None, pools[0]),
+                                             ("v", vc, vs if e4m3 else None, pools[1])):
+        if e4m3:
+            codes, scales = R.decode(base), base_s.double()
+            R.append_e4m3(want[name], codes, scales, table, seq, pos)
+            assert torch.equal(got_s.cpu().double(), scales), name
+            assert torch.equal(R.decode(got), codes), name
+        else:
+            pool = base.double()
+            for n in range(N):
+                if seq[n] >= 0:
+                    page, slot = R.place(table, int(seq[n]), int(pos[n]), pt)
+                    pool[page, :, slot] = want[name][n]
+            assert torch.equal(got.cpu().double(), pool), name
+
+
+def test_append_e4m3_token_by_token(s5):
+    """Appending tokens one at a time, the scale growing inside regions, equals the
+    definition step by step; and a rolled-back position written again keeps the scale held."""
+    gen = torch.Generator().manual_seed(3)
+    geom = geometry(s5, 2, 4)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
+    kc, vc = (torch.zeros((3, 2, 8, 128), dtype=torch.uint8) for _ in "kv")
+    ks, vs = (torch.full((3, 2, 1), float("nan")) for _ in "kv")
+    gpu = [t.cuda() for t in (kc, vc, table, ks, vs)]
+    cache = s5.PagedCache(*gpu)
+    ref = [[R.decode(kc), ks.double()], [R.decode(vc), vs.double()]]
+    for p in list(range(20)) + [13, 14, 16, 17]:
+        x = normal(gen, 2, 1, 2, 128, scale=2.0 ** (p % 5 * 3 - 6))
+        seq, pos = rows_of((0, p, 1))
+        for i in range(2):
+            R.append_e4m3(x[i].double(), *ref[i], table, seq, pos)
+        s5.step5_kv_append_e4m3(geom, *dev(x[0], x[1]), cache, *dev(seq, pos))
+        for i, (c, s) in enumerate(((gpu[0], gpu[3]), (gpu[1], gpu[4]))):
+            assert torch.equal(R.decode(c), ref[i][0]), p
+            assert torch.equal(s.cpu().double().nan_to_num(-1.0), ref[i][1].nan_to_num(-1.0)), p
+    assert status(s5) == 0
+
+
+def test_append_e4m3_special_values(s5):
+    """Zero regions, the largest and smallest bf16 values, infinities (saturate) and NaN (kept; scale
+    from the rest)."""
+    geom = geometry(s5, 1, 4)
+    x = torch.ones((40, 1, 128), dtype=torch.bfloat16)
+    x[0:8] = 0.0
+    x[8, 0, 3] = torch.finfo(torch.bfloat16).max
+    x[16:24] = 2.0 ** -133
+    x[24, 0, 5], x[25, 0, 6] = float("inf"), -float("inf")
+    x[32:40] = 3.0
+    x[33, 0, 7] = float("nan")
+    seq, pos = rows_of((0, 0, 40))
+    table = torch.zeros((1, 1), dtype=torch.int32)
+    kc, vc, ks, vs = (torch.zeros((1, 1, 40, 128), dtype=torch.uint8), torch.zeros((1, 1, 40, 128), dtype=torch.uint8),
+                      torch.zeros((1, 1, 5)), torch.zeros((1, 1, 5)))
+    codes, scales = R.decode(kc), ks.double()
+    R.append_e4m3(x.double(), codes, scales, table, seq, pos)
+    gk, gv, gt, gks, gvs = dev(kc, vc, table, ks, vs)
+    s5.step5_kv_append_e4m3(geom, *dev(x, x), s5.PagedCache(gk, gv, gt, gks, gvs), *dev(seq, pos))
+    assert status(s5) == 0
+    assert torch.equal(gks.cpu().double(), scales) and torch.equal(gvs, gks)
+    assert torch.equal(torch.isnan(R.decode(gk)), torch.isnan(codes))
+    assert torch.equal(R.decode(gk).nan_to_num(0.0), codes.nan_to_num(0.0))
+
+
+def test_append_refuses_rows_on_the_device(s5):
+    """Rows out of range, out of order or without a page write nothing and raise the range flag."""
+    geom = geometry(s5, 2, 4)
+    table = torch.tensor([[1, -1], [0, 99]], dtype=torch.int32)
+    x = torch.ones((1, 2, 128), dtype=torch.bfloat16).cuda()
+    for b, p in ((0, 16), (0, -1), (2, 0), (-2, 0), (0, 8), (1, 15)):
+        kc, vc = (torch.full((2, 2, 8, 128), 9, dtype=torch.uint8, device="cuda") for _ in "kv")
+        ks, vs = (torch.full((2, 2, 1), 3.0, device="cuda") for _ in "kv")
+        seq, pos = dev(*rows_of((b, p, 1)))
+        s5.step5_kv_append_e4m3(geom, x, x, s5.PagedCache(kc, vc, table.cuda(), ks, vs), seq, pos)
+        assert status(s5) == s5.DEV_RANGE, (b, p)
+        assert bool((kc == 9).all()) and bool((vc == 9).all()) and bool((ks == 3).all()) and bool((vs == 3).all())
+        kb, vb = (torch.full((2, 2, 8, 128), 9.0, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        s5.step5_kv_append(geom, x, x, s5.PagedCache(kb, vb, table.cuda()), seq, pos)
+        assert status(s5) == s5.DEV_RANGE, (b, p)
+        assert bool((kb == 9).all()) and bool((vb == 9).all())
+    # a rope table shorter than the pages
+    cos, sin = dev(*S.rope_tables(4, 32))
+    seq, pos = dev(*rows_of((0, 4, 1)))
+    s5.step5_kv_append(geom, x, x, s5.PagedCache(kb, vb, table.cuda()), seq, pos, cos, sin)
+    assert status(s5) == s5.DEV_RANGE and bool((kb == 9).all())
+    # a sequence's rows out of order
+    kc, vc = (torch.full((2, 2, 8, 128), 9, dtype=torch.uint8, device="cuda") for _ in "kv")
+    ks, vs = (torch.full((2, 2, 1), 3.0, device="cuda") for _ in "kv")
+    seq, pos = dev(*rows_of((0, 5, 1), (0, 2, 1)))
+    s5.step5_kv_append_e4m3(geom, x.expand(2, -1, -1).contiguous(), x.expand(2, -1, -1).contiguous(),
+                            s5.PagedCache(kc, vc, table.cuda(), ks, vs), seq, pos)
+    assert status(s5) == s5.DEV_RANGE
+    assert bool((kc[1, :, 5] != 9).any()) and bool((kc[1, :, 2] == 9).all())
+
+
+def test_append_bf16_fills_the_contiguous_caches(s5):
+    """Without a table the bf16 append fills the caches that step5_sparse_attn reads: tokens
+    appended one chunk at a time give the same output as caches filled by hand."""
+    w = S.workload({"positions": [5003, 129], "B": 2}, seed=31)
+    t = S.materialize(w, device="cuda")
+    geom = s5.STEP5_GEOMETRY
+    k, v = (torch.zeros_like(t[n]) for n in ("k_cache", "v_cache"))
+    cache = s5.PagedCache(k, v)
+    for b in range(2):
+        for at in range(0, int(w.row_pos[b]) + 1, 1000):
+            n = min(1000, int(w.row_pos[b]) + 1 - at)
+            rows = [t[x][b, :, at:at + n].transpose(0, 1).contiguous() for x in ("k_cache", "v_cache")]
+            s5.step5_kv_append(geom, *rows, cache, *dev(*rows_of((b, at, n))))
+    ws = s5.Workspace.create(geom, w.N, w.r_cap)
+    ids = torch.empty((2, 4, 512), dtype=torch.int32, device="cuda")
+    cnt = torch.empty((2, 4), dtype=torch.int32, device="cuda")
+    s5.step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], t["sum_begin"], t["sum_end"],
+                              t["summaries"], max_regions_per_seq=w.max_span)
+    s5.step5_index_score_topk(geom, t["idx_q"], t["w"], t["row_seq"], t["row_pos"], t["cos"], t["sin"], t["summaries"],
+                              ids, cnt, ws.tensor, t_cap=w.t_cap)
+    outs = []
+    for kk, vv in ((k, v), (t["k_cache"], t["v_cache"])):
+        out = torch.empty((2, 32, 128), dtype=torch.bfloat16, device="cuda")
+        s5.step5_sparse_attn(geom, t["q"], kk, vv, t["row_seq"], t["row_pos"], ids, cnt, out, ws.tensor)
+        outs.append(out)
+    assert status(s5) == 0
+    assert torch.equal(*outs)
+
+
+# ------------------------------------------------------------------------------ attention
+
+class Case:
+    """A pool, its table and rows at (row_seq, row_pos), and the 64-bit answer."""
+
+    def __init__(self, s5, runs, G=4, hq=8, pt=64, seed=1, q_scale=1.5, lo=-9, hi=-4, extra=0, **geom):
+        self.s5, self.gen = s5, torch.Generator().manual_seed(seed)
+        self.geom = geometry(s5, G, hq, **geom)
+        self.seq, self.pos = rows_of(*runs)
+        self.N, B = len(self.seq), int(self.seq.max()) + 1
+        length = -(-(int(self.pos.max()) + 1 + extra) // pt)
+        self.table = tables(self.gen, B, length)
+        P = B * length + 3
+        self.k, self.ks = random_pool(self.gen, P, G, pt, lo, hi)
+        self.v, self.vs = random_pool(self.gen, P, G, pt, lo, hi)
+        self.q = normal(self.gen, self.N, G * hq, 128, scale=q_scale)
+        self.ws = s5.PagedWorkspace.create(self.geom)
+        self.ids = self.cnt = self.gate = None
+
+    def pick(self, counts=None):
+        G, top_k = self.geom.num_kv_groups, self.geom.top_k
+        self.ids = torch.full((self.N, G, top_k), -1, dtype=torch.int32)
+        self.cnt = torch.zeros((self.N, G), dtype=torch.int32)
+        for n in range(self.N):
+            own = int(self.pos[n]) // 8
+            for g in range(G):
+                c = min(top_k, own)
+                self.ids[n, g, :c] = torch.randperm(max(own, 1), generator=self.gen)[:c].int()
+                self.cnt[n, g] = c
+        return self
+
+    def cache(self):
+        return self.s5.PagedCache(*dev(self.k, self.v, self.table, self.ks, self.vs))
+
+    def run(self, window=0, cache=None, out=None):
+        out = torch.full((self.N, self.geom.num_q_heads, 128), 5.0, dtype=torch.bfloat16, device="cuda") if out is None else out
+        q, seq, pos, ids, cnt, gate = dev(self.q, self.seq, self.pos, self.ids, self.cnt, self.gate)
+        cache = cache or self.cache()
+        if ids is None:
+            self.s5.step5_paged_attn_e4m3(self.geom, q, cache, seq, pos, out, self.ws, window=window, gate=gate)
+        else:
+            self.s5.step5_sparse_attn_e4m3(self.geom, q, cache, seq, pos, ids, cnt, out, self.ws, gate=gate)
+        return out
+
+    def want(self, window=0):
+        return R.attend(self.q.double(), R.decode(self.k), R.decode(self.v), self.ks, self.vs, self.table, self.seq,
+                        self.pos, self.geom.softmax_scale, window, self.ids, self.cnt, self.gate)
+
+    def check(self, window=0):
+        got = self.run(window).cpu()
+        assert status(self.s5) == 0
+        out, mass = self.want(window)
+        real = self.seq >= 0
+        assert bool((got[~real] == 5.0).all())
+        assert R.off(got[real], out[real], mass[real]) <= 1.0
+
+
+SHAPES = [(4, 8, 64), (1, 16, 8), (2, 4, 24), (8, 8, 16)]
+ROWS = {
+    "first": [(0, 0, 1)], "region_end": [(0, 7, 1)], "region_start": [(0, 8, 1)], "tile": [(0, 127, 1)],
+    "past_tile": [(0, 128, 1)], "odd": [(0, 1001, 1)], "ragged": [(3, 300, 1), (0, 1, 1), (-1, 0, 1), (2, 2047, 1), (1, 515, 1)],
+    "draft": [(0, 130, 4), (1, 6, 4)], "chunk": [(0, 0, 37)], "chunk_on": [(0, 201, 50)],
+    "chunks": [(1, 100, 19), (0, 0, 21), (-1, 0, 2), (2, 63, 9)],
+}
+
+
+@pytest.mark.parametrize("rows", list(ROWS))
+@pytest.mark.parametrize("G, hq, pt", SHAPES)
+def test_paged_attention(s5, rows, G, hq, pt):
+    Case(s5, ROWS[rows], G, hq, pt, seed=len(rows)).check()
+
+
+@pytest.mark.parametrize("window", [1, 2, 7, 8, 9, 100, 128, 512, 5000])
+@pytest.mark.parametrize("rows", ["first", "odd", "ragged", "chunk_on", "chunks"])
+def test_paged_attention_window(s5, rows, window):
+    Case(s5, ROWS[rows], 2, 8, 24, seed=window).check(window)
+
+
+def test_paged_attention_scattered_rows(s5):
+    """Rows of one sequence in any order, some twice, beside others."""
+    c = Case(s5, [(0, 900, 1)] * 2 + [(0, 3, 1), (1, 77, 2), (0, 901, 3), (1, 12, 1), (0, 10, 1)], seed=9)
+    c.check()
+    c.check(64)
+
+
+def test_paged_attention_long_row(s5):
+    """One row of 70,001 tokens: the split of its keys over the GPU and their merge."""
+    Case(s5, [(0, 70000, 1)], 1, 8, 64, seed=5).check()
+
+
+def test_paged_attention_gate(s5):
+    for runs in ([(0, 1001, 1), (1, 9, 1)], [(0, 90, 40)]):
+        c = Case(s5, runs, seed=6)
+        c.gate = normal(c.gen, c.N, c.geom.num_q_heads, scale=2.0)
+        c.check()
+
+
+def test_paged_attention_extreme_scales(s5):
+    """Scales over 60 binades, zero regions of V with the smallest scale, zero q."""
+    c = Case(s5, [(0, 1200, 1), (0, 300, 20)], 2, 8, 16, seed=7)
+    c.vs = torch.exp2(torch.randint(-30, 30, c.vs.shape, generator=c.gen).float())
+    c.q[0, :4] = 0.0
+    c.check()
+    c = Case(s5, [(0, 1200, 1)], 2, 8, 16, seed=8)
+    zero = torch.randint(0, 2, c.vs.shape, generator=c.gen).bool()
+    c.vs[zero] = 2.0 ** -126
+    c.v.view(*c.vs.shape, 8, 128)[zero] = 0
+    c.check()
+
+
+def test_paged_attention_peaked_scores(s5):
+    """A few keys that hold nearly all weight, found late and early: the running maximum moves far."""
+    for at in (3, 640, 1199):
+        c = Case(s5, [(0, 1200, 1), (0, 1195, 8)], 1, 8, 16, seed=at)
+        page, slot = R.place(c.table, 0, at, 16)
+        best = (c.q[0, 3].float() * 40).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        c.k[page, 0, slot] = best
+        c.check()
+
+
+def test_paged_attention_sink(s5):
+    """One key 2^14 times as heavy as each of the others, whose sum is still half of the mass."""
+    c = Case(s5, [(0, 16383, 1)], 1, 8, 64, seed=2, lo=-7, hi=-6)
+    c.q[:] = 0.0
+    c.q[..., 0] = 1.0
+    c.k[...] = 0
+    page, slot = R.place(c.table, 0, 100, 64)
+    c.k[page, 0, slot, 0] = torch.tensor([448.0]).to(torch.float8_e4m3fn).view(torch.uint8)[0]
+    c.ks[page, 0, slot // 8] = 14 * np.log(2) / c.geom.softmax_scale / 448.0
+    c.v[...] = torch.tensor([1.0]).to(torch.float8_e4m3fn).view(torch.uint8)[0]
+    c.v[page, 0, slot] = 0
+    c.check()
+
+
+@pytest.mark.parametrize("rows", [[(0, 1002, 1)], [(0, 1002, 1), (0, 4, 1)], [(0, 300, 37)]])
+@pytest.mark.parametrize("window", [0, 101])
+def test_tokens_outside_never_reach_the_result(s5, rows, window):
+    """NaN codes and bad scales and pages outside a row's keys change nothing."""
+    c = Case(s5, rows, 2, 8, 24, seed=4, extra=200)
+    base = c.run(window)
+    last = int(c.pos.max())
+    nan = 0x7f
+    lows = [max(0, int(p) - window + 1) if window else 0 for p in c.pos]
+    first = min(lows)
+    for tok in range(0, c.table.shape[1] * 24):
+        page, slot = R.place(c.table, 0, tok, 24)
+        if tok > last or tok < first:
+            c.k[page, :, slot] = nan
+            c.v[page, :, slot] = nan
+            r = tok // 8
+            if r > last // 8 or r < first // 8:
+                c.ks[page, :, slot // 8] = float("nan")
+                c.vs[page, :, slot // 8] = 0.0
+    used = set(c.table.flatten().tolist())
+    for page in range(c.k.shape[0]):
+        if page not in used:
+            c.k[page], c.v[page], c.ks[page], c.vs[page] = nan, nan, float("inf"), -1.0
+    for i in range(c.table.shape[1]):
+        if i * 24 > last or (i + 1) * 24 <= first:
+            c.table[0, i] = -7
+    got = c.run(window)
+    assert status(s5) == 0
+    assert torch.equal(base, got)
+
+
+def test_nan_of_a_later_row_stays_with_it(s5):
+    """A NaN in a token's value reaches the rows that see the token and no row before it."""
+    c = Case(s5, [(0, 300, 37)], 2, 8, 24, seed=14)
+    base = c.run().cpu()
+    page, slot = R.place(c.table, 0, 320, 24)
+    c.v[page, 1, slot, 17] = 0x7f
+    got = c.run().cpu()
+    assert status(s5) == 0
+    sees = torch.zeros(got.shape, dtype=torch.bool)
+    sees[20:, 8:, 17] = True
+    assert bool(torch.isnan(got[sees]).all())
+    assert torch.equal(got[~sees], base[~sees])
+    c = Case(s5, [(0, 300, 37)], 2, 8, 24, seed=14)
+    c.k[page, 1, slot, 17] = 0x7f
+    got = c.run().cpu()
+    sees[20:, 8:] = True
+    assert bool(torch.isnan(got[sees]).all())
+    assert torch.equal(got[~sees], base[~sees])
+
+
+def test_bad_pages_scales_and_rows(s5):
+    """A region of the keys without a page or with a bad scale is left out and flagged; a
+    row out of range gets zeros."""
+    for runs in ([(0, 500, 1)], [(0, 480, 20)]):
+        c = Case(s5, runs, 2, 8, 16, seed=11)
+        want_seen = torch.ones(501, dtype=torch.bool)
+        c.table[0, 3] = -1
+        c.table[0, 9] = c.k.shape[0]
+        page, slot = R.place(c.table, 0, 200, 16)
+        c.ks[page, :, slot // 8] = float("inf")
+        page2, slot2 = R.place(c.table, 0, 300, 16)
+        c.vs[page2, :, slot2 // 8] = 0.0
+        for lo, n in ((48, 16), (144, 16), (200, 8), (296, 8)):
+            want_seen[lo:lo + n] = False
+        got = c.run().cpu()
+        assert status(s5) == s5.DEV_RANGE
+        for n in range(c.N):
+            p = int(c.pos[n])
+            toks = torch.arange(p + 1)[want_seen[:p + 1]]
+            at = [R.place(c.table, 0, int(t), 16) for t in toks]
+            pg, sl = torch.tensor([a[0] for a in at]), torch.tensor([a[1] for a in at])
+            for g in range(2):
+                kk = R.decode(c.k)[pg, g, sl] * c.ks[pg, g, sl // 8].double()[:, None]
+                vv = R.decode(c.v)[pg, g, sl] * c.vs[pg, g, sl // 8].double()[:, None]
+                x = torch.softmax(c.q[n, 8 * g:8 * g + 8].double() @ kk.T * c.geom.softmax_scale, -1)
+                assert R.off(got[n, 8 * g:8 * g + 8], x @ vv, x @ vv.abs()) <= 1.0
+    c = Case(s5, [(0, 100, 1), (0, 101, 1), (0, 102, 1), (0, 103, 1)], 2, 8, 16, seed=12)
+    good = c.run()
+    c.pos[1], c.seq[2] = 16 * c.table.shape[1], 7
+    got = c.run()
+    assert status(s5) == s5.DEV_RANGE
+    assert bool((got[1:3] == 0).all())
+    for n in (0, 3):  # the other rows as ever, up to the order of fp32 sums
+        assert float((got[n] - good[n]).float().abs().max()) <= 2.0 ** -7 * float(good[n].float().abs().max())
+    # a row none of whose regions can be read
+    c = Case(s5, [(0, 5, 1)], 2, 8, 16, seed=13)
+    c.table[0, 0] = -1
+    assert bool((c.run() == 0).all()) and status(s5) == s5.DEV_RANGE
+
+
+@pytest.mark.parametrize("top_k", [1, 5, 64, 512])
+@pytest.mark.parametrize("G, hq, pt", SHAPES)
+def test_sparse_attention(s5, top_k, G, hq, pt):
+    runs = [(2, 2000, 1), (0, 7, 1), (-1, 0, 1), (1, 0, 1), (0, 1000, 3)]
+    Case(s5, runs, G, hq, pt, seed=top_k, top_k=top_k).pick().check()
+
+
+def test_sparse_attention_many_rows(s5):
+    """A chunk of 150 rows beyond 512 regions, all 4 groups."""
+    Case(s5, [(0, 4200, 150)], seed=21).pick().check()
+
+
+def test_sparse_attention_gate_and_bad_picks(s5):
+    c = Case(s5, [(0, 1000, 2)], 2, 8, 16, seed=22, top_k=64).pick()
+    c.gate = normal(c.gen, c.N, 16, scale=2.0)
+    c.check()
+    want = c.want()
+    # ids at, past and below the range stand for nothing
+    ids, cnt = c.ids.clone(), c.cnt.clone()
+    c.cnt -= 3
+    short = c.want()
+    c.ids[..., 61], c.ids[..., 62], c.ids[..., 63] = 125, -1, 1 << 30
+    c.cnt += 3
+    got = c.run()
+    assert status(s5) == s5.DEV_RANGE
+    assert R.off(got, *short) <= 1.0
+    c.ids, c.cnt = ids, cnt + 1000  # a count past top_k is clamped
+    got = c.run()
+    assert status(s5) == s5.DEV_RANGE
+    assert R.off(got, *want) <= 1.0
+
+
+def test_attention_is_deterministic_and_replays(s5):
+    """The same inputs give the same bits, on other streams, with other calls on the
+    workspace in between, and captured into graphs that share the workspace."""
+    cases = [Case(s5, [(0, 9000, 1), (1, 33, 1)], seed=31), Case(s5, [(0, 5000, 1)], seed=32).pick(),
+             Case(s5, [(0, 1100, 60)], seed=33)]
+    caches = [c.cache() for c in cases]
+    ws = cases[0].ws
+    for c in cases:
+        c.ws = ws
+    first = [c.run(cache=m) for c, m in zip(cases, caches)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = [c.run(cache=m) for c, m in zip(cases, caches)]
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    for a, b in zip(first, again):
+        assert torch.equal(a, b)
+    graphs = []
+    for c, m in zip(cases, caches):
+        tensors = [t for t in dev(c.q, c.seq, c.pos, c.ids, c.cnt)]
+        out = torch.zeros_like(first[0][:1]).expand(c.N, -1, -1).contiguous()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            if tensors[3] is None:
+                s5.step5_paged_attn_e4m3(c.geom, tensors[0], m, tensors[1], tensors[2], out, ws)
+            else:
+                s5.step5_sparse_attn_e4m3(c.geom, tensors[0], m, tensors[1], tensors[2], tensors[3], tensors[4], out, ws)
+        graphs.append((g, out, tensors))
+    for _ in range(3):
+        for g, _, _ in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for (g, out, _), a in zip(graphs, first):
+        assert torch.equal(out, a)
+    assert status(s5) == 0
+
+
+# ------------------------------------------------------------------------------ together
+
+def test_run_together(s5):
+    """Prompt chunks appended, then decode steps of the whole path over the pages: every
+    step's output is the attention over the picked regions of what the cache holds, and
+    near the bf16 path's on the same tokens."""
+    w = S.workload({"positions": [4700, 4170], "B": 2}, seed=41)
+    t = S.materialize(w, device="cuda")
+    geom = s5.STEP5_GEOMETRY
+    pt, length = 32, -(-4710 // 32)
+    gen = torch.Generator().manual_seed(1)
+    table = tables(gen, 2, length)
+    cache = s5.PagedCache.create(geom, 2 * length + 3, pt, table.cuda())
+    cos, sin = dev(*S.rope_tables(length * pt, 64))
+    for b in range(2):
+        for at in range(0, int(w.row_pos[b]), 1999):
+            n = min(1999, int(w.row_pos[b]) - at)
+            rows = [t[x][b, :, at:at + n].transpose(0, 1).contiguous() for x in ("k_cache", "v_cache")]
+            s5.step5_kv_append_e4m3(geom, *rows, cache, *dev(*rows_of((b, at, n))), cos, sin)
+    ws, pws = s5.Workspace.create(geom, 2, w.r_cap), s5.PagedWorkspace.create(geom)
+    ids = torch.empty((2, 4, 512), dtype=torch.int32, device="cuda")
+    cnt = torch.empty((2, 4), dtype=torch.int32, device="cuda")
+    out, q_rot = (torch.empty((2, 32, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    k, v = (torch.stack([t[x][b, :, int(w.row_pos[b])] for b in range(2)]) for x in ("k_cache", "v_cache"))
+    s5.decode_step_paged(geom, t, cache, ws, pws, k, v, ids, cnt, q_rot, out, w.max_span, cos, sin)
+    assert status(s5) == 0
+    at = torch.from_numpy(w.row_pos).long()
+    assert torch.equal(q_rot.cpu().double(), R.rotate(t["q"].cpu().double(), cos.cpu(), sin.cpu(), at))
+    want = R.attend(q_rot.cpu(), R.decode(cache.k), R.decode(cache.v), cache.k_scales.cpu(), cache.v_scales.cpu(),
+                    table, w.row_seq, w.row_pos, geom.softmax_scale, ids=ids.cpu(), counts=cnt.cpu())
+    assert R.off(out, *want) <= 1.0
+    # the same step over bf16 caches: e4m3 rounds each key and value by at most 2^-4 of itself
+    kb, vb = (torch.zeros_like(t[x]) for x in ("k_cache", "v_cache"))
+    flat = s5.PagedCache(kb, vb)
+    for b in range(2):
+        n = int(w.row_pos[b]) + 1
+        rows = [t[x][b, :, :n].transpose(0, 1).contiguous() for x in ("k_cache", "v_cache")]
+        s5.step5_kv_append(geom, *rows, flat, *dev(*rows_of((b, 0, n))), cos, sin)
+    ref = torch.empty_like(out)
+    s5.step5_sparse_attn(geom, q_rot, kb, vb, t["row_seq"], t["row_pos"], ids, cnt, ref, ws.tensor)
+    assert status(s5) == 0
+    rel = float((out.float() - ref.float()).norm() / ref.float().norm())
+    assert rel <= 2.0 ** -4
