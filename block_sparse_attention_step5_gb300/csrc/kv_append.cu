@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
     uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + (row - t0) * 128 + l16 * 8;
     float s = scale_for(amax);
     if (t0 > 0) {
-        if (!(held > 0.0f) || held > 3.0e38f) {
+        if (!scale_ok(held)) {
             if (l16 == 0) raise_status(p.status, kDevRange);
         } else if (held >= s) {
             s = held;

@@ -59,9 +59,22 @@ struct PagedAttnParams {
     const uint16_t* gate;      // [N][Hq] bf16 logits or null
     uint16_t* out;             // [N][Hq][128]
     uint32_t* status;
+    uint32_t* counters;        // workspace: [kPagedMaxCtas], zero between calls
+    float* states;             // workspace: partial states of items that CTAs share
     int N, B, G, Hq, top_k, window;
-    float scale_log2;        // softmax_scale * log2(e)
+    int box_regions;           // regions of one TMA box (a power of two <= 16 that divides a page's)
+    int min_tiles;             // fewest tiles worth a CTA
+    float scale_log2;          // softmax_scale * log2(e)
 };
-cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t stream, bool pdl);
+constexpr int kPagedMaxCtas = 320;           // of one launch
+constexpr size_t kPagedCounterBytes = 4096;
+constexpr size_t kPagedStateFloats = (size_t)kPagedMaxCtas * 64 * 130;  // two states a CTA: 32 heads each, or 64 with half as many CTAs
+constexpr size_t kPagedWorkspaceBytes = kPagedCounterBytes + kPagedStateFloats * 4;
+// kmap, vmap: the pools as [rows][128] bytes, boxes of 8 * box_regions rows, 128-byte swizzle
+cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                   int num_sms, cudaStream_t stream, bool pdl);
+
+// A scale that can be used: positive and at most 2^126 (so that the power of two above it is finite).
+__device__ __forceinline__ bool scale_ok(float s) { return s > 0.0f && s <= 8.507059173e37f; }
 
 }  // namespace step5

@@ -22,6 +22,19 @@ step5_status check_pages(const step5_geometry* g, const step5_pages* pages, int3
     return STEP5_OK;
 }
 
+// A pool of e4m3 codes as [rows][128] bytes, boxes of 8 * box_regions rows, 128-byte swizzle.
+bool encode_pool_map(CUtensorMap* map, const void* base, uint64_t rows, int box_regions) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {128, rows};
+    cuuint64_t strides[1] = {128};
+    cuuint32_t box[2] = {128, (cuuint32_t)(8 * box_regions)};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t rot_dims,
                          int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride, const void* k_bf16,
                          int64_t k_stride, const void* v_bf16, int64_t v_stride, const int32_t* row_seq,
@@ -101,6 +114,8 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     p.gate = static_cast<const uint16_t*>(gate);
     p.out = static_cast<uint16_t*>(out_bf16);
     p.status = st;
+    p.counters = static_cast<uint32_t*>(workspace);
+    p.states = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes);
     p.N = N;
     p.B = B;
     p.G = geom->num_kv_groups;
@@ -108,7 +123,17 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     p.top_k = geom->top_k;
     p.window = window;
     p.scale_log2 = geom->softmax_scale * 1.4426950408889634f;
-    return launch_paged_attention(p, (cudaStream_t)stream, true) == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
+    // every token: the largest boxes that pages are made of; picks: one region each
+    p.box_regions = 1;
+    if (sel_ids == nullptr)
+        while (p.box_regions < 16 && (pages->page_tokens / 8) % (2 * p.box_regions) == 0) p.box_regions *= 2;
+    p.min_tiles = 1;
+    CUtensorMap kmap, vmap;
+    const uint64_t rows = (uint64_t)pages->num_pages * geom->num_kv_groups * pages->page_tokens;
+    if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))
+        return STEP5_ERR_CUDA;
+    return launch_paged_attention(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true) == cudaSuccess ? STEP5_OK
+                                                                                                      : STEP5_ERR_CUDA;
 }
 
 }  // namespace
@@ -139,7 +164,7 @@ step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages*
 }
 
 size_t step5_paged_workspace_bytes(const step5_geometry* geom) {
-    return check_geometry(geom) == STEP5_OK ? 256 : 0;
+    return check_geometry(geom) == STEP5_OK ? kPagedWorkspaceBytes : 0;
 }
 
 step5_status step5_paged_attn_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,

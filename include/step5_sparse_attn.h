@@ -432,8 +432,9 @@ step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages*
  * query head h of KV group g = h / (num_q_heads / G):
  *   keys  = tokens max(0, p - window + 1) .. p  (window 0: 0 .. p)
  *   out[n][h] = sigmoid(gate[n][h]) * softmax(softmax_scale * q[n][h] . K^T) V
- * with K and V the values code * scale, every score, weight and sum in fp32 (weights meet
- * V with at least 11 significant bits), one rounding to bf16; the factor is 1 with gate NULL
+ * with K and V the values code * scale, every score, weight and sum in fp32 (a weight times
+ * its V scale meets V's codes with 12 significant bits, or within 2^-24 of the row's largest weight
+ * times the largest V scale), one rounding to bf16; the factor is 1 with gate NULL
  * (gate [N][num_q_heads] bf16 logits).  q, out: [N][num_q_heads][head_dim] bf16.  Tokens
  * outside a row's keys never reach its result, whatever their codes, scales and table entries hold (a
  * region that a row sees in part has one scale).  A region of the keys whose table entry

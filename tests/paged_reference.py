@@ -82,7 +82,7 @@ def decode(codes_u8: torch.Tensor) -> torch.Tensor:
 
 def attend(q, k, v, ks, vs, table, row_seq, row_pos, scale, window=0, ids=None, counts=None, gate=None):
     """64-bit attention: q [N][Hq][128], codes' values k, v [P][G][pt][128], scales.  Returns
-    (out, mass): mass = sum p |v| per output, what a relative error of the weights acts on."""
+    (out, terms): what the errors of the weights act on (terms())."""
     N, Hq, D = q.shape
     G, pt = k.shape[1], k.shape[2]
     hq = Hq // G
@@ -106,11 +106,16 @@ def attend(q, k, v, ks, vs, table, row_seq, row_pos, scale, window=0, ids=None, 
             vv = v[page, g, slot] * vs[page, g, slot // 8].double()[:, None]
             w = torch.softmax(q[n, g * hq:(g + 1) * hq].double() @ kk.T * scale, -1)
             out[n, g * hq:(g + 1) * hq] = w @ vv
-            mass[n, g * hq:(g + 1) * hq] = w @ vv.abs()
+            mass[n, g * hq:(g + 1) * hq] = terms(w, v[page, g, slot], vs[page, g, slot // 8].double())
     if gate is not None:
         f = torch.sigmoid(gate.double())[..., None]
         out, mass = out * f, mass * f
     return out, mass
+
+
+def terms(w, codes, scales):
+    """sum_t w_t |v_t| + 2^-13 max scale * sum_t |code_t| for weights w [heads][L], codes [L][128], scales [L]."""
+    return w @ (codes.abs() * scales[:, None]) + 2.0 ** -13 * float(scales.max()) * codes.abs().sum(0)
 
 
 def tolerance(out, mass):
@@ -118,7 +123,11 @@ def tolerance(out, mass):
     off by at most 2^-11 of itself: 2^-12 for its rounding to the 12 bits that meet V, and
     2^-12 for its score (128 products and the exponential in fp32: scores of the tests stay below 2^6,
     an fp32 sum of 128 terms is off by less than 2^-17 of the terms' magnitudes, which are below 2^5)
-    and the sums.  The last term lets a result near zero be off by the same share of its terms."""
+    and the sums.  Small weights have a floor: they are held, times vscale over a power of two above
+    every vscale and times 2^5, in three e4m3 parts 2^5 apart, the last in steps of 2^-9 at the finest,
+    so a weight (against the row's largest) times its vscale is off by up to half a step,
+    2^-10 * 2^-10 * 2^-5 = 2^-25 of that power of two, which is at most twice the largest vscale:
+    sum_t 2^-24 max scale |code_t| = 2^-11 of the second of terms()."""
     return 2.0 ** -8 * out.abs() + 2.0 ** -11 * mass + 1e-30
 
 

@@ -431,9 +431,9 @@ def test_bad_pages_scales_and_rows(s5):
             pg, sl = torch.tensor([a[0] for a in at]), torch.tensor([a[1] for a in at])
             for g in range(2):
                 kk = R.decode(c.k)[pg, g, sl] * c.ks[pg, g, sl // 8].double()[:, None]
-                vv = R.decode(c.v)[pg, g, sl] * c.vs[pg, g, sl // 8].double()[:, None]
+                codes, scales = R.decode(c.v)[pg, g, sl], c.vs[pg, g, sl // 8].double()
                 x = torch.softmax(c.q[n, 8 * g:8 * g + 8].double() @ kk.T * c.geom.softmax_scale, -1)
-                assert R.off(got[n, 8 * g:8 * g + 8], x @ vv, x @ vv.abs()) <= 1.0
+                assert R.off(got[n, 8 * g:8 * g + 8], x @ (codes * scales[:, None]), R.terms(x, codes, scales)) <= 1.0
     c = Case(s5, [(0, 100, 1), (0, 101, 1), (0, 102, 1), (0, 103, 1)], 2, 8, 16, seed=12)
     good = c.run()
     c.pos[1], c.seq[2] = 16 * c.table.shape[1], 7
