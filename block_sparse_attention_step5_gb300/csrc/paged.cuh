@@ -59,17 +59,17 @@ struct PagedAttnParams {
     const uint16_t* gate;      // [N][Hq] bf16 logits or null
     uint16_t* out;             // [N][Hq][128]
     uint32_t* status;
-    uint32_t* counters;        // workspace: [kPagedMaxCtas], zero between calls
+    int4* shared_items;        // workspace: [kPagedMaxCtas], the item that begins in a CTA and goes on in others
     float* states;             // workspace: partial states of items that CTAs share
     int N, B, G, Hq, top_k, window;
     int box_regions;           // regions of one TMA box (a power of two <= 16 that divides a page's)
     int min_tiles;             // fewest tiles worth a CTA
     float scale_log2;          // softmax_scale * log2(e)
 };
-constexpr int kPagedMaxCtas = 320;           // of one launch
-constexpr size_t kPagedCounterBytes = 4096;
-constexpr size_t kPagedStateFloats = (size_t)kPagedMaxCtas * 64 * 130;  // two states a CTA: 32 heads each, or 64 with half as many CTAs
-constexpr size_t kPagedWorkspaceBytes = kPagedCounterBytes + kPagedStateFloats * 4;
+constexpr int kPagedMaxCtas = 480;           // of one launch
+constexpr size_t kPagedItemBytes = 16 * 512;
+constexpr size_t kPagedStateFloats = (size_t)kPagedMaxCtas * 2 * 16 * 130;  // two states a CTA of up to 16 heads
+constexpr size_t kPagedWorkspaceBytes = kPagedItemBytes + kPagedStateFloats * 4;
 // kmap, vmap: the pools as [rows][128] bytes, boxes of 8 * box_regions rows, 128-byte swizzle
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                    int num_sms, cudaStream_t stream, bool pdl);

@@ -114,8 +114,8 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     p.gate = static_cast<const uint16_t*>(gate);
     p.out = static_cast<uint16_t*>(out_bf16);
     p.status = st;
-    p.counters = static_cast<uint32_t*>(workspace);
-    p.states = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedCounterBytes);
+    p.shared_items = static_cast<int4*>(workspace);
+    p.states = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kPagedItemBytes);
     p.N = N;
     p.B = B;
     p.G = geom->num_kv_groups;

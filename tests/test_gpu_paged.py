@@ -313,6 +313,19 @@ def test_paged_attention_long_row(s5):
     Case(s5, [(0, 70000, 1)], 1, 8, 64, seed=5).check()
 
 
+@pytest.mark.parametrize("tiles", [900, 1100, 1777, 2500, 3333])
+def test_paged_attention_runs_of_tiles(s5, tiles):
+    """Rows whose tiles are cut at other places of their look-ahead: every CTA's run starts
+    somewhere inside an item."""
+    rest = tiles - 2 * (tiles // 3)
+    Case(s5, [(b, 128 * n - 5, 1) for b, n in enumerate((tiles // 3, rest, tiles // 3))], 1, 4, 64, seed=tiles).check()
+
+
+@pytest.mark.parametrize("n", [23, 37, 101])
+def test_sparse_attention_runs_of_tiles(s5, n):
+    Case(s5, [(0, 4300, n), (1, 1511, n // 2)], 2, 8, 16, seed=n).pick().check()
+
+
 def test_paged_attention_gate(s5):
     for runs in ([(0, 1001, 1), (1, 9, 1)], [(0, 90, 40)]):
         c = Case(s5, runs, seed=6)
