@@ -45,14 +45,17 @@ constexpr float kSlack = 3.0f;       // log2 units a tile's maximum may pass the
 constexpr float kPTop = 32.0f;       // weights are split from p * 2^(8 - slack): at most 2^8, whose parts fit e4m3
 constexpr float kPart = 32.0f;       // a part against the one before it
 
-template <int H_, bool PICKS_>
+// MANY: for launches of many items, three CTAs an SM with few slots, which hide one another's latency (2,048 rows
+// of 512 picks: 1,171 us against 1,411 with two); for few items two CTAs with more copies in flight and fewer states to
+// join (16 rows of 512 picks: 31 us against 36).
+template <int H_, bool PICKS_, bool MANY_>
 struct Shape {
     static constexpr int H = H_;                       // query heads of a group
     static constexpr bool PICKS = PICKS_;
     static constexpr int NS = 2 * H < 16 ? 16 : 2 * H;
     static constexpr int NO = (3 * H + 15) / 16 * 16;
-    static constexpr int kCtas = H > 8 ? 2 : 3;        // per SM
-    static constexpr int kSlots = H > 8 ? 5 : 3;
+    static constexpr int kCtas = MANY_ && H <= 8 ? 3 : 2;  // per SM
+    static constexpr int kSlots = kCtas == 3 ? 3 : 5;
     static_assert(kSlots <= 6, "the barriers of copies and the ring are reused after 4 and 8 tiles");
     static constexpr uint32_t kCols = 2 * NS + NO <= 64 ? 64 : 128;
     static constexpr uint32_t kQBytes = NS * 128, kPBytes = 128 * NO;
@@ -136,6 +139,33 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, off by at most 2^-22 of
     return y;
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+        "mov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // The next e4m3 part of two f16 values: its codes, and what is left of the values times 2^5
 // (both steps exact).
 __device__ __forceinline__ uint32_t next_part(__half2& x) {
@@ -210,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     uint8_t* slots = smem;
     uint8_t* qt = smem + S::kSlots * kSlotBytes;
     uint8_t* pt = qt + S::kQBytes;
-    __shared__ __align__(8) uint64_t kfull[4], vfull[4], empty[S::kSlots], sbar[2], obar[2], pbar[2], qbar, tbar[kRing];
+    __shared__ __align__(8) uint64_t kfull[4], vfull[4], empty[S::kSlots], sbar[2], obar[2], pbar[2], qbar;
     __shared__ Meta ring[kRing][kTile];
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
@@ -234,12 +264,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         }
         for (int s = 0; s < S::kSlots; ++s) mbar_init(&empty[s], 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&sbar[s], 1);
+            mbar_init(&sbar[s], 2);
             mbar_init(&obar[s], 1);
-            mbar_init(&pbar[s], kSoft);
+            mbar_init(&pbar[s], kSoft / 32);
         }
-        mbar_init(&qbar, kSoft);
-        for (int s = 0; s < kRing; ++s) mbar_init(&tbar[s], kLoadWarps);
+        mbar_init(&qbar, kSoft / 32);
         fence_mbar_init();
         s_fail = 0;
     }
@@ -380,7 +409,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 }
                 if (lw == 0 && lane == 0) s_note[t & (kRing - 1)] = note;
                 __syncwarp();
-                if (lane == 0) arrive(&tbar[t & (kRing - 1)]);
             }
             uint64_t* full = isv ? &vfull[t & 3] : &kfull[t & 3];
             const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
@@ -460,9 +488,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             const int j = qk ? (t == 0 ? 0 : 2 * t - 1) : (t + 1 < run ? 2 * t + 2 : 2 * t + 1), slot = j % S::kSlots;
             if (!wait(qk ? &kfull[t & 3] : &vfull[t & 3], (uint32_t)((t >> 2) & 1))) ok = false;
             const int note = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_note[t & (kRing - 1)]), 0);
-            // S_t's buffer has been read (tile t - 2); q of a segment's first tile is there; P_t is
+            // First product: tile t - 2 is through (its S has been read, and its P, which the softmax of tile t
+            // overwrites); q of a segment's first tile is there.  Second: P_t is there.
             if (qk) {
-                if (t >= 2 && !wait(&pbar[t & 1], (uint32_t)(((t - 2) >> 1) & 1))) ok = false;
+                if (t >= 2 && !wait(&obar[t & 1], (uint32_t)(((t - 2) >> 1) & 1))) ok = false;
                 if ((note & 256) && !wait(&qbar, (uint32_t)(seg++ & 1))) ok = false;
             } else {
                 if (!wait(&pbar[t & 1], (uint32_t)((t >> 1) & 1))) ok = false;
@@ -476,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)  // 32 dims each
                         tc::mma_f8(tmem + (uint32_t)(S::NS * (t & 1)), da + 2 * i, dq + 2 * i, S::kIdesc1, i > 0);
+                    arrive(&sbar[t & 1]);  // (hands the tile's ring entry on, which came with its K)
                     tc::commit(&sbar[t & 1]);
                     tc::commit(&empty[slot]);
                 }
@@ -507,7 +537,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // ---------------- softmax warps: one key per thread (its TMEM lane)
         const int key = tid, q = key >> 3;
         const uint32_t lanes = tc::taddr(tmem, warp * 32, 0);
-        float m_ref[H], l_part[H], vref = 0.0f, vinv = 0.0f;
+        float2 neg_m[H / 2], l_part[H / 2];  // less the running maxima, the row sums of this thread's keys
+        float vref = 0.0f, vinv = 0.0f;
         Item it{}, done{};  // the segment's item; that of the segment before, for its epilogue
         int64_t done_begin = 0;
         bool whole = true;
@@ -554,7 +585,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 *to(H + u) = make_uint2(lo[0], lo[1]);
             }
             fence_proxy_async();
-            arrive(&qbar);
+            __syncwarp();
+            if (lane == 0) arrive(&qbar);
         };
 
         // O of the segment that ended with tile t - 1, and its output or partial state.
@@ -564,7 +596,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             tc::fence_after_sync();
             float(&rd)[4][H + 1] = red[2];
             int hidx = 0;
-            const float sum = fold<H, 16>(l_part, lane, &hidx, Add{});
+            float l[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) l[h] = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
+            const float sum = fold<H, 16>(l, lane, &hidx, Add{});
             if ((lane & (32 / H - 1)) == 0) rd[warp][hidx] = sum;
             if (!w_ok) give_up();
             if (group_or(1, kSoft, !w_ok || *reinterpret_cast<volatile int*>(&s_fail) != 0)) {
@@ -594,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     write_out<H>(p, done.n, done.g, h, key, v);
                 } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
                     if (key == 0) {
-                        st[h] = m_ref[h];
+                        st[h] = -(h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x);
                         st[H + h] = L;
                     }
                     st[2 * H + h * 128 + key] = v;
@@ -636,36 +671,34 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             off = 0;
             vref = vinv = 0.0f;
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                m_ref[h] = -INFINITY;
-                l_part[h] = 0.0f;
+            for (int h = 0; h < H / 2; ++h) {
+                neg_m[h] = both(INFINITY);
+                l_part[h] = both(0.0f);
             }
             for (int i = 0; i < seg; ++i, ++t) {
-                bool w_ok = wait(&tbar[t & (kRing - 1)], (uint32_t)((t / kRing) & 1));
+                // (tile t - 2's second product is done too: the first product of this one waited for it)
+                bool w_ok = wait(&sbar[t & 1], (uint32_t)((t >> 1) & 1));
+                tc::fence_after_sync();
                 const Meta me = ring[t & (kRing - 1)][q];
                 const bool sees = (me.mask >> (key & 7) & 1u) != 0;
-                w_ok &= wait(&sbar[t & 1], (uint32_t)((t >> 1) & 1));
-                tc::fence_after_sync();
                 // s[h] = q . kcode kscale; its logit in log2 units is s[h] cq[h], y[h] that less the running maximum
-                float s[H], y[H];
+                float2 s[H / 2], y[H / 2];
                 const uint32_t sb = lanes + (uint32_t)(S::NS * (t & 1));
-                if constexpr (H == 16) {
-                    float lo[16];
-                    tc::ld16(sb, s);
-                    tc::ld16(sb + H, lo);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) s[h] = fmaf(lo[h], 1.0f / kPart, s[h]) * me.ks;
-                } else {
-                    float x[16];
+                {
+                    float x[16], z[16];
                     tc::ld16(sb, x);
+                    if constexpr (H == 16) tc::ld16(sb + H, z);
 #pragma unroll
-                    for (int h = 0; h < H; ++h) s[h] = fmaf(x[H + h], 1.0f / kPart, x[h]) * me.ks;
+                    for (int h = 0; h < H; h += 2) {
+                        const float2 lo = H == 16 ? make_float2(z[h], z[h + 1]) : make_float2(x[(H + h) & 15], x[(H + h + 1) & 15]);
+                        s[h / 2] = mul2(fma2(lo, both(1.0f / kPart), make_float2(x[h], x[h + 1])), both(me.ks));
+                    }
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    y[h] = fmaf(s[h], cq[h], -m_ref[h]);
-                    top = fmaxf(top, y[h]);
+                for (int h = 0; h < H; h += 2) {
+                    y[h / 2] = fma2(s[h / 2], *reinterpret_cast<const float2*>(cq + h), neg_m[h / 2]);
+                    top = fmaxf(top, fmaxf(y[h / 2].x, y[h / 2].y));
                 }
                 // The running maxima move when a key passes one by more than the slack, vref when a
                 // vscale passes it; l and O are rescaled then.  Every softmax thread takes the same steps.
@@ -675,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     float alpha[H];
                     int hidx = 0;
 #pragma unroll
-                    for (int h = 0; h < H; ++h) alpha[h] = sees ? s[h] * cq[h] : -INFINITY;
+                    for (int h = 0; h < H; ++h) alpha[h] = sees ? (h & 1 ? s[h / 2].y : s[h / 2].x) * cq[h] : -INFINITY;
                     const float wmax = fold<H, 16>(alpha, lane, &hidx, Max{});
                     const uint32_t vmax = __reduce_max_sync(0xffffffffu, sees ? __float_as_uint(me.vs) : 0u);
                     float(&rd)[4][H + 1] = red[t & 1];
@@ -697,14 +730,18 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const float tmax = fmaxf(fmaxf(rd[0][h], rd[1][h]), fmaxf(rd[2][h], rd[3][h]));
+                        float& neg = h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x;
+                        float& l = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
                         alpha[h] = 1.0f;
-                        if (tmax > m_ref[h] + kSlack || (m_ref[h] == -INFINITY && tmax > -INFINITY)) {
-                            alpha[h] = ex2(m_ref[h] - tmax);
-                            m_ref[h] = tmax;
-                            l_part[h] *= alpha[h];
+                        if (tmax > kSlack - neg || (neg == INFINITY && tmax > -INFINITY)) {
+                            alpha[h] = ex2(-neg - tmax);
+                            neg = -tmax;
+                            l *= alpha[h];
                         }
-                        y[h] = fmaf(s[h], cq[h], -m_ref[h]);
                     }
+#pragma unroll
+                    for (int h = 0; h < H; h += 2)
+                        y[h / 2] = fma2(s[h / 2], *reinterpret_cast<const float2*>(cq + h), neg_m[h / 2]);
                     if (i > 0) {
                         w_ok = wait(&obar[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1));
                         tc::fence_after_sync();
@@ -718,23 +755,25 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                         }
                     }
                 }
-                const float vf = sees ? me.vs * vinv * kPTop : 0.0f;
+                if (__any_sync(0xffffffffu, !sees)) {  // (a key that is not seen may have anything for a score)
+#pragma unroll
+                    for (int h = 0; h < H / 2; ++h) y[h] = sees ? y[h] : both(-INFINITY);
+                }
+                const float2 vf = both(sees ? me.vs * vinv * kPTop : 0.0f);
                 uint32_t part[3][H / 4];
 #pragma unroll
                 for (int h = 0; h < H; h += 2) {
-                    const float p0 = sees ? ex2(y[h]) : 0.0f, p1 = sees ? ex2(y[h + 1]) : 0.0f;
-                    l_part[h] += p0;
-                    l_part[h + 1] += p1;
+                    const float2 w = make_float2(ex2(y[h / 2].x), ex2(y[h / 2].y));
+                    l_part[h / 2] = add2(l_part[h / 2], w);
                     // f16 keeps 11 bits of a weight (half a step is 2^-12 of it), the parts all of them
-                    __half2 x = __floats2half2_rn(p0 * vf, p1 * vf);
+                    __half2 x = __float22half2_rn(mul2(w, vf));
                     const uint32_t a = next_part(x), b = next_part(x), c = last_part(x);
                     if (h % 4 == 0)
                         part[0][h / 4] = a, part[1][h / 4] = b, part[2][h / 4] = c;
                     else
-                        part[0][h / 4] |= a << 16, part[1][h / 4] |= b << 16, part[2][h / 4] |= c << 16;
+                        part[0][h / 4] = __byte_perm(part[0][h / 4], a, 0x5410), part[1][h / 4] = __byte_perm(part[1][h / 4], b, 0x5410),
+                        part[2][h / 4] = __byte_perm(part[2][h / 4], c, 0x5410);
                 }
-                // the P buffer was last read by the second product two tiles back
-                if (t >= 2) w_ok &= wait(&obar[t & 1], (uint32_t)(((t >> 1) - 1) & 1));
                 uint8_t* pb = pt + (t & 1) * S::kPBytes + q * S::kPGroup + (key & 7) * 16;
                 if constexpr (H == 16) {
 #pragma unroll
@@ -758,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 fence_proxy_async();
                 tc::fence_before_sync();
                 if (!w_ok) give_up();  // (the warps leave together at the next barrier)
-                arrive(&pbar[t & 1]);
+                __syncwarp();
+                if (lane == 0) arrive(&pbar[t & 1]);
             }
             if (failed) break;
         }
@@ -852,8 +892,10 @@ cudaError_t launch_shape(const PagedAttnParams& p, const CUtensorMap& kmap, cons
 template <int H>
 cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
                          cudaStream_t stream, bool pdl) {
-    if (p.sel_ids != nullptr) return launch_shape<Shape<H, true>>(p, kmap, vmap, num_sms, stream, pdl);
-    return launch_shape<Shape<H, false>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (p.sel_ids == nullptr) return launch_shape<Shape<H, false, false>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (H <= 8 && (int64_t)p.N * p.G >= 2 * num_sms)
+        return launch_shape<Shape<H, true, H <= 8>>(p, kmap, vmap, num_sms, stream, pdl);
+    return launch_shape<Shape<H, true, false>>(p, kmap, vmap, num_sms, stream, pdl);
 }
 
 }  // namespace
