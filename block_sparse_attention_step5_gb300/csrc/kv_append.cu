@@ -2,13 +2,14 @@
 // for each region and KV group), with NEOX rotation of k (and of q) on the way.
 //
 // Rotation is the indexer's (x1 c - x2 s, x2 c + x1 s over pairs (i, i + rot / 2) from bf16
-// cos/sin, the exact sum rounded once to bf16).  A head vector is 256 bytes: sixteen lanes
-// take 16 bytes each, and since rot / 2 is a multiple of 8 a lane's eight partners lie in one
-// other lane of the sixteen, so rotation costs four shuffles and two 16-byte table loads.
+// cos/sin, the exact sum rounded once to bf16).  A head vector is sixteen 16-byte chunks and eight
+// lanes: since rot / 2 is a multiple of 8, a lane takes both chunks of its eight pairs (or two that are only
+// copied), so nothing is exchanged between lanes and every access is 16 bytes.  The kernel moves bytes: bound by HBM for
+// chunks (2,048 rows of 40 heads in bf16, 42 MB), by the latency of its three dependent loads for a decode row.
 //
-// In e4m3 a region's eight tokens share a scale, so the sixteen lanes of the first row that
-// falls into a region (its leader: a row on a region's first token, or one that does not
-// continue the row before) take all of the call's tokens of that region for one (group, k or v):
+// In e4m3 a region's eight tokens share a scale, so one warp (four tokens of eight lanes, twice) takes all of the
+// call's tokens of a region for one (group, k or v), from the first of them on (the leader: a row on a
+// region's first token, or one that does not continue the row before):
 //   s = max(the scale held, if the region holds earlier tokens; the smallest power of two
 //           >= max |x| / 448; 2^-126),      code = e4m3(x / s).
 // A power of two divides exactly, costs an e4m3 value no precision (it has an exponent of its
@@ -21,43 +22,45 @@ namespace step5 {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kUnitsPerBlock = kAppendThreads / 16;
+constexpr int kAppendWarps = kAppendThreads / 32;
 
-// Eight bf16 values (dims 8 lane .. 8 lane + 7 of a head vector held by 16 lanes), rotated.
-// Every lane of the warp takes part in the shuffles.
-__device__ __forceinline__ uint4 rotate8(uint4 x, const AppendParams& p, int pos, int l16, bool valid) {
-    const int half8 = p.rot >> 4;  // lanes that hold the first elements of the pairs
-    const bool first = l16 < half8, second = !first && l16 < 2 * half8;
-    const int partner = first ? l16 + half8 : (second ? l16 - half8 : l16);
-    uint4 y;
-    y.x = __shfl_sync(0xffffffffu, x.x, partner, 16);
-    y.y = __shfl_sync(0xffffffffu, x.y, partner, 16);
-    y.z = __shfl_sync(0xffffffffu, x.z, partner, 16);
-    y.w = __shfl_sync(0xffffffffu, x.w, partner, 16);
-    if (!(first || second) || !valid) return x;
-    const int64_t at = (int64_t)pos * (p.rot >> 1) + 8 * (first ? l16 : l16 - half8);
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(p.cos + at));
-    const uint4 s = __ldg(reinterpret_cast<const uint4*>(p.sin + at));
-    auto two = [&](uint32_t xv, uint32_t yv, uint32_t cv, uint32_t sv) {
-        const uint32_t lo = neox_rotate(bf16_lo(xv), bf16_lo(yv), bf16_lo(cv), bf16_lo(sv), first);
-        const uint32_t hi = neox_rotate(bf16_hi(xv), bf16_hi(yv), bf16_hi(cv), bf16_hi(sv), first);
-        return lo | (hi << 16);
-    };
-    return make_uint4(two(x.x, y.x, c.x, s.x), two(x.y, y.y, c.y, s.y), two(x.z, y.z, c.z, s.z),
-                      two(x.w, y.w, c.w, s.w));
+// Two chunks (8 bf16 each) of a head vector.
+struct Chunks {
+    uint4 a, b;
+};
+
+// First chunk of lane l8 of a vector whose first 2 * half8 chunks are rotated, and the distance to its second.
+__device__ __forceinline__ int first_chunk(int l8, int half8) { return l8 < half8 ? l8 : 2 * l8; }
+__device__ __forceinline__ int second_chunk(int l8, int half8) { return l8 < half8 ? l8 + half8 : 2 * l8 + 1; }
+
+// x c + y s, products exact in fp32, rounded to odd: of the two fp32 numbers around the exact sum the one with an odd
+// last bit.  Its rounding to bf16 (16 bits shorter) is the exact sum's.
+__device__ __forceinline__ float odd_sum(float x, float c, float y, float s) {
+    const float xc = __fmul_rn(x, c), down = __fmaf_rd(y, s, xc), up = __fmaf_ru(y, s, xc);
+    return (__float_as_uint(down) & 1u) ? down : up;
 }
 
-// The largest finite |bf16| of eight, as bits (NaN left out, infinity taken as the largest finite value).
-__device__ __forceinline__ uint32_t amax8(uint4 x) {
-    uint32_t m = 0;
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t a = w[i] & 0x7fffu, b = (w[i] >> 16) & 0x7fffu;
-        if (a <= 0x7f80u) m = max(m, a);
-        if (b <= 0x7f80u) m = max(m, b);
-    }
-    return min(m, 0x7f7fu);
+__device__ __forceinline__ uint32_t rotate2(uint32_t x, uint32_t y, uint32_t c, uint32_t s, bool first) {
+    const float n = first ? -1.0f : 1.0f;
+    return pack_bf16x2(odd_sum(bf16_lo(x), bf16_lo(c), bf16_lo(y), n * bf16_lo(s)),
+                       odd_sum(bf16_hi(x), bf16_hi(c), bf16_hi(y), n * bf16_hi(s)));
+}
+
+__device__ __forceinline__ void rotate(Chunks& x, const uint4& c, const uint4& s) {
+    const Chunks o = x;
+    x.a = make_uint4(rotate2(o.a.x, o.b.x, c.x, s.x, true), rotate2(o.a.y, o.b.y, c.y, s.y, true),
+                     rotate2(o.a.z, o.b.z, c.z, s.z, true), rotate2(o.a.w, o.b.w, c.w, s.w, true));
+    x.b = make_uint4(rotate2(o.b.x, o.a.x, c.x, s.x, false), rotate2(o.b.y, o.a.y, c.y, s.y, false),
+                     rotate2(o.b.z, o.a.z, c.z, s.z, false), rotate2(o.b.w, o.a.w, c.w, s.w, false));
+}
+
+// The largest finite |bf16| of two packed ones, as bits (NaN left out, infinity taken as the largest finite value).
+__device__ __forceinline__ uint32_t amax2(uint32_t w) {
+    const uint32_t a = w & 0x7fffu, b = (w >> 16) & 0x7fffu;
+    return min(max(a <= 0x7f80u ? a : 0u, b <= 0x7f80u ? b : 0u), 0x7f7fu);
+}
+__device__ __forceinline__ uint32_t amax8(const uint4& x) {
+    return max(max(amax2(x.x), amax2(x.y)), max(amax2(x.z), amax2(x.w)));
 }
 
 // The smallest power of two s >= 2^-126 with |x| <= 448 s = 1.75 * 2^8 s, x given as bf16 bits.
@@ -66,7 +69,7 @@ __device__ __forceinline__ float scale_for(uint32_t amax) {
     return __uint_as_float((uint32_t)max(e, 1) << 23);
 }
 
-__device__ __forceinline__ uint2 encode8(uint4 x, float inv) {
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
     auto two = [&](uint32_t w) {
         return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(w) * inv, bf16_hi(w) * inv), __NV_SATFINITE,
                                                   __NV_E4M3);
@@ -86,142 +89,174 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
     return r;
 }
 
+// Row vectors: q's heads, and in bf16 k's and v's too.  Four vectors of the row to a warp at a time, two times
+// in flight: q, k and v are asked for before the row's position is known.
 template <bool E4M3>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams p) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, l16 = lane & 15;
-    const int nq = p.q ? p.Hq : 0, per = nq + 2 * p.G;
-    const int64_t u = (int64_t)blockIdx.x * kUnitsPerBlock + (threadIdx.x >> 4);
-    const int64_t n64 = u / per;
-    const int n = (int)n64, j = (int)(u - n64 * per);
-    const bool have = n64 < p.N;
-    int b = -1, pos = 0;
-    if (have) {
-        b = p.row_seq[n];
-        pos = p.row_pos[n];
-    }
-    bool ok = have && b >= 0 && b < p.B && pos >= 0 && pos < p.pos_cap;
-    if (have && !ok && b != -1 && j == 0 && l16 == 0) raise_status(p.status, kDevRange);
-    const bool is_q = j < nq;
-    const int g = is_q ? 0 : (j - nq) % p.G;
-    const bool is_v = !is_q && j - nq >= p.G;
-
-    if (!E4M3) {
-        int64_t row = -1;
-        const uint16_t* src = nullptr;
-        uint16_t* dst = nullptr;
-        if (ok) {
-            if (is_q) {
-                src = p.q + n * p.q_stride + (int64_t)j * 128;
-                dst = p.q_out + ((int64_t)n * p.Hq + j) * 128;
-            } else {
-                row = page_row(p.pages, p.G, b, g, pos);
-                if (row < 0) {
-                    if (l16 == 0) raise_status(p.status, kDevRange);
-                } else {
-                    src = (is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride) + (int64_t)g * 128;
-                    dst = static_cast<uint16_t*>(is_v ? p.v_pages : p.k_pages) + row * 128;
-                }
-            }
+__device__ __forceinline__ void append_row(const AppendParams& p, uint32_t id, int lane) {
+    const int n = (int)(id >> p.row_shift), part = (int)(id & ((1u << p.row_shift) - 1)), l8 = lane & 7;
+    if (n >= p.N) return;
+    const int half8 = p.rot >> 4, c0 = first_chunk(l8, half8) * 8, c1 = second_chunk(l8, half8) * 8;
+    const bool turns = l8 < half8;
+    const int nq = p.q ? p.Hq : 0, vectors = nq + (E4M3 ? 0 : 2 * p.G), step = 4 << p.row_shift;
+    const int b = p.row_seq[n], pos = p.row_pos[n];
+    const bool ok = b >= 0 && b < p.B && pos >= 0 && pos < p.pos_cap;
+    if (!ok && b != -1 && part == 0 && lane == 0) raise_status(p.status, kDevRange);
+    uint4 cs = make_uint4(0, 0, 0, 0), sn = cs;
+    for (int v0 = part * 4 + (lane >> 3); v0 < vectors; v0 += 2 * step) {
+        Chunks x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = v0 + i * step, j = v - nq;
+            if (v >= vectors) continue;
+            const uint16_t* src = v < nq ? p.q + n * p.q_stride + (int64_t)v * 128
+                                         : (j < p.G ? p.k + n * p.k_stride + (int64_t)j * 128
+                                                    : p.v + n * p.v_stride + (int64_t)(j - p.G) * 128);
+            x[i].a = __ldg(reinterpret_cast<const uint4*>(src + c0));
+            x[i].b = __ldg(reinterpret_cast<const uint4*>(src + c1));
         }
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (src) x = *reinterpret_cast<const uint4*>(src + l16 * 8);
-        x = rotate8(x, p, pos, l16, src != nullptr && !is_v && p.rot > 0);
-        if (dst) *reinterpret_cast<uint4*>(dst + l16 * 8) = x;
+        if (!ok) return;
+        if (turns) {
+            cs = __ldg(reinterpret_cast<const uint4*>(p.cos + (int64_t)pos * (p.rot >> 1) + 8 * l8));
+            sn = __ldg(reinterpret_cast<const uint4*>(p.sin + (int64_t)pos * (p.rot >> 1) + 8 * l8));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int v = v0 + i * step, j = v - nq;
+            if (v >= vectors) continue;
+            uint16_t* dst = p.q_out + ((int64_t)n * p.Hq + v) * 128;
+            if (!E4M3 && v >= nq) {
+                const int64_t row = page_row(p.pages, p.G, b, j < p.G ? j : j - p.G, pos);
+                if (row < 0) {
+                    if (l8 == 0) raise_status(p.status, kDevRange);
+                    continue;
+                }
+                dst = static_cast<uint16_t*>(j < p.G ? p.k_pages : p.v_pages) + row * 128;
+            }
+            if (turns && (v < nq || j < p.G)) rotate(x[i], cs, sn);
+            *reinterpret_cast<uint4*>(dst + c0) = x[i].a;
+            *reinterpret_cast<uint4*>(dst + c1) = x[i].b;
+        }
+    }
+}
+
+// The m tokens of the call from row n on (position pos of sequence b) that lie in one region, for one
+// (group, k or v).
+__device__ __forceinline__ void append_region(const AppendParams& p, int n, int m, int b, int pos, int g, bool is_v,
+                                              int lane) {
+    const int l8 = lane & 7, tok = lane >> 3, t0 = pos & 7;
+    const int64_t row = page_row(p.pages, p.G, b, g, pos);
+    if (row < 0) {
+        if (lane == 0) raise_status(p.status, kDevRange);
         return;
     }
-
-    // rows n .. n + 7 of the same sequence, one to a lane: how many continue this row inside its region
-    const int t0 = pos & 7;
-    int cnt = 0;
-    bool leads = false;
-    {
-        bool next = false;
-        if (ok && !is_q && l16 > 0 && l16 < 8 - t0 && n + l16 < p.N)
-            next = p.row_seq[n + l16] == b && p.row_pos[n + l16] == pos + l16 && pos + l16 < p.pos_cap;
-        const uint32_t bits = (__ballot_sync(0xffffffffu, next) >> (lane & 16)) & 0xffffu;
-        cnt = __ffs(~(bits >> 1));  // 1 + the run of following rows
-    }
-    int64_t row = -1;
-    if (ok && !is_q) {
-        const bool same = n > 0 && p.row_seq[n - 1] == b;
-        const int before = same ? p.row_pos[n - 1] : -1;
-        if (same && before != pos - 1) {  // a sequence's rows out of order
-            if (l16 == 0) raise_status(p.status, kDevRange);
-        } else {
-            leads = !same || t0 == 0;
-        }
-        if (leads) {
-            row = page_row(p.pages, p.G, b, g, pos);
-            if (row < 0) {
-                if (l16 == 0) raise_status(p.status, kDevRange);
-                leads = false;
+    float* scale_at = (is_v ? p.v_scales : p.k_scales) + (row >> 3);
+    uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + (row - t0) * 128;
+    float held = 0.0f;  // read and written by the first lane alone
+    if (t0 > 0 && lane == 0) held = *scale_at;
+    const int half8 = p.rot >> 4, c0 = first_chunk(l8, half8) * 8, c1 = second_chunk(l8, half8) * 8;
+    const int64_t stride = is_v ? p.v_stride : p.k_stride;
+    const uint16_t* src = (is_v ? p.v : p.k) + n * stride + (int64_t)g * 128;
+    Chunks x[2];
+    uint4 cs[2], sn[2];
+    const bool turns = !is_v && l8 < half8;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = tok + 4 * i;
+        x[i].a = x[i].b = cs[i] = sn[i] = make_uint4(0, 0, 0, 0);
+        if (t < m) {
+            x[i].a = *reinterpret_cast<const uint4*>(src + t * stride + c0);
+            x[i].b = *reinterpret_cast<const uint4*>(src + t * stride + c1);
+            if (turns) {
+                const int64_t at = (int64_t)(pos + t) * (p.rot >> 1) + 8 * l8;
+                cs[i] = __ldg(reinterpret_cast<const uint4*>(p.cos + at));
+                sn[i] = __ldg(reinterpret_cast<const uint4*>(p.sin + at));
             }
         }
     }
-    if (!leads) cnt = 0;
-    if (ok && is_q) cnt = 1;
-    const uint16_t* src = nullptr;
-    int64_t stride = 0;
-    if (is_q) {
-        src = p.q + n * p.q_stride + (int64_t)j * 128;
-    } else {
-        stride = is_v ? p.v_stride : p.k_stride;
-        src = (is_v ? p.v : p.k) + n * stride + (int64_t)g * 128;
-    }
-    const int most = __reduce_max_sync(0xffffffffu, cnt);  // the warp's two units take the same steps
-    uint4 x[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-        x[t] = t < cnt ? *reinterpret_cast<const uint4*>(src + t * stride + l16 * 8) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-        if (t < most) x[t] = rotate8(x[t], p, pos + t, l16, t < cnt && !is_v && p.rot > 0);
-    // the scale held, read and written by the unit's first lane alone
-    float* scale_at = leads ? (is_v ? p.v_scales : p.k_scales) + (row >> 3) : nullptr;
-    float held = 1.0f;
-    if (leads && t0 > 0 && l16 == 0) held = *scale_at;
-    held = __shfl_sync(0xffffffffu, held, 0, 16);
     uint32_t amax = 0;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) amax = max(amax, amax8(x[t]));
-#pragma unroll
-    for (int d = 8; d; d >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (cnt == 0) return;
-    if (is_q) {
-        *reinterpret_cast<uint4*>(p.q_out + ((int64_t)n * p.Hq + j) * 128 + l16 * 8) = x[0];
-        return;
+    for (int i = 0; i < 2; ++i) {
+        if (turns) rotate(x[i], cs[i], sn[i]);
+        amax = max(amax, max(amax8(x[i].a), amax8(x[i].b)));
     }
-    uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + (row - t0) * 128 + l16 * 8;
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    held = __shfl_sync(0xffffffffu, held, 0);
     float s = scale_for(amax);
     if (t0 > 0) {
         if (!scale_ok(held)) {
-            if (l16 == 0) raise_status(p.status, kDevRange);
+            if (lane == 0) raise_status(p.status, kDevRange);
         } else if (held >= s) {
             s = held;
         } else {
             const float f = held / s;
-            for (int t = 0; t < t0; ++t) {
-                uint2* at = reinterpret_cast<uint2*>(codes + t * 128);
-                const uint2 c = *at;
-                *at = make_uint2(rescale4(c.x, f), rescale4(c.y, f));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (tok + 4 * i >= t0) continue;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint2* at = reinterpret_cast<uint2*>(codes + (tok + 4 * i) * 128 + (c ? c1 : c0));
+                    const uint2 w = *at;
+                    *at = make_uint2(rescale4(w.x, f), rescale4(w.y, f));
+                }
             }
         }
     }
     const float inv = 1.0f / s;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
-        if (t < cnt) *reinterpret_cast<uint2*>(codes + (t0 + t) * 128) = encode8(x[t], inv);
-    if (l16 == 0) *scale_at = s;
+    for (int i = 0; i < 2; ++i) {
+        const int t = tok + 4 * i;
+        if (t >= m) continue;
+        *reinterpret_cast<uint2*>(codes + (t0 + t) * 128 + c0) = encode8(x[i].a, inv);
+        *reinterpret_cast<uint2*>(codes + (t0 + t) * 128 + c1) = encode8(x[i].b, inv);
+    }
+    if (lane == 0) *scale_at = s;
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const uint32_t id = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    if (!E4M3 || id >= p.region_warps) {
+        append_row<E4M3>(p, E4M3 ? id - p.region_warps : id, lane);
+        return;
+    }
+    // lane i: row n0 - 1 + i; lanes 1 .. rows_per_warp may lead a region
+    const uint32_t u = id % (2 * p.G);
+    const int n0 = (int)(id / (2 * p.G)) * p.rows_per_warp, rn = n0 - 1 + lane;
+    int rb = -1, rp = -1;
+    if (lane < 16 + 1 && rn >= 0 && rn < p.N) {
+        rb = p.row_seq[rn];
+        rp = p.row_pos[rn];
+    }
+    const int pb = __shfl_up_sync(0xffffffffu, rb, 1), pp = __shfl_up_sync(0xffffffffu, rp, 1);
+    const bool mine = lane >= 1 && lane <= p.rows_per_warp;
+    const bool in = rb >= 0 && rb < p.B && rp >= 0 && rp < p.pos_cap;
+    const bool follows = pb == rb && pp == rp - 1, strays = pb == rb && !follows;  // strays: a sequence's rows out of order
+    if (u == 0 && mine && ((!in && rb != -1) || (in && strays))) raise_status(p.status, kDevRange);
+    uint32_t leads = __ballot_sync(0xffffffffu, mine && in && !strays && (!follows || (rp & 7) == 0));
+    const uint32_t goes_on = __ballot_sync(0xffffffffu, in && follows && (rp & 7) != 0);
+    for (; leads; leads &= leads - 1) {
+        const int l = __ffs(leads) - 1;
+        const int m = __ffs(~(goes_on >> 1 >> l));  // 1 + the rows that follow in the region
+        append_region(p, n0 - 1 + l, m, __shfl_sync(0xffffffffu, rb, l), __shfl_sync(0xffffffffu, rp, l), (int)(u >> 1),
+                      u & 1, lane);
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendParams& p, bool e4m3, cudaStream_t stream, bool pdl) {
-    const int64_t units = (int64_t)p.N * ((p.q ? p.Hq : 0) + 2 * p.G);
+cudaError_t launch_append(const AppendParams& params, bool e4m3, cudaStream_t stream, bool pdl) {
+    AppendParams p = params;
+    // Warps to a row's vectors: 4 when the rows fill the GPU (each then takes two or three vectors a lane), 16 for few
+    // rows, whose latency counts.  Rows a region warp looks over for leaders: 8 in long chunks, one of which leads.
+    p.row_shift = p.N >= 512 ? 2 : 4;
+    p.rows_per_warp = p.N >= 512 ? 8 : 1;
+    p.region_warps = e4m3 ? (uint32_t)((p.N + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.G) : 0u;
+    const uint32_t warps = p.region_warps + (e4m3 && p.q == nullptr ? 0u : (uint32_t)p.N << p.row_shift);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((units + kUnitsPerBlock - 1) / kUnitsPerBlock));
+    cfg.gridDim = dim3((warps + kAppendWarps - 1) / kAppendWarps);
     cfg.blockDim = dim3(kAppendThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

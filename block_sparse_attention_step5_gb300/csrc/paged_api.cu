@@ -48,6 +48,7 @@ step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, i
     if ((q_bf16_or_null == nullptr) != (q_out_bf16_or_null == nullptr)) return STEP5_ERR_INVALID_ARGUMENT;
     if ((rope_cos_bf16 == nullptr) != (rope_sin_bf16 == nullptr)) return STEP5_ERR_INVALID_ARGUMENT;
     if (rot_dims < 0 || rot_dims > geom->head_dim || rot_dims % 16) return STEP5_ERR_UNSUPPORTED;
+    if (N > 1 << 24) return STEP5_ERR_UNSUPPORTED;
     const int64_t G = geom->num_kv_groups, Hq = geom->num_q_heads, D = geom->head_dim;
     if (k_stride < G * D || v_stride < G * D || k_stride % 8 || v_stride % 8) return STEP5_ERR_INVALID_ARGUMENT;
     if (q_bf16_or_null && (q_stride < Hq * D || q_stride % 8)) return STEP5_ERR_INVALID_ARGUMENT;

@@ -399,7 +399,8 @@ typedef struct {
  * row's heads), each row's heads dense: slices of one projection's output will do.
  * q_out [N][num_q_heads][head_dim].  Rows are independent; two rows of a call with the
  * same sequence and position leave one of the two behind.  A row out of range, or at or past
- * min(t_cap, table_len * page_tokens), writes nothing.  Pointers 16-byte aligned. */
+ * min(t_cap, table_len * page_tokens), writes nothing.  Pointers 16-byte aligned.
+ * N <= 2^24. */
 step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                              int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
                              const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,
@@ -419,7 +420,8 @@ step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* page
  * past 2^120.  A scale held that is not finite and positive is ignored (STEP5_DEV_RANGE).
  * The rows of one sequence must stand together in a call, at consecutive ascending
  * positions (a chunk, or one decode row); a row that follows one of its own sequence at
- * any other position sets STEP5_DEV_RANGE and nothing is written for it and its region. */
+ * any other position sets STEP5_DEV_RANGE, and neither its k and v are written nor those of
+ * the rows behind it up to the next region. */
 step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                                   int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
                                   const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,

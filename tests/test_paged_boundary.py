@@ -37,7 +37,7 @@ def append(s5, e4m3=True, geom=None, pages=(8, 64, 4), N=1, B=1, rot=128, t_cap=
     (dict(pages=(8, 64, 1 << 26)), 1),          # 2^32 tokens a sequence
     (dict(table=None), 1),                      # no table: a sequence is one page
     (dict(table=None, pages=(8, 64, 1), B=9), 1),
-    (dict(N=0), 1), (dict(N=-1), 1), (dict(B=0), 1), (dict(t_cap=0), 1),
+    (dict(N=0), 1), (dict(N=-1), 1), (dict(N=(1 << 24) + 1), 2), (dict(B=0), 1), (dict(t_cap=0), 1),
     (dict(rot=24), 2), (dict(rot=144), 2), (dict(rot=-16), 2),
     (dict(k=None), 1), (dict(v=None), 1), (dict(seq=None), 1), (dict(pos=None), 1), (dict(kp=None), 1),
     (dict(vp=None), 1), (dict(q=None), 1), (dict(q_out=None), 1), (dict(cos=None), 1), (dict(sin=None), 1),
