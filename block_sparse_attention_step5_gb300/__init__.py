@@ -527,6 +527,16 @@ class PagedCache:
         self.k, self.v, self.block_table, self.k_scales, self.v_scales = k, v, block_table, k_scales, v_scales
         self.B = pages if block_table is None else block_table.shape[0]
         self.pages = Pages(pages, tokens, 1 if block_table is None else block_table.shape[1])
+        self.groups, self.head_dim, self.device = groups, k.shape[3], k.device
+        for t in (v, block_table, k_scales, v_scales):
+            if t is not None and t.device != k.device:
+                raise ValueError(f"the cache's tensors are on {k.device} and {t.device}")
+        if not all(t is None or t.is_contiguous() for t in (k, v, block_table, k_scales, v_scales)):
+            raise ValueError("the cache's tensors must be contiguous")
+        # the C calls' arguments, which stay the same as long as the tensors do
+        self._pages = ctypes.byref(self.pages)
+        self._pools = tuple(None if t is None else t.data_ptr()
+                            for t in ((k, v, k_scales, v_scales) if self.e4m3 else (k, v)) + (block_table,))
 
     @classmethod
     def create(cls, geom, num_pages: int, page_tokens: int, block_table: torch.Tensor, e4m3: bool = True,
@@ -540,13 +550,6 @@ class PagedCache:
         ks, vs = (torch.ones((num_pages, g.num_kv_groups, page_tokens // 8), dtype=torch.float32, device=device)
                   for _ in range(2))
         return cls(k, v, block_table, ks, vs)
-
-    def _args(self, geom):
-        """(pages, k, v, k_scales, v_scales, table) as the C calls take them."""
-        if self.k.shape[1] != geom.num_kv_groups or self.k.shape[3] != geom.head_dim:
-            raise ValueError("the cache's groups and head dim are not the geometry's")
-        return (ctypes.byref(self.pages), _ptr(self.k), _ptr(self.v), _ptr(self.k_scales), _ptr(self.v_scales),
-                _ptr(self.block_table))
 
 
 def step5_paged_workspace_bytes(geom) -> int:
@@ -569,52 +572,70 @@ class PagedWorkspace:
         return cls(t)
 
 
-def _rows_ptr(t: torch.Tensor, what: str, N: int, heads: int, dim: int):
-    """Pointer and row stride of a bf16 [N][heads][dim] tensor whose rows may lie apart."""
-    if tuple(t.shape) != (N, heads, dim) or t.dtype != torch.bfloat16:
-        raise ValueError(f"{what} must be bf16 [{N}][{heads}][{dim}], got {t.dtype} {tuple(t.shape)}")
+def _raise_for(what: str, t, dtype, shape, dev: int):
+    """Says what is wrong with a tensor argument that _arg or _rows has turned down."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{what} must be a tensor, got {type(t).__name__}")
     if not t.is_cuda:
-        raise ValueError("tensors passed to libstep5sa must be on the GPU")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"the heads of a row of {what} must lie together")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if N > 1 else heads * dim
+        raise ValueError(f"{what}: tensors passed to libstep5sa must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{what}: tensors passed to libstep5sa must be contiguous (of q, k and v the heads of each row)")
 
 
-def _same_device(dev: torch.device, **tensors):
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+def _arg(what: str, t, dtype, shape, dev: int) -> int:
+    """Address of a dense tensor of this type and shape on the current device."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or \
+            not t.is_contiguous():
+        _raise_for(what, t, dtype, shape, dev)
+    return t.data_ptr()
 
 
-def _int32_rows(N: int, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32 or t.shape[0] != N:
-            raise ValueError(f"{name} must be int32 with {N} rows, got {t.dtype} {tuple(t.shape)}")
+def _rows(what: str, t, heads: int, dim: int, dev: int, N: int):
+    """Address and row stride of a bf16 [N][heads][dim] tensor whose rows may lie apart."""
+    shape = (N, heads, dim)
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != shape:
+        _raise_for(what, t, torch.bfloat16, shape, dev)
+    s = t.stride()
+    if s[2] != 1 or (heads > 1 and s[1] != dim):
+        _raise_for(what, t, torch.bfloat16, shape, dev)
+    return t.data_ptr(), (s[0] if N > 1 else heads * dim)
 
 
-def _kv_append(fn: str, geom, k, v, cache: PagedCache, row_seq, row_pos, cos, sin, q, q_out, stream):
+def _device_and_stream(cache: "PagedCache", geom, stream):
+    """Current device and the stream's handle, after checking that the cache is there and fits the geometry."""
+    dev = torch.cuda.current_device()
+    if cache.device.type != "cuda" or cache.device.index != dev:
+        raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{dev}")
+    if cache.groups != geom.num_kv_groups or cache.head_dim != geom.head_dim:
+        raise ValueError("the cache's groups and head dim are not the geometry's")
+    return dev, (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+
+
+def _kv_append(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, row_pos, cos, sin, q, q_out, stream):
     g = Geometry.of(geom)
-    N = k.shape[0]
-    if cache.e4m3 != (fn == "step5_kv_append_e4m3"):
+    dev, st = _device_and_stream(cache, g, stream)
+    if cache.e4m3 != e4m3:
         raise ValueError(f"{fn} does not write this kind of pool")
-    _same_device(k.device, v=v, cache=cache.k, row_seq=row_seq, row_pos=row_pos, cos=cos, sin=sin, q=q, q_out=q_out)
-    _int32_rows(N, row_seq=row_seq, row_pos=row_pos)
-    kp, ks = _rows_ptr(k, "k", N, g.num_kv_groups, g.head_dim)
-    vp, vs = _rows_ptr(v, "v", N, g.num_kv_groups, g.head_dim)
-    qp, qs = (None, 0) if q is None else _rows_ptr(q, "q", N, g.num_q_heads, g.head_dim)
-    if q_out is not None and (q_out.dtype != torch.bfloat16 or q_out.numel() != N * g.num_q_heads * g.head_dim):
-        raise ValueError("q_out must be bf16 [N][num_q_heads][128]")
-    if cos is not None and (sin is None or cos.shape != sin.shape or cos.dtype != torch.bfloat16 or
-                            sin.dtype != torch.bfloat16):
-        raise ValueError("cos and sin must be bf16 tables of one shape")
-    t_cap, half = (1, 0) if cos is None else cos.shape
-    pages, kc, vc, ksc, vsc, table = cache._args(g)
-    scales = (ksc, vsc) if cache.e4m3 else ()
-    _check(fn, getattr(load(), fn)(ctypes.byref(g), pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
-                                   _ptr(row_seq), _ptr(row_pos), _ptr(cos), _ptr(sin), _ptr(q_out), kc, vc, *scales,
-                                   table, _stream(stream)))
+    N, G, Hq, D = k.shape[0], g.num_kv_groups, g.num_q_heads, g.head_dim
+    kp, ks = _rows("k", k, G, D, dev, N)
+    vp, vs = _rows("v", v, G, D, dev, N)
+    qp, qs, qo = None, 0, None
+    if q is not None or q_out is not None:
+        qp, qs = _rows("q", q, Hq, D, dev, N)
+        qo = _arg("q_out", q_out, torch.bfloat16, (N, Hq, D), dev)
+    cp, sp, t_cap, half = None, None, 1, 0
+    if cos is not None or sin is not None:
+        cp = _arg("cos", cos, torch.bfloat16, cos.shape if isinstance(cos, torch.Tensor) and cos.dim() == 2 else (), dev)
+        sp = _arg("sin", sin, torch.bfloat16, cos.shape, dev)
+        t_cap, half = cos.shape
+    st = getattr(load(), fn)(g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
+                             _arg("row_seq", row_seq, torch.int32, (N,), dev),
+                             _arg("row_pos", row_pos, torch.int32, (N,), dev), cp, sp, qo, *cache._pools, st)
+    if st:
+        raise Step5Error(fn, st)
 
 
 def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
@@ -623,33 +644,41 @@ def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, s
     writes it and v into the bf16 cache at (row_seq, row_pos) [N] int32; with q
     [N][Hq][128], its rotation into q_out.  q, k and v may be slices of one [N][heads][128]
     tensor (rows apart, heads together)."""
-    _kv_append("step5_kv_append", geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+    _kv_append("step5_kv_append", False, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
 
 
 def step5_kv_append_e4m3(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
                          stream=None):
     """step5_kv_append into an e4m3 cache: codes and the power-of-two scale of each region
     and group.  A sequence's rows stand together at ascending positions (see the header)."""
-    _kv_append("step5_kv_append_e4m3", geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+    _kv_append("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
 
 
-def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, before=(), after=()):
+def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None, sel_ids=None,
+                 sel_count=None):
     g = Geometry.of(geom)
-    N = q.shape[0]
+    dev, st = _device_and_stream(cache, g, stream)
     if not cache.e4m3:
         raise ValueError(f"{fn} reads e4m3 pools")
-    ws_t = ws.tensor if isinstance(ws, PagedWorkspace) else ws
-    _same_device(q.device, cache=cache.k, row_seq=row_seq, row_pos=row_pos, out=out, workspace=ws_t, gate=gate)
-    _int32_rows(N, row_seq=row_seq, row_pos=row_pos)
-    for name, t in (("q", q), ("out", out)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (N, g.num_q_heads, g.head_dim):
-            raise ValueError(f"{name} must be bf16 [N][{g.num_q_heads}][{g.head_dim}]")
-    if gate is not None and (gate.dtype != torch.bfloat16 or tuple(gate.shape) != (N, g.num_q_heads)):
-        raise ValueError("gate must be bf16 [N][num_q_heads]")
-    pages, kc, vc, ksc, vsc, table = cache._args(g)
-    _check(fn, getattr(load(), fn)(ctypes.byref(g), pages, N, cache.B, *before, _ptr(q), kc, vc, ksc, vsc, table,
-                                   _ptr(row_seq), _ptr(row_pos), *after, _ptr(gate), _ptr(out), _ptr(ws_t),
-                                   0 if ws_t is None else ws_t.numel() * ws_t.element_size(), _stream(stream)))
+    N, Hq = q.shape[0], g.num_q_heads
+    shape = (N, Hq, g.head_dim)
+    w = ws.tensor if isinstance(ws, PagedWorkspace) else ws
+    if w is not None and (w.get_device() != dev or not w.is_contiguous()):
+        _raise_for("workspace", w, w.dtype, w.shape, dev)
+    if window is None:
+        before = ()
+        after = (_arg("sel_ids", sel_ids, torch.int32, (N, g.num_kv_groups, g.top_k), dev),
+                 _arg("sel_count", sel_count, torch.int32, (N, g.num_kv_groups), dev))
+    else:
+        before, after = (window,), ()
+    st = getattr(load(), fn)(g, cache._pages, N, cache.B, *before, _arg("q", q, torch.bfloat16, shape, dev), *cache._pools,
+                             _arg("row_seq", row_seq, torch.int32, (N,), dev),
+                             _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
+                             None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
+                             _arg("out", out, torch.bfloat16, shape, dev), None if w is None else w.data_ptr(),
+                             0 if w is None else w.nbytes, st)
+    if st:
+        raise Step5Error(fn, st)
 
 
 def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
@@ -658,20 +687,15 @@ def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, wor
     cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
     sigmoid gate [N][Hq] when given."""
     _attend_e4m3("step5_paged_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                 before=(int(window),))
+                 window=int(window))
 
 
 def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                            gate=None, stream=None):
     """step5_sparse_attn over the e4m3 cache: the picked regions sel_ids [N][G][top_k],
     sel_count [N][G] and the row's own region."""
-    g, N = Geometry.of(geom), q.shape[0]
-    _int32_rows(N, sel_ids=sel_ids, sel_count=sel_count)
-    if tuple(sel_ids.shape) != (N, g.num_kv_groups, g.top_k) or tuple(sel_count.shape) != (N, g.num_kv_groups):
-        raise ValueError("sel_ids must be [N][G][top_k], sel_count [N][G]")
-    _same_device(q.device, sel_ids=sel_ids, sel_count=sel_count)
     _attend_e4m3("step5_sparse_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                 after=(_ptr(sel_ids), _ptr(sel_count)))
+                 sel_ids=sel_ids, sel_count=sel_count)
 
 
 def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws: PagedWorkspace, k, v, sel_ids,
