@@ -70,11 +70,17 @@ struct PagedAttnParams {
 };
 constexpr int kPagedMaxCtas = 480;           // of one launch
 constexpr size_t kPagedItemBytes = 16 * 512;
-constexpr size_t kPagedStateFloats = (size_t)kPagedMaxCtas * 2 * 16 * 130;  // two states a CTA of up to 16 heads
+constexpr int kChunkMaxCtas = 160;           // of a launch of the kernel for several rows a sequence
+// two states a CTA: of up to 16 heads each, or of 256 head rows
+constexpr size_t kPagedStateFloats = (size_t)kChunkMaxCtas * 2 * 256 * 130;
+static_assert((size_t)kPagedMaxCtas * 2 * 16 * 130 <= kPagedStateFloats, "workspace");
 constexpr size_t kPagedWorkspaceBytes = kPagedItemBytes + kPagedStateFloats * 4;
 // kmap, vmap: the pools as [rows][128] bytes, boxes of 8 * box_regions rows, 128-byte swizzle
 cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                    int num_sms, cudaStream_t stream, bool pdl);
+// The same for launches whose sequences have several rows (no picks).
+cudaError_t launch_paged_chunk(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
+                               cudaStream_t stream, bool pdl);
 
 // A scale that can be used: positive and at most 2^126 (so that the power of two above it is finite).
 __device__ __forceinline__ bool scale_ok(float s) { return s > 0.0f && s <= 8.507059173e37f; }

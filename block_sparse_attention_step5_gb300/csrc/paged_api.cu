@@ -133,8 +133,11 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     const uint64_t rows = (uint64_t)pages->num_pages * geom->num_kv_groups * pages->page_tokens;
     if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))
         return STEP5_ERR_CUDA;
-    return launch_paged_attention(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true) == cudaSuccess ? STEP5_OK
-                                                                                                      : STEP5_ERR_CUDA;
+    // rows of a sequence share its keys' tiles when there are two of them or more on average
+    const bool chunk = sel_ids == nullptr && N >= 2 * (int64_t)B;
+    const cudaError_t e = chunk ? launch_paged_chunk(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true)
+                                : launch_paged_attention(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
+    return e == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 
 }  // namespace

@@ -28,8 +28,7 @@
 // Roles in a CTA: four softmax warps (one thread per key of the tile), a warp for each of the two
 // products, and two that look entries up (region, pool row, scales, four tiles ahead in steps) and issue the
 // copies, K a tile ahead of V, and leave what the softmax needs of each region in a small ring.
-#include "paged.cuh"
-#include "tcgen05.cuh"
+#include "paged_device.cuh"
 
 namespace step5 {
 
@@ -43,7 +42,6 @@ constexpr int kRing = 8;             // tiles whose scales and masks are in shar
 constexpr uint32_t kSlotBytes = kTile * 1024;
 constexpr float kSlack = 3.0f;       // log2 units a tile's maximum may pass the running one by
 constexpr float kPTop = 32.0f;       // weights are split from p * 2^(8 - slack): at most 2^8, whose parts fit e4m3
-constexpr float kPart = 32.0f;       // a part against the one before it
 
 // MANY: for launches of many items, three CTAs an SM with few slots, which hide one another's latency (2,048 rows
 // of 512 picks: 1,171 us against 1,411 with two); for few items two CTAs with more copies in flight and fewer states to
@@ -93,92 +91,6 @@ struct Max {
 struct Add {
     __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
-
-// Barrier over a named group of threads, returning whether any of them passed `v`.
-__device__ __forceinline__ bool group_or(int id, int threads, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(threads), "r"(v ? 1u : 0u)
-        : "memory");
-    return r != 0;
-}
-
-// Waits for phase `parity` of the barrier; gives up after 2^22 polls (far beyond any copy or product).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
-    const uint32_t addr = smem_u32(bar);
-    for (uint32_t i = 0; i < (1u << 22); ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        if (done) return true;
-    }
-    return false;
-}
-
-// True for one lane of the (converged) warp, the same each time.
-__device__ __forceinline__ bool elect() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {  // 2^x, off by at most 2^-22 of it
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
-        "mov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-
-// The next e4m3 part of two f16 values: its codes, and what is left of the values times 2^5
-// (both steps exact).
-__device__ __forceinline__ uint32_t next_part(__half2& x) {
-    const __half2_raw xr = x;
-    const uint32_t c = __nv_cvt_halfraw2_to_fp8x2(xr, __NV_SATFINITE, __NV_E4M3);
-    const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
-    x = __hmul2(__hsub2(x, __half2(f)), __float2half2_rn(kPart));
-    return c;
-}
-__device__ __forceinline__ uint32_t last_part(__half2 x) {
-    const __half2_raw xr = x;
-    return __nv_cvt_halfraw2_to_fp8x2(xr, __NV_SATFINITE, __NV_E4M3);
-}
 
 // An item: the keys of row n in group g, tiles of 16 entries.  Without picks entry e is region
 // r0 + e (r0 a multiple of the box), with picks the e-th pick and the own region behind them.
