@@ -23,6 +23,8 @@
 // Work.  As in the kernel for single rows, the tiles of all (block of rows, group) items are laid end to end and each
 // CTA takes an equal run; a second kernel joins the items that CTAs share.  A block's rows may belong to several sequences: its
 // tiles are those of each sequence in turn, with the other rows masked.
+#include <type_traits>
+
 #include "paged_device.cuh"
 
 namespace step5 {
@@ -427,21 +429,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t k_addr = smem_u32(k8), v_addr = smem_u32(v16), q_addr = smem_u32(qs);
         bool ok = true;
         int segs = 0;
-        auto note_of = [&](int t) {
-            return __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(&ring[t & (kRing - 1)].note), 0);
+        auto check = [&](bool waited) {
+            ok = __all_sync(0xffffffffu, waited) && ok;
+            if (!ok && lane == 0) give_up();
+            return ok;
         };
+        uint32_t note = 0;  // of the tile whose Q K was issued last
         auto qk = [&](int w, int t) {
-            if (w == 0) ok = ok && wait(&kfull[t & 1], (uint32_t)((t >> 1) & 1));
-            if (failed(ok)) {
-                ok = false;
-                return;
+            if (w == 0) {
+                if (!check(wait(&kfull[t & 1], (uint32_t)((t >> 1) & 1)))) return;
+                note = __shfl_sync(0xffffffffu, ring[t & (kRing - 1)].note, 0);
+                if (note & 1u) ++segs;
             }
-            if (note_of(t) & 1u) ok = wait(&qbar[w], (uint32_t)((segs - 1 + (w == 0 ? 1 : 0)) & 1));
-            if (failed(ok)) {
-                ok = false;
-                return;
-            }
-            if (w == 0 && (note_of(t) & 1u)) ++segs;
+            if ((note & 1u) && !check(wait(&qbar[w], (uint32_t)((segs - 1) & 1)))) return;
             tc::fence_after_sync();
             const uint64_t db = tc::smem_desc(k_addr + (uint32_t)(t & 1) * kKv8Bytes, 16, 1024, tc::kSwizzle128);
             const uint64_t da = tc::smem_desc(q_addr + 2u * w * kQPartBytes, 16, 1024, tc::kSwizzle128);
@@ -455,20 +455,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
         };
-        auto pv = [&](int w, int t, uint32_t note) {
-            if (w == 0) ok = ok && wait(&cfull[t & 1], (uint32_t)((t >> 1) & 1));
-            ok = ok && wait(&pbar[w], (uint32_t)(t & 1));
-            if (failed(ok)) {
-                ok = false;
-                return;
-            }
+        auto pv = [&](int w, int t, uint32_t of) {
+            if (w == 0 && !check(wait(&cfull[t & 1], (uint32_t)((t >> 1) & 1)))) return;
+            if (!check(wait(&pbar[w], (uint32_t)(t & 1)))) return;
             tc::fence_after_sync();
             const uint64_t db = tc::smem_desc(v_addr + (uint32_t)(t & 1) * kV16Bytes, kKv8Bytes, 1024, tc::kSwizzle128);
             if (elect()) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)  // 16 keys each
-                    tc::mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * i, db + 128u * i, kIdescPv, !(note & 1u) || i > 0);
-                if (note & 2u) {
+                    tc::mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * i, db + 128u * i, kIdescPv, !(of & 1u) || i > 0);
+                if (of & 2u) {
                     arrive(&obar[w]);  // (hands the converting warps' notes on)
                     tc::commit(&obar[w]);
                 }
@@ -479,10 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         qk(0, 0);
         if (ok) qk(1, 0);
         for (int t = 0; t < run && ok; ++t) {
-            const uint32_t note = note_of(t);
-            const bool more = t + 1 < run, turn = (note & 2u) != 0;
-            for (int w = 0; w < 2 && ok; ++w) {
-                pv(w, t, note);
+            const uint32_t of = note;
+            const bool more = t + 1 < run, turn = (of & 2u) != 0;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                if (ok) pv(w, t, of);
                 if (ok && more && !turn) qk(w, t + 1);
             }
             if (ok && more && turn) {
@@ -531,46 +528,55 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint4* src = reinterpret_cast<const uint4*>(v8 + (t & 1) * kKv8Bytes + key * 128);
             uint8_t* dst = v16 + (t & 1) * kV16Bytes + key * 128;
             const int sw = key & 7;
-            uint64_t seen = valid;
-            if (!(note & 4u)) {
-                const int tok = tl.t0 + key;
-                seen = 0;
-                if (tl.ok >> (key >> 3) & 1u)
-                    for (uint64_t m = tl.rows; m; m &= m - 1) {
-                        const int j = __ffsll((long long)m) - 1;
-                        const int2 s = s_seen[cw][j];
-                        if (tok >= s.x && tok <= s.y) seen |= 1ull << j;
-                    }
-            }
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {  // 16 dims
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (seen) x = src[c ^ sw];
-                if (seen && seen != valid) {
-                    uint32_t* xs = reinterpret_cast<uint32_t*>(&x);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {  // codes 0x7f and 0xff
-                        uint32_t bad = ((xs[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        if (bad == 0) continue;
-                        xs[i] &= ~((bad >> 7) * 0xffu);
-                        s_any_nan[(segs - 1) & 7] = 1;
-                        for (; bad; bad &= bad - 1)
-                            atomicOr(&s_nan[(segs - 1) & 7][c * 16 + i * 4 + ((__ffs(bad) - 1) >> 3)], (unsigned long long)seen);
-                    }
-                }
+            auto widen = [&](int c, const uint4& x) {  // dims 16 c .. 16 c + 15: chunks 2 (c % 4) and the next of half c / 4
                 const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
                 uint32_t h[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(xs[i] & 0xffffu), __NV_E4M3);
                     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(xs[i] >> 16), __NV_E4M3);
-                    h[2 * i] = (uint32_t)a.x | ((uint32_t)a.y << 16);
-                    h[2 * i + 1] = (uint32_t)b.x | ((uint32_t)b.y << 16);
+                    const __half2 a2(a), b2(b);
+                    h[2 * i] = *reinterpret_cast<const uint32_t*>(&a2);
+                    h[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&b2);
                 }
-                // dims 16 c .. 16 c + 15: chunks 2 (c % 4), 2 (c % 4) + 1 of half c / 4
                 uint8_t* to = dst + (c >> 2) * kKv8Bytes;
                 *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ sw) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                 *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            };
+            if (note & 4u) {
+                uint4 x[8];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) x[c] = src[c ^ sw];
+#pragma unroll
+                for (int c = 0; c < 8; ++c) widen(c, x[c]);
+            } else {
+                const int tok = tl.t0 + key;
+                uint64_t seen = 0;
+                if (tl.ok >> (key >> 3) & 1u)
+                    for (uint64_t m = tl.rows; m; m &= m - 1) {
+                        const int j = __ffsll((long long)m) - 1;
+                        const int2 s = s_seen[cw][j];
+                        if (tok >= s.x && tok <= s.y) seen |= 1ull << j;
+                    }
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (seen) x = src[c ^ sw];
+                    if (seen != valid) {
+                        uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {  // codes 0x7f and 0xff
+                            uint32_t bad = ((xs[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                            if (bad == 0) continue;
+                            xs[i] &= ~((bad >> 7) * 0xffu);
+                            s_any_nan[(segs - 1) & 7] = 1;
+                            for (; bad; bad &= bad - 1)
+                                atomicOr(&s_nan[(segs - 1) & 7][c * 16 + i * 4 + ((__ffs(bad) - 1) >> 3)], (unsigned long long)seen);
+                        }
+                        x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                    }
+                    widen(c, x);
+                }
             }
             fence_proxy_async();
             __syncwarp();
@@ -734,68 +740,81 @@ __global__ void __launch_bounds__(kThreads, 1)
                     to = in ? row.pos - tl.t0 : -1;
                     oks = tl.ok;
                 }
-                const float vtop = vinv * kPTop;
-                uint32_t pk[64];
-                float2 sum;
-                // With the running maximum as it is; if a weight comes out too large, that moves to the row's largest and the tile is
-                // done again (twice at most).
-#pragma unroll 1
-                for (int go = 0; go < 2; ++go) {
-                    float top = -INFINITY;
-                    sum = both(0.0f);
+                // the row's largest logit in the tile (in log2 units); the running maximum follows it when it is passed by more
+                // than the slack, which rescales l and O
+                float mx = -INFINITY;
+                auto largest = [&](auto edge) {
 #pragma unroll
                     for (int c = 0; c < 128; c += 32) {
                         float x[32];
                         tc::ld32(s_at + c, x);
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
-                            const int reg = c / 8 + g;
-                            const float2 f = both(tl.ks[reg] * cq), vf = both(tl.vs[reg] * vtop), nm = both(neg_m);
+                            if constexpr (decltype(edge)::value) {
 #pragma unroll
-                            for (int d = 0; d < 8; d += 2) {
-                                const int col = c + 8 * g + d;
-                                float2 y = fma2(make_float2(x[8 * g + d], x[8 * g + d + 1]), f, nm);
-                                if (!all) {
-                                    const bool okr = (oks >> reg & 1u) != 0;
-                                    if (!(okr && col >= from && col <= to)) y.x = -INFINITY;
-                                    if (!(okr && col + 1 >= from && col + 1 <= to)) y.y = -INFINITY;
+                                for (int d = 0; d < 8; ++d) {
+                                    const int col = c + 8 * g + d;
+                                    if (!((oks >> (c / 8 + g) & 1u) && col >= from && col <= to)) x[8 * g + d] = -INFINITY;
                                 }
-                                top = fmaxf(top, fmaxf(y.x, y.y));
-                                const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
-                                sum = add2(sum, e2);
-                                const __half2 h = __float22half2_rn(mul2(e2, vf));
-                                pk[(c + 8 * g + d) / 2] = *reinterpret_cast<const uint32_t*>(&h);
                             }
+                            const float* v = x + 8 * g;
+                            const float m8 = fmaxf(max3(max3(v[0], v[1], v[2]), v[3], v[4]), max3(v[5], v[6], v[7]));
+                            mx = fmaxf(mx, m8 * tl.ks[c / 8 + g]);  // (ks > 0 where the region is readable; -inf * 0 is no maximum)
                         }
                     }
-                    if (go == 1 || !__any_sync(0xffffffffu, top > kSlack)) break;
-                    float mx = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 128; c += 32) {
-                        float x[32];
-                        tc::ld32(s_at + c, x);
-#pragma unroll
-                        for (int d = 0; d < 32; ++d) {
-                            const int reg = c / 8 + d / 8;
-                            if ((oks >> reg & 1u) && c + d >= from && c + d <= to) mx = fmaxf(mx, x[d] * (tl.ks[reg] * cq));
-                        }
-                    }
+                };
+                if (all)
+                    largest(std::false_type{});
+                else
+                    largest(std::true_type{});
+                mx *= cq;
+                const bool up = mx > kSlack - neg_m || (neg_m == INFINITY && mx > -INFINITY);
+                if (__any_sync(0xffffffffu, up)) {
                     float alpha = 1.0f;
-                    if (top > kSlack) {
+                    if (up) {
                         alpha = ex2(-neg_m - mx);
                         l *= alpha;
                         neg_m = -mx;
                     }
                     if (i > 0) rescale(alpha);
                 }
-                l += sum.x + sum.y;
-                {
-                    uint32_t a[32], b[32];
+                // weights: P takes the first half of S's place, behind the columns already read
+                const float vtop = vinv * kPTop;
+                float2 sum = both(0.0f);
+                auto weights = [&](auto edge) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) a[x] = pk[x], b[x] = pk[32 + x];
-                    tc::st32(s_at, a);
-                    tc::st32(s_at + 32, b);
-                }
+                    for (int c = 0; c < 128; c += 32) {
+                        float x[32];
+                        tc::ld32(s_at + c, x);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            const int reg = c / 8 + g;
+                            const float2 f = both(tl.ks[reg] * cq), vf = both(tl.vs[reg] * vtop), nm = both(neg_m);
+#pragma unroll
+                            for (int d = 0; d < 8; d += 2) {
+                                float2 y = fma2(make_float2(x[8 * g + d], x[8 * g + d + 1]), f, nm);
+                                if constexpr (decltype(edge)::value) {
+                                    const int col = c + 8 * g + d;
+                                    const bool okr = (oks >> reg & 1u) != 0;
+                                    if (!(okr && col >= from && col <= to)) y.x = -INFINITY;
+                                    if (!(okr && col + 1 >= from && col + 1 <= to)) y.y = -INFINITY;
+                                }
+                                const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+                                sum = add2(sum, e2);
+                                const __half2 h = __float22half2_rn(mul2(e2, vf));
+                                pk[4 * g + d / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                            }
+                        }
+                        tc::st16u(s_at + c / 2, pk);
+                    }
+                };
+                if (all)
+                    weights(std::false_type{});
+                else
+                    weights(std::true_type{});
+                l += sum.x + sum.y;
+                tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) arrive(&pbar[w]);
