@@ -87,12 +87,18 @@ struct Walk {
         for (int i = 0; i < S::RL; ++i) v |= (uint64_t)__ballot_sync(0xffffffffu, f(mine[i], arg)) << (32 * i);
         return v;
     }
-    __device__ __forceinline__ int open(const PagedAttnParams& p, int n0, int lane) {
+    __device__ __forceinline__ void rows_of(const PagedAttnParams& p, int n0, int lane) {
 #pragma unroll
         for (int i = 0; i < S::RL; ++i) {
             mine[i] = Row{-1, -1, 0};
             if (lane + 32 * i < S::NB) mine[i] = row_at(p, n0 + lane + 32 * i);
         }
+    }
+    __device__ __forceinline__ int open(const PagedAttnParams& p, int n0, int lane) {
+        rows_of(p, n0, lane);
+        return begin(p);
+    }
+    __device__ __forceinline__ int begin(const PagedAttnParams& p) {  // tiles of the block; the walk at the first
         valid = votes([](const Row& r, int) { return r.b >= 0; }, 0);
         bad = votes([](const Row& r, int) { return r.b == -2; }, 0);
         todo = valid;
@@ -164,6 +170,18 @@ __device__ __forceinline__ void write_out8(const PagedAttnParams& p, int n0, int
                    pack_bf16x2(v[6] * f, v[7] * f));
 }
 
+// 32 bytes, in one store (a whole sector) where the buffer allows it; 16-byte aligned.
+__device__ __forceinline__ void store32(void* to, const uint32_t (&v)[8]) {
+    if (reinterpret_cast<uintptr_t>(to) & 31) {
+        static_cast<uint4*>(to)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4*>(to)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -218,10 +236,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t of_group, total, per, start;
     {
         int* tiles = reinterpret_cast<int*>(smem);  // (nothing is copied yet)
-        for (int i = warp; i < blocks; i += kThreads / 32) {
-            Walk<S> w;
-            const int t = w.open(p, i * NB, lane);
-            if (lane == 0) tiles[i] = t;
+        constexpr int kWarps = kThreads / 32, kDeep = 4;  // (rows of four blocks in flight)
+        for (int i = warp; i < blocks; i += kWarps * kDeep) {
+            Walk<S> w[kDeep];
+#pragma unroll
+            for (int x = 0; x < kDeep; ++x) w[x].rows_of(p, i + x * kWarps < blocks ? (i + x * kWarps) * NB : p.N, lane);
+#pragma unroll
+            for (int x = 0; x < kDeep; ++x) {
+                const int t = w[x].begin(p);
+                if (lane == 0 && i + x * kWarps < blocks) tiles[i + x * kWarps] = t;
+            }
         }
         __syncthreads();
         const int chunk = (blocks + kThreads - 1) / kThreads, i0 = min(blocks, tid * chunk), i1 = min(blocks, i0 + chunk);
@@ -544,11 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ sw) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
             };
             if (note & 4u) {
-                uint4 x[8];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) x[c] = src[c ^ sw];
-#pragma unroll
-                for (int c = 0; c < 8; ++c) widen(c, x[c]);
+#pragma unroll 1
+                for (int c = 0; c < 8; c += 2) {
+                    const uint4 x = src[c ^ sw], y = src[(c + 1) ^ sw];
+                    widen(c, x);
+                    widen(c + 1, y);
+                }
             } else {
                 const int tok = tl.t0 + key;
                 uint64_t seen = 0;
@@ -590,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int w = warp >> 2, r = tid & 127, j = w * RB + r / HQ;  // row tile, head row in it, row of the block
         const uint32_t lanes = tc::taddr(tmem, (warp & 3) * 32, 0);
         const uint32_t s_at = lanes + 128u * w, o_at = lanes + 256u + 128u * w;
-        uint8_t* qh = qs + 2 * w * kQPartBytes + r * 128;
         float neg_m = INFINITY, l = 0.0f, vref = 0.0f, vinv = 0.0f, cq = 0.0f;
         Row row{-1, -1, 0};
         Walk<S> walk{};
@@ -600,45 +624,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0, segs = 0;
         bool ok = true;
 
+        // The warp's 32 head rows, 16 lanes to each.
         auto build_q = [&] {
-            const int n = s.blk * NB + j;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)n * p.Hq + (int64_t)s.g * HQ + r % HQ) * 128);
-            const bool have = row.b >= 0;
-            uint32_t a = 0;
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (have) x = __ldg(src + c);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            const int d8 = lane & 15, hr0 = (warp & 3) * 32 + (lane >> 4);
+            const uint32_t rows_ok = __ballot_sync(0xffffffffu, row.b >= 0);
+            const uint16_t* src = p.q + ((int64_t)(s.blk * NB + w * RB) * p.Hq + (int64_t)s.g * HQ) * 128 + d8 * 8;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                uint4 x[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) a = max(a, max(xs[i] & 0x7fffu, (xs[i] >> 16) & 0x7fffu));
-            }
-            // q * 2^(7 - e) is below 2^8 for the largest |q|, whose exponent is e
-            const int ex = a == 0 ? 0 : max((int)(a >> 7) - 127, -100);
-            const float up = __uint_as_float((uint32_t)(min(7 - ex, 120) + 127) << 23);
-            cq = a < 0x7f80u ? p.scale_log2 / up : __int_as_float(0x7fc00000);
-#pragma unroll 4
-            for (int c = 0; c < 8; ++c) {
-                uint32_t hi[4], lo[4];
+                for (int i = 0; i < 8; ++i) {
+                    const int hr = hr0 + i0 + 2 * i;
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (rows_ok >> (i0 + 2 * i + (lane >> 4)) & 1u)
+                        x[i] = __ldg(reinterpret_cast<const uint4*>(src + ((int64_t)(hr / HQ) * p.Hq + hr % HQ) * 128));
+                }
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (have) x = __ldg(src + 2 * c + i);
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                for (int i = 0; i < 8; ++i) {
+                    const int hr = hr0 + i0 + 2 * i;
+                    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    uint32_t a = 0;
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) a = max(a, max(xs[y] & 0x7fffu, (xs[y] >> 16) & 0x7fffu));
+#pragma unroll
+                    for (int d = 8; d; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+                    // q * 2^(7 - e) is below 2^8 for the largest |q|, whose exponent is e
+                    const int ex = a == 0 ? 0 : max((int)(a >> 7) - 127, -100);
+                    const float up = __uint_as_float((uint32_t)(min(7 - ex, 120) + 127) << 23);
+                    const float c = a < 0x7f80u ? p.scale_log2 / up : __int_as_float(0x7fc00000);
+                    const float c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, 16);
+                    if (lane == i0 + 2 * i) cq = c0;
+                    if (lane == i0 + 2 * i + 1) cq = c1;
+                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
                         __half2 v = __floats2half2_rn(bf16_lo(xs[y]) * up, bf16_hi(xs[y]) * up);
-                        const uint32_t h8 = next_part(v);  // (leaves what is left times 2^5)
-                        const uint32_t l8 = last_part(__hmul2(v, __float2half2_rn(1.0f / kPart)));
-                        if (y & 1)
-                            hi[2 * i + (y >> 1)] |= h8 << 16, lo[2 * i + (y >> 1)] |= l8 << 16;
-                        else
-                            hi[2 * i + (y >> 1)] = h8, lo[2 * i + (y >> 1)] = l8;
+                        hi[y >> 1] |= next_part(v) << (16 * (y & 1));  // (leaves what is left times 2^5)
+                        lo[y >> 1] |= last_part(__hmul2(v, __float2half2_rn(1.0f / kPart))) << (16 * (y & 1));
                     }
+                    uint8_t* to = qs + 2 * w * kQPartBytes + hr * 128 + (((d8 >> 1) ^ (hr & 7)) << 4) + (d8 & 1) * 8;
+                    *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(to + kQPartBytes) = make_uint2(lo[0], lo[1]);
                 }
-                const int to = (c ^ (r & 7)) << 4;
-                *reinterpret_cast<uint4*>(qh + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(qh + kQPartBytes + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             fence_proxy_async();
             __syncwarp();
@@ -665,31 +692,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return;
             }
             tc::fence_after_sync();
-            const bool any_nan = s_any_nan[i & 7] != 0;
-            const float f = l == 0.0f ? 0.0f : vref * (1.0f / kPTop) / l;
-            float* st = p.states + ((int64_t)2 * blockIdx.x + (e_begin >= start ? 1 : 0)) * kStateFloats;
+            const bool any_nan = s_any_nan[i & 7] != 0, whole = e.n == e.nt;
+            float f = l == 0.0f ? 0.0f : vref * (1.0f / kPTop) / l;
             const int hr = w * 128 + r;
-            if (e.n != e.nt) *reinterpret_cast<float2*>(st + 2 * hr) = make_float2(-neg_m, l);
+            const int64_t at = (int64_t)(e.blk * NB + j) * p.Hq + (int64_t)e.g * HQ + r % HQ;
+            float* st = p.states + ((int64_t)2 * blockIdx.x + (e_begin >= start ? 1 : 0)) * kStateFloats;
+            if (!whole) *reinterpret_cast<float2*>(st + 2 * hr) = make_float2(-neg_m, l);
+            if (whole && p.gate != nullptr && e_row.b != -1) f *= 1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at])));
 #pragma unroll 1
             for (int c = 0; c < 128; c += 32) {
                 float o[32];
                 __syncwarp();
                 tc::ld32(o_at + c, o);
 #pragma unroll
-                for (int d = 0; d < 32; d += 8) {
-                    if (e_row.b == -1) break;
-                    float v[8];
+                for (int d = 0; d < 32; ++d) {
+                    o[d] = l == 0.0f ? 0.0f : o[d] * f;
+                    if (any_nan && (s_nan[i & 7][c + d] >> j & 1u)) o[d] = __int_as_float(0x7fc00000);
+                }
+                if (whole && e_row.b != -1) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) {
-                        v[x] = l == 0.0f ? 0.0f : o[d + x] * f;
-                        if (any_nan && (s_nan[i & 7][c + d + x] >> j & 1u)) v[x] = __int_as_float(0x7fc00000);
+                    for (int d = 0; d < 32; d += 16) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) u[x] = pack_bf16x2(o[d + 2 * x], o[d + 2 * x + 1]);
+                        store32(p.out + at * 128 + c + d, u);
                     }
-                    if (e.n == e.nt) {
-                        write_out8<S>(p, e.blk * NB, e.g, hr, c + d, v);
-                    } else {  // CTAs share the item; each leaves its state, which the join kernel reads
-                        float4* to = reinterpret_cast<float4*>(st + 512 + hr * 128 + c + d);
-                        to[0] = make_float4(v[0], v[1], v[2], v[3]);
-                        to[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else if (!whole) {  // CTAs share the item; each leaves its state, which the join kernel reads
+#pragma unroll
+                    for (int d = 0; d < 32; d += 8) {
+                        uint32_t u[8];
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) u[x] = __float_as_uint(o[d + x]);
+                        store32(st + 512 + hr * 128 + c + d, u);
                     }
                 }
             }
@@ -743,30 +777,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the row's largest logit in the tile (in log2 units); the running maximum follows it when it is passed by more
                 // than the slack, which rescales l and O
                 float mx = -INFINITY;
-                auto largest = [&](auto edge) {
+                uint32_t xa[32], xb[32];  // columns of S
+                auto largest = [&](int c, uint32_t(&x)[32], auto edge) {
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        float x[32];
-                        tc::ld32(s_at + c, x);
+                    for (int g = 0; g < 4; ++g) {
+                        float v[8];
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
+                        for (int d = 0; d < 8; ++d) {
+                            v[d] = __uint_as_float(x[8 * g + d]);
                             if constexpr (decltype(edge)::value) {
-#pragma unroll
-                                for (int d = 0; d < 8; ++d) {
-                                    const int col = c + 8 * g + d;
-                                    if (!((oks >> (c / 8 + g) & 1u) && col >= from && col <= to)) x[8 * g + d] = -INFINITY;
-                                }
+                                const int col = c + 8 * g + d;
+                                if (!((oks >> (c / 8 + g) & 1u) && col >= from && col <= to)) v[d] = -INFINITY;
                             }
-                            const float* v = x + 8 * g;
-                            const float m8 = fmaxf(max3(max3(v[0], v[1], v[2]), v[3], v[4]), max3(v[5], v[6], v[7]));
-                            mx = fmaxf(mx, m8 * tl.ks[c / 8 + g]);  // (ks > 0 where the region is readable; -inf * 0 is no maximum)
                         }
+                        const float m8 = fmaxf(max3(max3(v[0], v[1], v[2]), v[3], v[4]), max3(v[5], v[6], v[7]));
+                        mx = fmaxf(mx, m8 * tl.ks[c / 8 + g]);  // (ks > 0 where the region is readable; -inf * 0 is no maximum)
+                    }
+                };
+                // (loops, not unrolled further: straight code for a whole tile ran 20 % slower, short of instructions)
+                auto all_largest = [&](auto edge) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 64) {
+                        tc::get32(s_at + c, xa);
+                        tc::get32(s_at + c + 32, xb);
+                        tc::got32(xa);
+                        tc::got32(xb);
+                        largest(c, xa, edge);
+                        largest(c + 32, xb, edge);
                     }
                 };
                 if (all)
-                    largest(std::false_type{});
+                    all_largest(std::false_type{});
                 else
-                    largest(std::true_type{});
+                    all_largest(std::true_type{});
                 mx *= cq;
                 const bool up = mx > kSlack - neg_m || (neg_m == INFINITY && mx > -INFINITY);
                 if (__any_sync(0xffffffffu, up)) {
@@ -781,38 +824,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights: P takes the first half of S's place, behind the columns already read
                 const float vtop = vinv * kPTop;
                 float2 sum = both(0.0f);
-                auto weights = [&](auto edge) {
+                auto weights = [&](int c, uint32_t(&x)[32], auto edge) {
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int c = 0; c < 128; c += 32) {
-                        float x[32];
-                        tc::ld32(s_at + c, x);
-                        uint32_t pk[16];
+                    for (int g = 0; g < 4; ++g) {
+                        const int reg = c / 8 + g;
+                        const float2 f = both(tl.ks[reg] * cq), vf = both(tl.vs[reg] * vtop), nm = both(neg_m);
 #pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const int reg = c / 8 + g;
-                            const float2 f = both(tl.ks[reg] * cq), vf = both(tl.vs[reg] * vtop), nm = both(neg_m);
-#pragma unroll
-                            for (int d = 0; d < 8; d += 2) {
-                                float2 y = fma2(make_float2(x[8 * g + d], x[8 * g + d + 1]), f, nm);
-                                if constexpr (decltype(edge)::value) {
-                                    const int col = c + 8 * g + d;
-                                    const bool okr = (oks >> reg & 1u) != 0;
-                                    if (!(okr && col >= from && col <= to)) y.x = -INFINITY;
-                                    if (!(okr && col + 1 >= from && col + 1 <= to)) y.y = -INFINITY;
-                                }
-                                const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
-                                sum = add2(sum, e2);
-                                const __half2 h = __float22half2_rn(mul2(e2, vf));
-                                pk[4 * g + d / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                        for (int d = 0; d < 8; d += 2) {
+                            float2 y = fma2(make_float2(__uint_as_float(x[8 * g + d]), __uint_as_float(x[8 * g + d + 1])), f, nm);
+                            if constexpr (decltype(edge)::value) {
+                                const int col = c + 8 * g + d;
+                                const bool okr = (oks >> reg & 1u) != 0;
+                                if (!(okr && col >= from && col <= to)) y.x = -INFINITY;
+                                if (!(okr && col + 1 >= from && col + 1 <= to)) y.y = -INFINITY;
                             }
+                            const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+                            sum = add2(sum, e2);
+                            const __half2 h = __float22half2_rn(mul2(e2, vf));
+                            pk[4 * g + d / 2] = *reinterpret_cast<const uint32_t*>(&h);
                         }
-                        tc::st16u(s_at + c / 2, pk);
+                    }
+                    tc::st16u(s_at + c / 2, pk);
+                };
+                auto all_weights = [&](auto edge) {
+#pragma unroll 1
+                    for (int c = 0; c < 128; c += 32) {
+                        tc::get32(s_at + c, xa);
+                        tc::got32(xa);
+                        weights(c, xa, edge);
                     }
                 };
                 if (all)
-                    weights(std::false_type{});
+                    all_weights(std::false_type{});
                 else
-                    weights(std::true_type{});
+                    all_weights(std::true_type{});
                 l += sum.x + sum.y;
                 tc::wait_st();
                 tc::fence_before_sync();
