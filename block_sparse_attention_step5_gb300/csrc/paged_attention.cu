@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 // The running maxima move when a key passes one by more than the slack, vref when a
                 // vscale passes it; l and O are rescaled then.  Every softmax thread takes the same steps.
                 if (!w_ok) give_up();
-                if (group_or(1, kSoft, (sees && (top > kSlack || me.vs > vref)) || !w_ok)) {
+                if (__builtin_expect(group_or(1, kSoft, (sees && (top > kSlack || me.vs > vref)) || !w_ok), 0)) {
                     if (*reinterpret_cast<volatile int*>(&s_fail) != 0) failed = true;
                     float alpha[H];
                     int hidx = 0;
@@ -699,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 }
                 // a copied V row that the row does not see is zeroed: the cache may hold anything there, and
                 // a zero weight must meet a finite value
-                if (me.loaded && !sees) {
+                if (__builtin_expect(me.loaded && !sees, 0)) {
                     const int slot = (t + 1 < run ? 2 * t + 2 : 2 * t + 1) % S::kSlots;
                     w_ok &= wait(&vfull[t & 3], (uint32_t)((t >> 2) & 1));
                     uint4* vr = reinterpret_cast<uint4*>(slots + slot * kSlotBytes + key * 128);

@@ -87,18 +87,12 @@ struct Walk {
         for (int i = 0; i < S::RL; ++i) v |= (uint64_t)__ballot_sync(0xffffffffu, f(mine[i], arg)) << (32 * i);
         return v;
     }
-    __device__ __forceinline__ void rows_of(const PagedAttnParams& p, int n0, int lane) {
+    __device__ __forceinline__ int open(const PagedAttnParams& p, int n0, int lane) {
 #pragma unroll
         for (int i = 0; i < S::RL; ++i) {
             mine[i] = Row{-1, -1, 0};
             if (lane + 32 * i < S::NB) mine[i] = row_at(p, n0 + lane + 32 * i);
         }
-    }
-    __device__ __forceinline__ int open(const PagedAttnParams& p, int n0, int lane) {
-        rows_of(p, n0, lane);
-        return begin(p);
-    }
-    __device__ __forceinline__ int begin(const PagedAttnParams& p) {  // tiles of the block; the walk at the first
         valid = votes([](const Row& r, int) { return r.b >= 0; }, 0);
         bad = votes([](const Row& r, int) { return r.b == -2; }, 0);
         todo = valid;
@@ -236,16 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t of_group, total, per, start;
     {
         int* tiles = reinterpret_cast<int*>(smem);  // (nothing is copied yet)
-        constexpr int kWarps = kThreads / 32, kDeep = 4;  // (rows of four blocks in flight)
-        for (int i = warp; i < blocks; i += kWarps * kDeep) {
-            Walk<S> w[kDeep];
-#pragma unroll
-            for (int x = 0; x < kDeep; ++x) w[x].rows_of(p, i + x * kWarps < blocks ? (i + x * kWarps) * NB : p.N, lane);
-#pragma unroll
-            for (int x = 0; x < kDeep; ++x) {
-                const int t = w[x].begin(p);
-                if (lane == 0 && i + x * kWarps < blocks) tiles[i + x * kWarps] = t;
-            }
+        for (int i = warp; i < blocks; i += kThreads / 32) {
+            Walk<S> w;
+            const int t = w.open(p, i * NB, lane);
+            if (lane == 0) tiles[i] = t;
         }
         __syncthreads();
         const int chunk = (blocks + kThreads - 1) / kThreads, i0 = min(blocks, tid * chunk), i1 = min(blocks, i0 + chunk);
@@ -569,11 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (note & 4u) {
 #pragma unroll 1
-                for (int c = 0; c < 8; c += 2) {
-                    const uint4 x = src[c ^ sw], y = src[(c + 1) ^ sw];
-                    widen(c, x);
-                    widen(c + 1, y);
-                }
+                for (int c = 0; c < 8; ++c) widen(c, src[c ^ sw]);
             } else {
                 const int tok = tl.t0 + key;
                 uint64_t seen = 0;
@@ -630,24 +614,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t rows_ok = __ballot_sync(0xffffffffu, row.b >= 0);
             const uint16_t* src = p.q + ((int64_t)(s.blk * NB + w * RB) * p.Hq + (int64_t)s.g * HQ) * 128 + d8 * 8;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                uint4 x[8];
+            for (int i0 = 0; i0 < 32; i0 += 8) {
+                uint4 x[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const int hr = hr0 + i0 + 2 * i;
                     x[i] = make_uint4(0, 0, 0, 0);
                     if (rows_ok >> (i0 + 2 * i + (lane >> 4)) & 1u)
                         x[i] = __ldg(reinterpret_cast<const uint4*>(src + ((int64_t)(hr / HQ) * p.Hq + hr % HQ) * 128));
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const int hr = hr0 + i0 + 2 * i;
                     const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    uint32_t a = 0;
+                    uint32_t a2 = __vmaxu2(__vmaxu2(xs[0] & 0x7fff7fffu, xs[1] & 0x7fff7fffu),
+                                           __vmaxu2(xs[2] & 0x7fff7fffu, xs[3] & 0x7fff7fffu));
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) a = max(a, max(xs[y] & 0x7fffu, (xs[y] >> 16) & 0x7fffu));
-#pragma unroll
-                    for (int d = 8; d; d >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, d));
+                    for (int d = 8; d; d >>= 1) a2 = __vmaxu2(a2, __shfl_xor_sync(0xffffffffu, a2, d));
+                    const uint32_t a = max(a2 & 0xffffu, a2 >> 16);
                     // q * 2^(7 - e) is below 2^8 for the largest |q|, whose exponent is e
                     const int ex = a == 0 ? 0 : max((int)(a >> 7) - 127, -100);
                     const float up = __uint_as_float((uint32_t)(min(7 - ex, 120) + 127) << 23);
@@ -705,10 +689,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tc::ld32(o_at + c, o);
 #pragma unroll
-                for (int d = 0; d < 32; ++d) {
-                    o[d] = l == 0.0f ? 0.0f : o[d] * f;
-                    if (any_nan && (s_nan[i & 7][c + d] >> j & 1u)) o[d] = __int_as_float(0x7fc00000);
-                }
+                for (int d = 0; d < 32; ++d) o[d] = l == 0.0f ? 0.0f : o[d] * f;
+                if (any_nan)
+#pragma unroll
+                    for (int d = 0; d < 32; ++d)
+                        if (s_nan[i & 7][c + d] >> j & 1u) o[d] = __int_as_float(0x7fc00000);
                 if (whole && e_row.b != -1) {
 #pragma unroll
                     for (int d = 0; d < 32; d += 16) {
@@ -757,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_after_sync();
                 const Tile& tl = ring[t & (kRing - 1)];
-                if (tl.vmax > vref) {  // (the same for every thread)
+                if (__builtin_expect(tl.vmax > vref, 0)) {  // (the same for every thread)
                     const uint32_t u = __float_as_uint(tl.vmax);
                     const float up = __uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u));
                     if (i > 0) rescale(vref / up);
@@ -777,8 +762,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the row's largest logit in the tile (in log2 units); the running maximum follows it when it is passed by more
                 // than the slack, which rescales l and O
                 float mx = -INFINITY;
-                uint32_t xa[32], xb[32];  // columns of S
-                auto largest = [&](int c, uint32_t(&x)[32], auto edge) {
+                uint32_t x[32];  // columns of S
+                auto largest = [&](int c, const uint32_t(&x)[32], auto edge) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         float v[8];
@@ -797,13 +782,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (loops, not unrolled further: straight code for a whole tile ran 20 % slower, short of instructions)
                 auto all_largest = [&](auto edge) {
 #pragma unroll 1
-                    for (int c = 0; c < 128; c += 64) {
-                        tc::get32(s_at + c, xa);
-                        tc::get32(s_at + c + 32, xb);
-                        tc::got32(xa);
-                        tc::got32(xb);
-                        largest(c, xa, edge);
-                        largest(c + 32, xb, edge);
+                    for (int c = 0; c < 128; c += 32) {
+                        tc::get32(s_at + c, x);
+                        tc::got32(x);
+                        largest(c, x, edge);
                     }
                 };
                 if (all)
@@ -812,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     all_largest(std::true_type{});
                 mx *= cq;
                 const bool up = mx > kSlack - neg_m || (neg_m == INFINITY && mx > -INFINITY);
-                if (__any_sync(0xffffffffu, up)) {
+                if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {
                     float alpha = 1.0f;
                     if (up) {
                         alpha = ex2(-neg_m - mx);
@@ -824,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // weights: P takes the first half of S's place, behind the columns already read
                 const float vtop = vinv * kPTop;
                 float2 sum = both(0.0f);
-                auto weights = [&](int c, uint32_t(&x)[32], auto edge) {
+                auto weights = [&](int c, const uint32_t(&x)[32], auto edge) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -850,9 +832,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 auto all_weights = [&](auto edge) {
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
-                        tc::get32(s_at + c, xa);
-                        tc::got32(xa);
-                        weights(c, xa, edge);
+                        tc::get32(s_at + c, x);
+                        tc::got32(x);
+                        weights(c, x, edge);
                     }
                 };
                 if (all)
