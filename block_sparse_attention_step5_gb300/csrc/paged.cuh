@@ -61,7 +61,7 @@ struct PagedAttnParams {
     const uint16_t* gate;      // [N][Hq] bf16 logits or null
     uint16_t* out;             // [N][Hq][128]
     uint32_t* status;
-    int4* shared_items;        // workspace: [kPagedMaxCtas], the item that begins in a CTA and goes on in others
+    int4* shared_items;        // workspace: [kPagedMaxCtas], items that CTAs share: (n, g, first CTA, last CTA or -1)
     float* states;             // workspace: partial states of items that CTAs share
     int N, B, G, Hq, top_k, window;
     int box_regions;           // regions of one TMA box (a power of two <= 16 that divides a page's)

@@ -21,8 +21,8 @@
 // a power of two not below any vscale so far, so that the parts' range is spent on what a key adds to the
 // output; the row sum takes the weight without it.
 //
-// Work.  The tiles of all (rows, group) items are laid end to end and every CTA takes an equal
-// run of them, so a ragged batch, one long row and a chunk of many rows all fill the GPU; a second
+// Work.  An item is a (row, group).  Few items are cut into equal parts, many have their tiles laid end to end
+// and cut into equal runs, so that a ragged batch, one long row and a chunk of many rows all fill the GPU; a second
 // kernel joins the items that CTAs share, in CTA order (the bits do not depend on timing).
 //
 // Roles in a CTA: four softmax warps (one thread per key of the tile), a warp for each of the two
@@ -160,7 +160,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __shared__ float red[3][4][H + 1];
     __shared__ __align__(16) float s_cq[2][H];
     __shared__ int64_t s_scan[kThreads / 32];
-    __shared__ int s_item, s_off;
+    __shared__ int s_tiles[kThreads], s_item, s_off, s_run, s_first, s_last;
+    __shared__ uint32_t s_ctas[kThreads / 32][32];
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int items = p.N * p.G;
@@ -190,11 +191,63 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (tid < kSoft) reinterpret_cast<uint4*>(qt + 2 * H * 128)[i] = make_uint4(0, 0, 0, 0);
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.shared_items[blockIdx.x].z = -1;  // (again below if an item that other CTAs share begins here)
 
-    // this CTA's run of tiles: thread sums of the items' tiles, their prefix, the item that the run starts in
-    int64_t total, start, per;
-    {
+    // This CTA's run of tiles, from tile off0 of item item0 on.
+    int64_t start = 0, per = 1;  // (many items: the run's first tile among all, tiles of a run)
+    const bool few = 2 * items <= (int)gridDim.x;
+    if (few) {
+        // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the smallest L of 32 tried that needs
+        // no more CTAs than there are (2 L0 always does).  No CTA then has parts of two items.
+        const int mine = tid < items ? item_at<PICKS>(p, tid).tiles : 0;
+        s_tiles[tid] = mine;
+        int64_t sum = mine;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) s_scan[warp] = sum;
+        if (tid == 0) s_run = 0;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
+        const uint32_t least = max((uint32_t)p.min_tiles, (uint32_t)((total + gridDim.x - 1) / gridDim.x));
+        uint32_t most = least + (least * (uint32_t)lane + 30u) / 31u;  // this lane's L
+        uint32_t ctas = 0;
+        for (int i = warp; i < items; i += kThreads / 32) ctas += ((uint32_t)s_tiles[i] + most - 1u) / most;
+        s_ctas[warp][lane] = ctas;
+        __syncthreads();
+        ctas = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) ctas += s_ctas[w][lane];
+        most = __shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, ctas <= gridDim.x)) - 1);
+        const int parts = (int)(((uint32_t)mine + most - 1u) / most);
+        int inc = parts;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int first = inc - parts;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w)
+            if (w < warp) first += (int)s_scan[w];
+        const int part = (int)blockIdx.x - first;
+        if (part >= 0 && part < parts) {
+            s_item = tid;
+            s_off = (int)((int64_t)mine * part / parts);
+            s_run = (int)((int64_t)mine * (part + 1) / parts) - s_off;
+            s_first = first;
+            s_last = first + parts - 1;
+            if (part == 0) p.shared_items[tid] = make_int4(0, 0, 0, -1);  // (again below if it has several parts)
+        }
+        if (blockIdx.x == 0 && tid < items && mine == 0) p.shared_items[tid] = make_int4(0, 0, 0, -1);
+    } else {
+        // Many: the items' tiles are laid end to end and every CTA takes an equal run of them.
+        if (tid == 0) {
+            p.shared_items[blockIdx.x] = make_int4(0, 0, 0, -1);  // (again below if an item that other CTAs share begins here)
+            s_run = 0;
+        }
         const int chunk = (items + kThreads - 1) / kThreads;
         const int i0 = min(items, tid * chunk), i1 = min(items, i0 + chunk);
         int64_t sum = 0;
@@ -207,18 +260,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         }
         if (lane == 31) s_scan[warp] = inc;
         __syncthreads();
-        int64_t before = inc - sum;
-        total = 0;
+        int64_t before = inc - sum, total = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += s_scan[w];
             total += s_scan[w];
         }
-        if (total < (1 << 30))
-            per = ((int)total + (int)gridDim.x - 1) / (int)gridDim.x;
-        else
-            per = (total + gridDim.x - 1) / gridDim.x;
-        if (per < p.min_tiles) per = p.min_tiles;
+        per = (total + gridDim.x - 1) / gridDim.x;
         start = blockIdx.x * per;
         if (start >= before && start < before + sum) {
             int64_t at = before;
@@ -227,6 +275,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 if (start < at + t) {
                     s_item = i;
                     s_off = (int)(start - at);
+                    s_run = (int)min(per, total - start);
                     break;
                 }
                 at += t;
@@ -237,8 +286,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
-    const int run = (int)(start < total ? min(per, total - start) : 0);
-    const int item0 = s_item, off0 = s_off;
+    const int run = s_run, item0 = s_item, off0 = s_off;
 
     if (run == 0) {
         // nothing to do
@@ -453,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         float vref = 0.0f, vinv = 0.0f;
         Item it{}, done{};  // the segment's item; that of the segment before, for its epilogue
         int64_t done_begin = 0;
-        bool whole = true;
+        bool whole = true, begins = true;  // it has the whole item, its first tile
         bool failed = false;
         int t = 0;  // tile of the run
 
@@ -532,11 +580,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 for (int h = 0; h < H; ++h)
                     o[h] = a[h] + (a[H + h] + (H == 8 ? b[h] : a[(2 * H + h) & 15]) * (1.0f / kPart)) * (1.0f / kPart);
             }
-            float* st = p.states + ((int64_t)2 * blockIdx.x + (done_begin >= start ? 1 : 0)) * S::kState;
+            float* st = p.states + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const float L = (rd[0][h] + rd[1][h]) + (rd[2][h] + rd[3][h]);
-                const float v = L == 0.0f ? 0.0f : o[h] / L * (vref * (1.0f / kPTop));
+                const float v = L == 0.0f ? 0.0f : o[h] * __fdividef(vref * (1.0f / kPTop), L);
                 if (whole) {
                     write_out<H>(p, done.n, done.g, h, key, v);
                 } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
@@ -547,8 +595,12 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     st[2 * H + h * 128 + key] = v;
                 }
             }
-            if (!whole && done_begin >= start && tid == 0)
-                p.shared_items[blockIdx.x] = make_int4(done.n, done.g, (int)((done_begin + done.tiles - 1) / per), 0);
+            if (!whole && begins && tid == 0) {
+                if (few)
+                    p.shared_items[item0] = make_int4(done.n, done.g, s_first, s_last);
+                else
+                    p.shared_items[blockIdx.x] = make_int4(done.n, done.g, (int)blockIdx.x, (int)((done_begin + done.tiles - 1) / per));
+            }
         };
 
         int segs = 0, nitem = item0, off = off0;
@@ -579,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             done = it;
             done_begin = start + (run - left) - off;
             whole = seg == it.tiles;
+            begins = off == 0;
             left -= seg;
             off = 0;
             vref = vinv = 0.0f;
@@ -721,41 +774,49 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     if (warp == 0) tc::dealloc(tmem, S::kCols);
 }
 
-// Joins the items that CTAs of the launch before shared: a block per (CTA in which such an item
-// begins, head column), its threads' groups of 128 dims taking every kJoinGroups-th state, so that all
-// loads are in flight at once (the states lie in L2; the join is latency, not bandwidth).  The sums run in an order
-// fixed by the CTAs.
-constexpr int kJoinGroups = 8;
+// Joins the items that CTAs of the launch before shared: a block per (entry of shared_items, head), its threads'
+// groups of 128 dims taking every kJoinGroups-th state, eight of them asked for before the weights are known
+// (the states lie in L2; the join is latency, not bandwidth).  The sums run in an order fixed by the CTAs.
+constexpr int kJoinGroups = 4;
 template <class S>
 __global__ void __launch_bounds__(128 * kJoinGroups) join_kernel(PagedAttnParams p) {
     __shared__ float sw[kPagedMaxCtas], sm[kJoinGroups * 4], so[kJoinGroups][128], sl[kJoinGroups];
     pdl_wait();
     pdl_launch_dependents();
-    const int first = blockIdx.x, c = blockIdx.y, tid = threadIdx.x, d = tid & 127, grp = tid >> 7;
-    const int4 item = p.shared_items[first];
-    const int last = item.z;
-    if (last < 0) return;
-    auto state = [&](int cta) { return p.states + ((int64_t)2 * cta + (cta == first ? 1 : 0)) * S::kState; };
-    const int n = last - first + 1;
+    const int c = blockIdx.y, tid = threadIdx.x, d = tid & 127, grp = tid >> 7;
+    const int4 item = p.shared_items[blockIdx.x];
+    const int first = item.z, n = item.w - first + 1;
+    if (item.w < 0) return;
+    auto state = [&](int i) { return p.states + ((int64_t)2 * (first + i) + (i == 0 ? 1 : 0)) * S::kState; };
+    constexpr int kDeep = 8;
+    float v[kDeep];
+#pragma unroll
+    for (int x = 0; x < kDeep; ++x) v[x] = grp + x * kJoinGroups < n ? state(grp + x * kJoinGroups)[2 * S::H + c * 128 + d] : 0.0f;
     // the states' weights 2^(m - M) l
-    float m = -INFINITY, l = 0.0f;
-    if (tid < n) {
-        m = state(first + tid)[c];
-        l = state(first + tid)[S::H + c];
-    }
-    float M = l == 0.0f ? -INFINITY : m;
+    float M = -INFINITY;
+    for (int i = tid; i < n; i += 128 * kJoinGroups)
+        if (state(i)[S::H + c] != 0.0f) M = fmaxf(M, state(i)[c]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     if ((tid & 31) == 0) sm[tid >> 5] = M;
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < kJoinGroups * 4; ++x) M = fmaxf(M, sm[x]);
-    if (tid < n) sw[tid] = l == 0.0f ? 0.0f : ex2(m - M) * l;
+    for (int i = tid; i < n; i += 128 * kJoinGroups) {
+        const float l = state(i)[S::H + c];
+        sw[i] = l == 0.0f ? 0.0f : ex2(state(i)[c] - M) * l;
+    }
     __syncthreads();
     float o = 0.0f, w = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kDeep; ++x)
+        if (grp + x * kJoinGroups < n) {
+            o = fmaf(sw[grp + x * kJoinGroups], v[x], o);
+            w += sw[grp + x * kJoinGroups];
+        }
 #pragma unroll 8
-    for (int i = grp; i < n; i += kJoinGroups) {
-        o = fmaf(sw[i], state(first + i)[2 * S::H + c * 128 + d], o);
+    for (int i = grp + kDeep * kJoinGroups; i < n; i += kJoinGroups) {
+        o = fmaf(sw[i], state(i)[2 * S::H + c * 128 + d], o);
         w += sw[i];
     }
     so[grp][d] = o;
@@ -795,6 +856,7 @@ cudaError_t launch_shape(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     cfg.numAttrs = pdl ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, paged_attn_kernel<S>, kmap, vmap, p);
     if (e != cudaSuccess) return e;
+    if (2 * p.N * p.G <= (int)cfg.gridDim.x) cfg.gridDim.x = (unsigned)(p.N * p.G);  // (the entries are by item then)
     cfg.gridDim.y = S::H;
     cfg.blockDim = dim3(128 * kJoinGroups);
     cfg.dynamicSmemBytes = 0;

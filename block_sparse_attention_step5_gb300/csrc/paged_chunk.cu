@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kMmaWarp) tc::alloc(&s_tmem, kCols);
     pdl_wait();
     pdl_launch_dependents();
-    if (tid == 0) p.shared_items[blockIdx.x].z = -1;
+    if (tid == 0) p.shared_items[blockIdx.x].w = -1;
 
     // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups.
     int64_t of_group, total, per, start;
@@ -713,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (e.n != e.nt && e_begin >= start && tid == 0)
-                p.shared_items[blockIdx.x] = make_int4(e.blk * NB, e.g, (int)((e_begin + e.nt - 1) / per), 0);
+                p.shared_items[blockIdx.x] = make_int4(e.blk * NB, e.g, (int)blockIdx.x, (int)((e_begin + e.nt - 1) / per));
         };
 
         for (int left = run; left > 0 && ok;) {
@@ -863,7 +863,7 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
     pdl_launch_dependents();
     const int first = blockIdx.x, hr = blockIdx.y * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * 8;
     const int4 item = p.shared_items[first];
-    const int last = item.z, n = item.x + hr / S::HQ;
+    const int last = item.w, n = item.x + hr / S::HQ;
     if (last < 0 || n >= p.N || p.row_seq[n] == -1) return;
     auto state = [&](int cta) { return p.states + ((int64_t)2 * cta + (cta == first ? 1 : 0)) * kStateFloats; };
     float M = -INFINITY;
