@@ -111,13 +111,13 @@ __device__ __forceinline__ void append_row(const AppendParams& p, uint32_t id, i
             const uint16_t* src = v < nq ? p.q + n * p.q_stride + (int64_t)v * 128
                                          : (j < p.G ? p.k + n * p.k_stride + (int64_t)j * 128
                                                     : p.v + n * p.v_stride + (int64_t)(j - p.G) * 128);
-            x[i].a = __ldg(reinterpret_cast<const uint4*>(src + c0));
-            x[i].b = __ldg(reinterpret_cast<const uint4*>(src + c1));
+            x[i].a = *reinterpret_cast<const uint4*>(src + c0);
+            x[i].b = *reinterpret_cast<const uint4*>(src + c1);
         }
         if (!ok) return;
         if (turns) {
-            cs = __ldg(reinterpret_cast<const uint4*>(p.cos + (int64_t)pos * (p.rot >> 1) + 8 * l8));
-            sn = __ldg(reinterpret_cast<const uint4*>(p.sin + (int64_t)pos * (p.rot >> 1) + 8 * l8));
+            cs = *reinterpret_cast<const uint4*>(p.cos + (int64_t)pos * (p.rot >> 1) + 8 * l8);
+            sn = *reinterpret_cast<const uint4*>(p.sin + (int64_t)pos * (p.rot >> 1) + 8 * l8);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -168,8 +168,8 @@ __device__ __forceinline__ void append_region(const AppendParams& p, int n, int 
             x[i].b = *reinterpret_cast<const uint4*>(src + t * stride + c1);
             if (turns) {
                 const int64_t at = (int64_t)(pos + t) * (p.rot >> 1) + 8 * l8;
-                cs[i] = __ldg(reinterpret_cast<const uint4*>(p.cos + at));
-                sn[i] = __ldg(reinterpret_cast<const uint4*>(p.sin + at));
+                cs[i] = *reinterpret_cast<const uint4*>(p.cos + at);
+                sn[i] = *reinterpret_cast<const uint4*>(p.sin + at);
             }
         }
     }

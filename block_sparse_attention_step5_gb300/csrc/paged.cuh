@@ -20,7 +20,7 @@ struct PageMap {
 __device__ __forceinline__ int64_t page_row(const PageMap& m, int G, int b, int g, int tok) {
     const int slot = tok / m.page_tokens;
     if (slot >= m.table_len) return -1;
-    const int page = m.table ? __ldg(m.table + (int64_t)b * m.table_len + slot) : b;
+    const int page = m.table ? m.table[(int64_t)b * m.table_len + slot] : b;
     if (page < 0 || page >= m.num_pages) return -1;
     return ((int64_t)page * G + g) * m.page_tokens + (tok - slot * m.page_tokens);
 }

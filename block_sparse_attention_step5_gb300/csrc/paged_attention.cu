@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (steps & 1) {
                 n_r = -1;
                 if (PICKS) {
-                    if (e < it.entries) n_r = e == it.entries - 1 ? it.hi >> 3 : __ldg(ids + e);
+                    if (e < it.entries) n_r = e == it.entries - 1 ? it.hi >> 3 : ids[e];
                 } else if (it.b >= 0 && e < (it.entries + k - 1) / k * k && ((it.r0 + e) | (k - 1)) >= (it.lo >> 3)) {
                     n_r = it.r0 + e;  // (with its box, of which some region is the row's)
                 }
@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (steps & 4) {
                 n_ks = n_vs = 0.0f;
                 if (n_row >= 0) {
-                    n_ks = __ldg(p.k_scales + (n_row >> 3));
-                    n_vs = __ldg(p.v_scales + (n_row >> 3));
+                    n_ks = p.k_scales[n_row >> 3];
+                    n_vs = p.v_scales[n_row >> 3];
                 }
             }
         };
