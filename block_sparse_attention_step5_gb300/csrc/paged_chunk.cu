@@ -96,17 +96,20 @@ struct Walk {
         valid = votes([](const Row& r, int) { return r.b >= 0; }, 0);
         bad = votes([](const Row& r, int) { return r.b == -2; }, 0);
         todo = valid;
-        int t = 0;
-        while (todo) {
-            pass(p);
-            t += tiles;
-        }
         if (valid == 0) {  // one empty tile if anything is to be written
             b = -1, lo = 0, hi = -1, max_lo = 0, min_hi = -1, rows = 0, r0 = regions = at = 0;
             return tiles = bad ? 1 : 0;
         }
-        todo = valid;
         pass(p);
+        int t = tiles;
+        if (todo) {  // several sequences: count them all, then back to the first
+            while (todo) {
+                pass(p);
+                t += tiles;
+            }
+            todo = valid;
+            pass(p);
+        }
         return t;
     }
     __device__ __forceinline__ void pass(const PagedAttnParams& p) {
@@ -226,6 +229,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
 
+    // (every row's sequence and position on their way before the walks below, which take them one block at a time)
+    for (int i = tid * 32; i < p.N; i += kThreads * 32) {
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_seq + i));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_pos + i));
+    }
     // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups.
     int64_t of_group, total, per, start;
     {
@@ -331,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (steps & 2) {
                 n_ks = n_vs = 0.0f;
                 if (n_row >= 0) {
-                    n_ks = __ldg(p.k_scales + (n_row >> 3));
-                    n_vs = __ldg(p.v_scales + (n_row >> 3));
+                    n_ks = p.k_scales[n_row >> 3];
+                    n_vs = p.v_scales[n_row >> 3];
                 }
             }
         };
@@ -506,10 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp >= kConvWarp) {
-        // ---------------- V's codes to f16: a key to a thread.  A key that no row of the block sees becomes zero (the cache may
-        // hold anything there); of a key that only some rows see, NaN codes are taken out and noted for those rows.
+        // ---------------- V's codes to f16: a key to a thread.  In a tile of which some row does not see some key, NaN codes
+        // become zero (the cache may hold anything there, and a zero weight must meet a finite value), noted for the rows that see
+        // them.
         const int cw = warp - kConvWarp, key = cw * 32 + lane;
-        uint64_t valid = 0;
         int segs = 0;
         for (int t = 0; t < run; ++t) {
             bool ok = wait(&vfull[t & 1], (uint32_t)((t >> 1) & 1));
@@ -525,15 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++segs;
                 __syncwarp();
-                valid = 0;
-#pragma unroll
-                for (int i = 0; i < S::RL; ++i) {
-                    Row r{-1, -1, 0};
-                    if (lane + 32 * i < NB) {
-                        r = row_at(p, tl.n0 + lane + 32 * i);
-                        s_seen[cw][lane + 32 * i] = make_int2(r.lo, r.pos);
-                    }
-                    valid |= (uint64_t)__ballot_sync(0xffffffffu, r.b >= 0) << (32 * i);
+                for (int i = lane; i < NB; i += 32) {
+                    const Row r = row_at(p, tl.n0 + i);
+                    s_seen[cw][i] = make_int2(r.lo, r.pos);
                 }
                 __syncwarp();
             }
@@ -559,32 +561,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) widen(c, src[c ^ sw]);
             } else {
-                const int tok = tl.t0 + key;
-                uint64_t seen = 0;
-                if (tl.ok >> (key >> 3) & 1u)
-                    for (uint64_t m = tl.rows; m; m &= m - 1) {
-                        const int j = __ffsll((long long)m) - 1;
-                        const int2 s = s_seen[cw][j];
-                        if (tok >= s.x && tok <= s.y) seen |= 1ull << j;
-                    }
 #pragma unroll 1
                 for (int c = 0; c < 8; ++c) {
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (seen) x = src[c ^ sw];
-                    if (seen != valid) {
-                        uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+                    const uint4 x = src[c ^ sw];
+                    uint32_t xs[4] = {x.x, x.y, x.z, x.w}, bad[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {  // codes 0x7f and 0xff
-                            uint32_t bad = ((xs[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                            if (bad == 0) continue;
-                            xs[i] &= ~((bad >> 7) * 0xffu);
-                            s_any_nan[(segs - 1) & 7] = 1;
-                            for (; bad; bad &= bad - 1)
-                                atomicOr(&s_nan[(segs - 1) & 7][c * 16 + i * 4 + ((__ffs(bad) - 1) >> 3)], (unsigned long long)seen);
+                    for (int i = 0; i < 4; ++i) bad[i] = ((xs[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // 0x7f, 0xff
+                    if (__builtin_expect((bad[0] | bad[1] | bad[2] | bad[3]) != 0, 0)) {
+                        const int tok = tl.t0 + key;
+                        unsigned long long seen = 0;
+                        if (tl.ok >> (key >> 3) & 1u)
+                            for (uint64_t m = tl.rows; m; m &= m - 1) {
+                                const int2 s = s_seen[cw][__ffsll((long long)m) - 1];
+                                if (tok >= s.x && tok <= s.y) seen |= m & (0 - m);
+                            }
+                        if (seen) s_any_nan[(segs - 1) & 7] = 1;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            xs[i] &= ~((bad[i] >> 7) * 0xffu);
+                            for (uint32_t m = seen ? bad[i] : 0u; m; m &= m - 1)
+                                atomicOr(&s_nan[(segs - 1) & 7][c * 16 + i * 4 + ((__ffs(m) - 1) >> 3)], seen);
                         }
-                        x = make_uint4(xs[0], xs[1], xs[2], xs[3]);
                     }
-                    widen(c, x);
+                    widen(c, make_uint4(xs[0], xs[1], xs[2], xs[3]));
                 }
             }
             fence_proxy_async();
@@ -608,47 +607,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0, segs = 0;
         bool ok = true;
 
-        // The warp's 32 head rows, 16 lanes to each.
+        // The warp's 32 head rows, eight lanes of 16 dims to each; the next eight rows are on their way meanwhile.
         auto build_q = [&] {
-            const int d8 = lane & 15, hr0 = (warp & 3) * 32 + (lane >> 4);
+            const int l8 = lane & 7, hr0 = (warp & 3) * 32 + (lane >> 3);
             const uint32_t rows_ok = __ballot_sync(0xffffffffu, row.b >= 0);
-            const uint16_t* src = p.q + ((int64_t)(s.blk * NB + w * RB) * p.Hq + (int64_t)s.g * HQ) * 128 + d8 * 8;
+            const uint16_t* src = p.q + ((int64_t)(s.blk * NB + w * RB) * p.Hq + (int64_t)s.g * HQ) * 128 + l8 * 16;
+            uint4 nx[2][2];
+            auto ask = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int hr = hr0 + i0 + 4 * i;
+                    nx[i][0] = nx[i][1] = make_uint4(0, 0, 0, 0);
+                    if (rows_ok >> (i0 + 4 * i + (lane >> 3)) & 1u) {
+                        const uint4* at = reinterpret_cast<const uint4*>(src + ((int64_t)(hr / HQ) * p.Hq + hr % HQ) * 128);
+                        nx[i][0] = at[0];
+                        nx[i][1] = at[1];
+                    }
+                }
+            };
+            ask(0);
 #pragma unroll 1
             for (int i0 = 0; i0 < 32; i0 += 8) {
-                uint4 x[4];
+                const uint4 x[2][2] = {{nx[0][0], nx[0][1]}, {nx[1][0], nx[1][1]}};
+                if (i0 < 24) ask(i0 + 8);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int hr = hr0 + i0 + 2 * i;
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    if (rows_ok >> (i0 + 2 * i + (lane >> 4)) & 1u)
-                        x[i] = __ldg(reinterpret_cast<const uint4*>(src + ((int64_t)(hr / HQ) * p.Hq + hr % HQ) * 128));
-                }
+                for (int i = 0; i < 2; ++i) {
+                    const int hr = hr0 + i0 + 4 * i;
+                    const uint32_t xs[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                    uint32_t a2 = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int hr = hr0 + i0 + 2 * i;
-                    const uint32_t xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                    uint32_t a2 = __vmaxu2(__vmaxu2(xs[0] & 0x7fff7fffu, xs[1] & 0x7fff7fffu),
-                                           __vmaxu2(xs[2] & 0x7fff7fffu, xs[3] & 0x7fff7fffu));
+                    for (int y = 0; y < 8; ++y) a2 = __vmaxu2(a2, xs[y] & 0x7fff7fffu);
 #pragma unroll
-                    for (int d = 8; d; d >>= 1) a2 = __vmaxu2(a2, __shfl_xor_sync(0xffffffffu, a2, d));
+                    for (int d = 4; d; d >>= 1) a2 = __vmaxu2(a2, __shfl_xor_sync(0xffffffffu, a2, d));
                     const uint32_t a = max(a2 & 0xffffu, a2 >> 16);
                     // q * 2^(7 - e) is below 2^8 for the largest |q|, whose exponent is e
                     const int ex = a == 0 ? 0 : max((int)(a >> 7) - 127, -100);
                     const float up = __uint_as_float((uint32_t)(min(7 - ex, 120) + 127) << 23);
                     const float c = a < 0x7f80u ? p.scale_log2 / up : __int_as_float(0x7fc00000);
-                    const float c0 = __shfl_sync(0xffffffffu, c, 0), c1 = __shfl_sync(0xffffffffu, c, 16);
-                    if (lane == i0 + 2 * i) cq = c0;
-                    if (lane == i0 + 2 * i + 1) cq = c1;
-                    uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+                    const float mine = __shfl_sync(0xffffffffu, c, (lane & 3) * 8);
+                    if (lane >> 2 == (i0 >> 2) + i) cq = mine;
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        __half2 v = __floats2half2_rn(bf16_lo(xs[y]) * up, bf16_hi(xs[y]) * up);
-                        hi[y >> 1] |= next_part(v) << (16 * (y & 1));  // (leaves what is left times 2^5)
-                        lo[y >> 1] |= last_part(__hmul2(v, __float2half2_rn(1.0f / kPart))) << (16 * (y & 1));
+                    for (int y = 0; y < 8; ++y) {
+                        const float2 v2 = mul2(make_float2(bf16_lo(xs[y]), bf16_hi(xs[y])), both(up));
+                        const __half2 v = __float22half2_rn(v2);
+                        const uint32_t h = last_part(v);
+                        const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)h, __NV_E4M3);
+                        const uint32_t l = last_part(__hsub2(v, __half2(back)));
+                        hi[y >> 1] = y & 1 ? __byte_perm(hi[y >> 1], h, 0x5410) : h;
+                        lo[y >> 1] = y & 1 ? __byte_perm(lo[y >> 1], l, 0x5410) : l;
                     }
-                    uint8_t* to = qs + 2 * w * kQPartBytes + hr * 128 + (((d8 >> 1) ^ (hr & 7)) << 4) + (d8 & 1) * 8;
-                    *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2*>(to + kQPartBytes) = make_uint2(lo[0], lo[1]);
+                    uint8_t* to = qs + 2 * w * kQPartBytes + hr * 128 + ((l8 ^ (hr & 7)) << 4);
+                    *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(to + kQPartBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             fence_proxy_async();
@@ -749,31 +760,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vref = up;
                     vinv = 1.0f / up;
                 }
-                // the columns that the row sees, unless every row sees all: from .. to, of readable regions
+                // the columns that the row sees, unless every row sees all: from .. to - 1, of readable regions
                 const bool all = (tl.note & 4u) != 0;
-                int from = 0, to = 127;
-                uint32_t oks = 0xffffu;
-                if (!all) {
-                    const bool in = row.b >= 0 && (tl.rows >> j & 1u);
-                    from = in ? row.lo - tl.t0 : 128;
-                    to = in ? row.pos - tl.t0 : -1;
-                    oks = tl.ok;
+                int from = 0, to = 0;
+                if (!all && row.b >= 0 && (tl.rows >> j & 1u)) {
+                    from = min(max(row.lo - tl.t0, 0), 128);
+                    to = min(max(row.pos - tl.t0 + 1, 0), 128);
                 }
+                // those of columns c .. c + 31 as a mask
+                auto seen = [&](int c) {
+                    const uint32_t okr = tl.ok >> (c >> 3) & 15u;
+                    const uint32_t below = to - c >= 32 ? ~0u : (1u << max(to - c, 0)) - 1u;
+                    const uint32_t under = from - c >= 32 ? ~0u : (1u << max(from - c, 0)) - 1u;
+                    return below & ~under & ((okr * 0x00204081u & 0x01010101u) * 0xffu);
+                };
                 // the row's largest logit in the tile (in log2 units); the running maximum follows it when it is passed by more
                 // than the slack, which rescales l and O
                 float mx = -INFINITY;
                 uint32_t x[32];  // columns of S
                 auto largest = [&](int c, const uint32_t(&x)[32], auto edge) {
+                    const uint32_t mask = decltype(edge)::value ? seen(c) : ~0u;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         float v[8];
 #pragma unroll
                         for (int d = 0; d < 8; ++d) {
                             v[d] = __uint_as_float(x[8 * g + d]);
-                            if constexpr (decltype(edge)::value) {
-                                const int col = c + 8 * g + d;
-                                if (!((oks >> (c / 8 + g) & 1u) && col >= from && col <= to)) v[d] = -INFINITY;
-                            }
+                            if constexpr (decltype(edge)::value) v[d] = mask >> (8 * g + d) & 1u ? v[d] : -INFINITY;
                         }
                         const float m8 = fmaxf(max3(max3(v[0], v[1], v[2]), v[3], v[4]), max3(v[5], v[6], v[7]));
                         mx = fmaxf(mx, m8 * tl.ks[c / 8 + g]);  // (ks > 0 where the region is readable; -inf * 0 is no maximum)
@@ -808,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 sum = both(0.0f);
                 auto weights = [&](int c, const uint32_t(&x)[32], auto edge) {
                     uint32_t pk[16];
+                    const uint32_t mask = decltype(edge)::value ? seen(c) : ~0u;
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int reg = c / 8 + g;
@@ -816,10 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int d = 0; d < 8; d += 2) {
                             float2 y = fma2(make_float2(__uint_as_float(x[8 * g + d]), __uint_as_float(x[8 * g + d + 1])), f, nm);
                             if constexpr (decltype(edge)::value) {
-                                const int col = c + 8 * g + d;
-                                const bool okr = (oks >> reg & 1u) != 0;
-                                if (!(okr && col >= from && col <= to)) y.x = -INFINITY;
-                                if (!(okr && col + 1 >= from && col + 1 <= to)) y.y = -INFINITY;
+                                y.x = mask >> (8 * g + d) & 1u ? y.x : -INFINITY;
+                                y.y = mask >> (8 * g + d + 1) & 1u ? y.y : -INFINITY;
                             }
                             const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
                             sum = add2(sum, e2);
