@@ -43,7 +43,7 @@ constexpr uint32_t kIdescQk = tc::instr_desc(tc::kFmtE4M3, false, false, 128, 12
 constexpr uint32_t kIdescPv = tc::instr_desc(tc::kFmtF16, false, true, 128, 128);
 constexpr float kSlack = 6.0f;                  // log2 units a weight may lie above the running maximum
 constexpr float kPTop = 256.0f;                 // P = p 2^8 vscale / vref <= 2^14
-constexpr int kStateFloats = 256 * 130;         // of a partial state: (m, l) and o[128] of each head row
+constexpr int kStateFloats = 256 * 130;         // of a partial state: (m, l) of each head row, o as [16][256 head rows][8 dims]
 
 template <int HQ_>
 struct Shape {
@@ -57,11 +57,8 @@ struct Row {
     int b, pos, lo;  // keys: tokens lo .. pos of sequence b; b = -1: padding or past N, -2: out of range (zeros)
 };
 
-__device__ __forceinline__ Row row_at(const PagedAttnParams& p, int n) {
-    Row r{-1, -1, 0};
-    if (n >= p.N) return r;
-    r.b = p.row_seq[n];
-    r.pos = p.row_pos[n];
+__device__ __forceinline__ Row row_of(const PagedAttnParams& p, int b, int pos) {
+    Row r{b, pos, 0};
     if (r.b == -1) return r;
     if (r.b < 0 || r.b >= p.B || r.pos < 0 || r.pos / p.pages.page_tokens >= p.pages.table_len) {
         r.b = -2;
@@ -69,6 +66,9 @@ __device__ __forceinline__ Row row_at(const PagedAttnParams& p, int n) {
     }
     r.lo = p.window > 0 ? max(0, r.pos - p.window + 1) : 0;
     return r;
+}
+__device__ __forceinline__ Row row_at(const PagedAttnParams& p, int n) {
+    return n < p.N ? row_of(p, p.row_seq[n], p.row_pos[n]) : Row{-1, -1, 0};
 }
 
 // The tiles of a block of rows as a warp walks them: those of each of its sequences in turn.
@@ -87,12 +87,25 @@ struct Walk {
         for (int i = 0; i < S::RL; ++i) v |= (uint64_t)__ballot_sync(0xffffffffu, f(mine[i], arg)) << (32 * i);
         return v;
     }
-    __device__ __forceinline__ int open(const PagedAttnParams& p, int n0, int lane) {
+    // Asks for a block's rows; what open() then takes.
+    struct Rows {
+        int seq[S::RL], pos[S::RL];
+    };
+    static __device__ __forceinline__ Rows fetch(const PagedAttnParams& p, int n0, int lane) {
+        Rows r;
 #pragma unroll
         for (int i = 0; i < S::RL; ++i) {
-            mine[i] = Row{-1, -1, 0};
-            if (lane + 32 * i < S::NB) mine[i] = row_at(p, n0 + lane + 32 * i);
+            const int n = n0 + lane + 32 * i;
+            const bool in = lane + 32 * i < S::NB && n < p.N;
+            r.seq[i] = in ? p.row_seq[n] : -1;
+            r.pos[i] = in ? p.row_pos[n] : -1;
         }
+        return r;
+    }
+    // At the first tile of these rows; returns how many there are.
+    __device__ __forceinline__ int open(const PagedAttnParams& p, const Rows& r) {
+#pragma unroll
+        for (int i = 0; i < S::RL; ++i) mine[i] = row_of(p, r.seq[i], r.pos[i]);
         valid = votes([](const Row& r, int) { return r.b >= 0; }, 0);
         bad = votes([](const Row& r, int) { return r.b == -2; }, 0);
         todo = valid;
@@ -229,18 +242,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
 
-    // (every row's sequence and position on their way before the walks below, which take them one block at a time)
-    for (int i = tid * 32; i < p.N; i += kThreads * 32) {
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_seq + i));
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(p.row_pos + i));
-    }
     // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups.
     int64_t of_group, total, per, start;
     {
         int* tiles = reinterpret_cast<int*>(smem);  // (nothing is copied yet)
+        auto ahead = Walk<S>::fetch(p, warp * NB, lane);
         for (int i = warp; i < blocks; i += kThreads / 32) {
+            const auto rows = ahead;
+            ahead = Walk<S>::fetch(p, (i + kThreads / 32) * NB, lane);
             Walk<S> w;
-            const int t = w.open(p, i * NB, lane);
+            const int t = w.open(p, rows);
             if (lane == 0) tiles[i] = t;
         }
         __syncthreads();
@@ -257,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncthreads();
         int64_t before = inc - sum;
         of_group = 0;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < warp) before += s_scan[w];
             of_group += s_scan[w];
@@ -297,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.blk = 0;
                 if (++s.g >= p.G) return false;
             }
-            s.nt = w.open(p, s.blk * NB, lane);
+            s.nt = w.open(p, w.fetch(p, s.blk * NB, lane));
             if (s.nt > s.off) break;
             ++s.blk;
         }
@@ -719,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t u[8];
 #pragma unroll
                         for (int x = 0; x < 8; ++x) u[x] = __float_as_uint(o[d + x]);
-                        store32(st + 512 + hr * 128 + c + d, u);
+                        store32(st + 512 + ((c + d) >> 3) * 2048 + hr * 8, u);
                     }
                 }
             }
@@ -868,12 +880,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the items that CTAs of the launch before shared: a block per (CTA in which such an item begins, 16 of its
-// head rows), 16 threads of 8 dims to a head row, states in the CTAs' order.
+// head rows), 16 threads of 8 dims to a head row (a warp: 8 rows, 4 threads each), states in the CTAs' order.
 template <class S>
 __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
     pdl_wait();
     pdl_launch_dependents();
-    const int first = blockIdx.x, hr = blockIdx.y * 16 + (threadIdx.x >> 4), d0 = (threadIdx.x & 15) * 8;
+    const int first = blockIdx.x, hr = blockIdx.y * 16 + (threadIdx.x >> 7) * 8 + (threadIdx.x & 7), d8 = (threadIdx.x >> 3) & 15;
     const int4 item = p.shared_items[first];
     const int last = item.w, n = item.x + hr / S::HQ;
     if (last < 0 || n >= p.N || p.row_seq[n] == -1) return;
@@ -888,7 +900,7 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
 #pragma unroll 4
     for (int i = first; i <= last; ++i) {
         const float2 ml = *reinterpret_cast<const float2*>(state(i) + 2 * hr);
-        const float4* v = reinterpret_cast<const float4*>(state(i) + 512 + hr * 128 + d0);
+        const float4* v = reinterpret_cast<const float4*>(state(i) + 512 + d8 * 2048 + hr * 8);
         const float4 a = v[0], b = v[1];
         const float f = ml.y == 0.0f ? 0.0f : ex2(ml.x - M) * ml.y;
         w += f;
@@ -898,7 +910,7 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
     }
 #pragma unroll
     for (int d = 0; d < 8; ++d) o[d] = w == 0.0f ? 0.0f : o[d] / w;
-    write_out8<S>(p, item.x, item.y, hr, d0, o);
+    write_out8<S>(p, item.x, item.y, hr, d8 * 8, o);
 }
 
 template <int HQ>
