@@ -65,7 +65,6 @@ struct PagedAttnParams {
     float* states;             // workspace: partial states of items that CTAs share
     int N, B, G, Hq, top_k, window;
     int box_regions;           // regions of one TMA box (a power of two <= 16 that divides a page's)
-    int min_tiles;             // fewest tiles worth a CTA
     float scale_log2;          // softmax_scale * log2(e)
 };
 constexpr int kPagedMaxCtas = 480;           // of one launch

@@ -128,7 +128,6 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     p.box_regions = 1;
     if (sel_ids == nullptr)
         while (p.box_regions < 16 && (pages->page_tokens / 8) % (2 * p.box_regions) == 0) p.box_regions *= 2;
-    p.min_tiles = 1;
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)pages->num_pages * geom->num_kv_groups * pages->page_tokens;
     if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))

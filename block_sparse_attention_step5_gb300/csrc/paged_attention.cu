@@ -110,7 +110,7 @@ __device__ __forceinline__ Item item_at(const PagedAttnParams& p, int i) {
     it.hi = p.row_pos[it.n];
     it.lo = it.r0 = it.entries = it.tiles = 0;
     if (it.b == -1) return it;
-    if (it.b < 0 || it.b >= p.B || it.hi < 0 || it.hi / p.pages.page_tokens >= p.pages.table_len) {
+    if (it.b < 0 || it.b >= p.B || it.hi < 0 || it.hi >= p.pages.page_tokens * p.pages.table_len) {  // (fits int32)
         it.b = -2;
         it.tiles = 1;
         return it;
@@ -161,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __shared__ __align__(16) float s_cq[2][H];
     __shared__ int64_t s_scan[kThreads / 32];
     __shared__ int s_tiles[kThreads], s_item, s_off, s_run, s_first, s_last;
+    __shared__ Item s_it;  // item s_item
     __shared__ uint32_t s_ctas[kThreads / 32][32];
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -198,18 +199,19 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     if (few) {
         // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the smallest L of 32 tried that needs
         // no more CTAs than there are (2 L0 always does).  No CTA then has parts of two items.
-        const int mine = tid < items ? item_at<PICKS>(p, tid).tiles : 0;
-        s_tiles[tid] = mine;
-        int64_t sum = mine;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        // (fewer than 2^8 items of at most 2^24 tiles)
+        Item own{};
+        if (tid < items) own = item_at<PICKS>(p, tid);
+        const uint32_t mine = (uint32_t)own.tiles;
+        s_tiles[tid] = own.tiles;
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
         if (lane == 0) s_scan[warp] = sum;
         if (tid == 0) s_run = 0;
         __syncthreads();
-        int64_t total = 0;
+        uint32_t total = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) total += s_scan[w];
-        const uint32_t least = max((uint32_t)p.min_tiles, (uint32_t)((total + gridDim.x - 1) / gridDim.x));
+        for (int w = 0; w < kThreads / 32; ++w) total += (uint32_t)s_scan[w];
+        const uint32_t least = max(1u, total / gridDim.x + (total % gridDim.x ? 1u : 0u));
         uint32_t most = least + (least * (uint32_t)lane + 30u) / 31u;  // this lane's L
         uint32_t ctas = 0;
         for (int i = warp; i < items; i += kThreads / 32) ctas += ((uint32_t)s_tiles[i] + most - 1u) / most;
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) ctas += s_ctas[w][lane];
         most = __shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, ctas <= gridDim.x)) - 1);
-        const int parts = (int)(((uint32_t)mine + most - 1u) / most);
+        const int parts = (int)((mine + most - 1u) / most);
         int inc = parts;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         const int part = (int)blockIdx.x - first;
         if (part >= 0 && part < parts) {
             s_item = tid;
+            s_it = own;
             s_off = (int)((int64_t)mine * part / parts);
             s_run = (int)((int64_t)mine * (part + 1) / parts) - s_off;
             s_first = first;
@@ -271,9 +274,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         if (start >= before && start < before + sum) {
             int64_t at = before;
             for (int i = i0; i < i1; ++i) {
-                const int t = item_at<PICKS>(p, i).tiles;
+                const Item it = item_at<PICKS>(p, i);
+                const int t = it.tiles;
                 if (start < at + t) {
                     s_item = i;
+                    s_it = it;
                     s_off = (int)(start - at);
                     s_run = (int)min(per, total - start);
                     break;
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // next four while these go by.
         int b_r = 0, b_row = -1, n_r = 0, n_row = -1, batch = -1, done = 0;
         float b_ks = 0.0f, b_vs = 0.0f, n_ks = 0.0f, n_vs = 0.0f;
+        bool fresh = false;  // n_ks, n_vs are the batch's
         const int32_t* ids = nullptr;
         auto look = [&](int of, int steps) {
             const int e = (of * 4 + (lane >> 3)) * kTile + q;
@@ -355,8 +361,15 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 fence_proxy_async();
                 __syncwarp();
             }
+            uint64_t* full = isv ? &vfull[t & 3] : &kfull[t & 3];
+            const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
+            if (lane == 0) expect_tx(full, (uint32_t)__popc(have) * 1024u * k);
+            __syncwarp();
+            if (row >= 0) tma_load_2d(dst + q * 1024, isv ? &vmap : &kmap, full, 0, row);
             if (!isv) {
-                // (this slot was free, so the softmax is past tile t - 5 and the ring's entry is free too)
+                // (this slot was free, so the softmax is past tile t - 5 and the ring's entry is free too; the copies are on
+                // their way while the scales of a segment's first tile come)
+                if (fresh) b_ks = n_ks, b_vs = n_vs, fresh = false;
                 if (lane >> 3 == (at & 3)) {
                     const int t0 = b_r * 8;
                     const int a = min(max(it.lo - t0, 0), 8), z = min(max(it.hi - t0 + 1, 0), 8);
@@ -370,11 +383,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 if (lw == 0 && lane == 0) s_note[t & (kRing - 1)] = note;
                 __syncwarp();
             }
-            uint64_t* full = isv ? &vfull[t & 3] : &kfull[t & 3];
-            const uint32_t have = __ballot_sync(0xffffffffu, row >= 0);
-            if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(have) * 1024u * k);
-            __syncwarp();
-            if (row >= 0) tma_load_2d(dst + q * 1024, isv ? &vmap : &kmap, full, 0, row);
+            if (lane == 0) arrive(full);
         };
         int row = -1;  // of the tile whose V is next
         uint32_t zero = 0;
@@ -385,8 +394,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (t < run) {
                 const bool first = in_seg == 0;
                 if (first) {  // the next segment
-                    it.tiles = 0;
-                    while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+                    it = s_it;
+                    if (t > 0) {
+                        it.tiles = 0;
+                        while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+                    }
                     if (nitem >= items) {  // (the rows have changed under the kernel)
                         ok = false;
                         break;
@@ -405,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 if (batch != at >> 2) {
                     if (done != 7) look(at >> 2, 7 & ~done);
                     batch = at >> 2;
-                    b_r = n_r, b_row = n_row, b_ks = n_ks, b_vs = n_vs, done = 0;
+                    b_r = n_r, b_row = n_row, fresh = true, done = 0;
                 } else if ((batch + 1) * 4 < it.tiles) {
                     const int todo = ((2 << (at & 3)) / 2 - 1) & ~done;  // one more step at tiles 1, 2 and 3
                     look(batch + 1, todo);
@@ -552,8 +564,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // O of the segment that ended with tile t - 1, and its output or partial state.
         auto epilogue = [&] {
             const int tl = t - 1;
-            const bool w_ok = wait(&obar[tl & 1], (uint32_t)((tl >> 1) & 1));
-            tc::fence_after_sync();
             float(&rd)[4][H + 1] = red[2];
             int hidx = 0;
             float l[H];
@@ -561,6 +571,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             for (int h = 0; h < H; ++h) l[h] = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
             const float sum = fold<H, 16>(l, lane, &hidx, Add{});
             if ((lane & (32 / H - 1)) == 0) rd[warp][hidx] = sum;
+            const bool w_ok = wait(&obar[tl & 1], (uint32_t)((tl >> 1) & 1));
+            tc::fence_after_sync();
             if (!w_ok) give_up();
             if (group_or(1, kSoft, !w_ok || *reinterpret_cast<volatile int*>(&s_fail) != 0)) {
                 failed = true;
@@ -605,8 +617,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 
         int segs = 0, nitem = item0, off = off0;
         for (int left = run; left > 0;) {
-            it.tiles = 0;
-            while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+            it = s_it;
+            if (t > 0) {
+                it.tiles = 0;
+                while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+            }
             if (nitem >= items) {
                 give_up();
                 failed = true;
