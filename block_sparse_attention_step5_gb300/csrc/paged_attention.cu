@@ -133,12 +133,9 @@ struct __align__(16) Meta {
     uint32_t loaded;  // 1: a copy brings its codes
 };
 
-// Dim d of head h of row n's group g, gated and rounded.
-template <int H>
-__device__ __forceinline__ void write_out(const PagedAttnParams& p, int n, int g, int h, int d, float v) {
-    const int64_t at = (int64_t)n * p.Hq + (int64_t)g * H + h;
-    if (p.gate != nullptr) v *= 1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at])));
-    p.out[at * 128 + d] = f32_to_bf16_bits(v);
+// The output v of a (row, head), number `at` of them, through its gate.
+__device__ __forceinline__ float gated(const PagedAttnParams& p, int64_t at, float v) {
+    return v * (1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at]))));
 }
 
 template <class S>
@@ -238,8 +235,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         if (part >= 0 && part < parts) {
             s_item = tid;
             s_it = own;
-            s_off = (int)((int64_t)mine * part / parts);
-            s_run = (int)((int64_t)mine * (part + 1) / parts) - s_off;
+            const uint32_t each = mine / (uint32_t)parts, more = mine % (uint32_t)parts;  // (the first ones take one more)
+            s_off = (int)((uint32_t)part * each + min((uint32_t)part, more));
+            s_run = (int)(each + ((uint32_t)part < more ? 1u : 0u));
             s_first = first;
             s_last = first + parts - 1;
             if (part == 0) p.shared_items[tid] = make_int4(0, 0, 0, -1);  // (again below if it has several parts)
@@ -592,20 +590,29 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 for (int h = 0; h < H; ++h)
                     o[h] = a[h] + (a[H + h] + (H == 8 ? b[h] : a[(2 * H + h) & 15]) * (1.0f / kPart)) * (1.0f / kPart);
             }
-            float* st = p.states + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState;
+            float L[H];
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                const float L = (rd[0][h] + rd[1][h]) + (rd[2][h] + rd[3][h]);
-                const float v = L == 0.0f ? 0.0f : o[h] * __fdividef(vref * (1.0f / kPTop), L);
-                if (whole) {
-                    write_out<H>(p, done.n, done.g, h, key, v);
-                } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
-                    if (key == 0) {
+                L[h] = (rd[0][h] + rd[1][h]) + (rd[2][h] + rd[3][h]);
+                o[h] = L[h] == 0.0f ? 0.0f : o[h] * __fdividef(vref * (1.0f / kPTop), L[h]);
+            }
+            if (whole) {
+                const int64_t at = (int64_t)done.n * p.Hq + (int64_t)done.g * H;
+                if (p.gate != nullptr)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) o[h] = gated(p, at + h, o[h]);
+#pragma unroll
+                for (int h = 0; h < H; ++h) p.out[(at + h) * 128 + key] = f32_to_bf16_bits(o[h]);
+            } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
+                float* st = p.states + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState;
+#pragma unroll
+                for (int h = 0; h < H; ++h) st[2 * H + h * 128 + key] = o[h];
+                if (key == 0)
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
                         st[h] = -(h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x);
-                        st[H + h] = L;
+                        st[H + h] = L[h];
                     }
-                    st[2 * H + h * 128 + key] = v;
-                }
             }
             if (!whole && begins && tid == 0) {
                 if (few)
@@ -699,25 +706,24 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                         break;
                     }
                     float ratio = 1.0f;
-                    const float v = fmaxf(fmaxf(rd[0][H], rd[1][H]), fmaxf(rd[2][H], rd[3][H]));
+                    const float old = vref, v = fmaxf(fmaxf(rd[0][H], rd[1][H]), fmaxf(rd[2][H], rd[3][H]));
                     if (v > vref) {
                         const uint32_t u = __float_as_uint(v);
                         const float next = __uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u));
-                        ratio = vref / next;
                         vref = next;
-                        vinv = 1.0f / next;
+                        vinv = __uint_as_float(0x7f000000u - __float_as_uint(next));  // (exact: next is 2^-126 .. 2^126)
+                        ratio = old * vinv;
                     }
 #pragma unroll
                     for (int h = 0; h < H; ++h) {
                         const float tmax = fmaxf(fmaxf(rd[0][h], rd[1][h]), fmaxf(rd[2][h], rd[3][h]));
                         float& neg = h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x;
                         float& l = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
-                        alpha[h] = 1.0f;
-                        if (tmax > kSlack - neg || (neg == INFINITY && tmax > -INFINITY)) {
-                            alpha[h] = ex2(-neg - tmax);
-                            neg = -tmax;
-                            l *= alpha[h];
-                        }
+                        const bool moves = tmax > kSlack - neg || (neg == INFINITY && tmax > -INFINITY);
+                        const float a = ex2(-neg - tmax);
+                        alpha[h] = moves ? a : 1.0f;
+                        neg = moves ? -tmax : neg;
+                        l *= alpha[h];
                     }
 #pragma unroll
                     for (int h = 0; h < H; h += 2)
@@ -845,7 +851,10 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
             o += so[x][d];
             w += sl[x];
         }
-        write_out<S::H>(p, item.x, item.y, c, d, w == 0.0f ? 0.0f : o / w);
+        const int64_t at = (int64_t)item.x * p.Hq + (int64_t)item.y * S::H + c;
+        o = w == 0.0f ? 0.0f : o / w;
+        if (p.gate != nullptr) o = gated(p, at, o);
+        p.out[at * 128 + d] = f32_to_bf16_bits(o);
     }
 }
 
