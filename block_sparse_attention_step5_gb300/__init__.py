@@ -558,7 +558,7 @@ def step5_paged_workspace_bytes(geom) -> int:
 
 @dataclass
 class PagedWorkspace:
-    """Device workspace of the attention calls over e4m3 pages, zeroed once on creation."""
+    """Device workspace of the attention calls over e4m3 pages (it may hold anything)."""
     tensor: torch.Tensor
 
     @classmethod
@@ -566,10 +566,7 @@ class PagedWorkspace:
         nbytes = step5_paged_workspace_bytes(geom)
         if nbytes == 0:
             raise Step5Error("step5_paged_workspace_bytes", 2, "unsupported geometry")
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        with torch.cuda.device(t.device):
-            step5_workspace_init(t)
-        return cls(t)
+        return cls(torch.empty(nbytes, dtype=torch.uint8, device=device))
 
 
 def _raise_for(what: str, t, dtype, shape, dev: int):

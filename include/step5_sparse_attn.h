@@ -417,7 +417,7 @@ step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* page
  * requantised: e4m3(code * held / s).  Tokens behind t1 are taken as absent (a position
  * may be written again after tokens were rolled back; the scale then shrinks only when the
  * region's first token is written).  Infinities saturate, NaN stays NaN; neither moves the scale
- * past 2^120.  A scale held that is not finite and positive is ignored (STEP5_DEV_RANGE).
+ * past 2^120.  A scale held that is not positive or above 2^126 is ignored (STEP5_DEV_RANGE).
  * The rows of one sequence must stand together in a call, at consecutive ascending
  * positions (a chunk, or one decode row); a row that follows one of its own sequence at
  * any other position sets STEP5_DEV_RANGE, and neither its k and v are written nor those of
@@ -435,18 +435,21 @@ step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages*
  *   keys  = tokens max(0, p - window + 1) .. p  (window 0: 0 .. p)
  *   out[n][h] = sigmoid(gate[n][h]) * softmax(softmax_scale * q[n][h] . K^T) V
  * with K and V the values code * scale, every score, weight and sum in fp32 (a weight times
- * its V scale meets V's codes with 12 significant bits, or within 2^-24 of the row's largest weight
- * times the largest V scale), one rounding to bf16; the factor is 1 with gate NULL
+ * its V scale meets V's codes with 11 significant bits or more, or within 2^-24 of the row's largest
+ * weight times the largest V scale; q meets K's codes exactly, or within 2^-17 of the head's
+ * largest value), one rounding to bf16; the factor is 1 with gate NULL
  * (gate [N][num_q_heads] bf16 logits).  q, out: [N][num_q_heads][head_dim] bf16.  Tokens
  * outside a row's keys never reach its result, whatever their codes, scales and table entries hold (a
  * region that a row sees in part has one scale).  A region of the keys whose table entry
- * or scale is bad (a scale must be finite and positive) is left out and sets
+ * or scale is bad (a scale must be positive and at most 2^126) is left out and sets
  * STEP5_DEV_RANGE; a row without keys, or out of range, gets zeros; a padding row's output
- * is left as it was.  N <= 65535.  Any order of rows; rows of one sequence that stand
- * together share its keys.
- * workspace: step5_paged_workspace_bytes(geom) bytes, 16-byte aligned, zeroed once
- * (step5_workspace_init); any number of calls with geometries of no more query heads per
- * group may use it one after another, captured or not, but not two at once. */
+ * is left as it was.  N <= 65535.  Any order of rows.
+ * With N >= 2 B the rows of a sequence that stand together (within 128 / heads of a group x 2 of
+ * them) share its keys' tiles; below, every row reads its keys on its own.  So for a prompt
+ * chunk of few sequences out of a large table pass those sequences' rows of the table, B of them.
+ * workspace: step5_paged_workspace_bytes(geom) bytes, 16-byte aligned, holding anything
+ * (nothing is kept in it from call to call); any number of calls may use it one after
+ * another, captured or not, but not two at once. */
 step5_status step5_paged_attn_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                                    int32_t window, const void* q_bf16, const uint8_t* k_pages_e4m3,
                                    const uint8_t* v_pages_e4m3, const float* k_scales_f32, const float* v_scales_f32,

@@ -120,15 +120,15 @@ def terms(w, codes, scales):
 
 def tolerance(out, mass):
     """One bf16 rounding of the result is off by at most 2^-8 of it.  Before it, a weight is
-    off by at most 2^-11 of itself: 2^-12 for its rounding to the 12 bits that meet V, and
+    off by at most 3 * 2^-12 of itself: 2^-11 for its rounding to the 11 bits (f16) that meet V, and
     2^-12 for its score (128 products and the exponential in fp32: scores of the tests stay below 2^6,
     an fp32 sum of 128 terms is off by less than 2^-17 of the terms' magnitudes, which are below 2^5)
     and the sums.  Small weights have a floor: they are held, times vscale over a power of two above
     every vscale and times 2^5, in three e4m3 parts 2^5 apart, the last in steps of 2^-9 at the finest,
     so a weight (against the row's largest) times its vscale is off by up to half a step,
     2^-10 * 2^-10 * 2^-5 = 2^-25 of that power of two, which is at most twice the largest vscale:
-    sum_t 2^-24 max scale |code_t| = 2^-11 of the second of terms()."""
-    return 2.0 ** -8 * out.abs() + 2.0 ** -11 * mass + 1e-30
+    sum_t 2^-24 max scale |code_t| = 2^-11 of the second of terms(), below 3 * 2^-12 of it."""
+    return 2.0 ** -8 * out.abs() + 3 * 2.0 ** -12 * mass + 1e-30
 
 
 def off(got, out, mass) -> float:

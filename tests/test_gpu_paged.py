@@ -194,6 +194,24 @@ def test_append_refuses_rows_on_the_device(s5):
     assert bool((kc[1, :, 5] != 9).any()) and bool((kc[1, :, 2] == 9).all())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_rotates_q_in_place(s5, e4m3):
+    geom = geometry(s5, 2, 8)
+    gen = torch.Generator().manual_seed(61)
+    q, k, v = (normal(gen, 33, h, 128).cuda() for h in (16, 2, 2))
+    cos, sin, seq, pos = dev(*S.rope_tables(64, 96), *rows_of((0, 5, 33)))
+    table = torch.arange(8, dtype=torch.int32, device="cuda").view(1, 8)
+    call = s5.step5_kv_append_e4m3 if e4m3 else s5.step5_kv_append
+    caches = [s5.PagedCache.create(geom, 8, 8, table, e4m3=e4m3) for _ in range(2)]
+    out = torch.empty_like(q)
+    call(geom, k, v, caches[0], seq, pos, cos, sin, q, out)
+    same = q.clone()
+    call(geom, k, v, caches[1], seq, pos, cos, sin, same, same)
+    assert status(s5) == 0
+    assert torch.equal(same, out) and not torch.equal(out, q)
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+
+
 def test_append_bf16_fills_the_contiguous_caches(s5):
     """Without a table the bf16 append fills the caches that step5_sparse_attn reads: tokens
     appended one chunk at a time give the same output as caches filled by hand."""
@@ -529,6 +547,82 @@ def test_attention_is_deterministic_and_replays(s5):
     for (g, out, _), a in zip(graphs, first):
         assert torch.equal(out, a)
     assert status(s5) == 0
+
+
+@pytest.mark.parametrize("runs", [[(0, 900, 1)], [(0, 60000, 1)], [(0, 100, 1), (1, 200, 1)], [(0, 700, 70), (1, 3, 40)], [(0, 3000, 33)]])
+def test_buffers_of_the_smallest_alignment(s5, runs):
+    """q and out at addresses that are multiples of 16 bytes and no more give the same bits."""
+    c = Case(s5, runs, 2, 8, 16, seed=51)
+    base = c.run()
+    n = base.numel()
+    q, out = (torch.zeros(n + 64, dtype=torch.bfloat16, device="cuda") for _ in "qo")
+    for at in (8, 24):
+        qv, ov = (x[at:at + n].view(base.shape) for x in (q, out))
+        assert qv.data_ptr() % 32 == 16 and ov.data_ptr() % 32 == 16
+        qv.copy_(c.q)
+        out.zero_()
+        s5.step5_paged_attn_e4m3(c.geom, qv, c.cache(), *dev(c.seq, c.pos), ov, c.ws)
+        assert status(s5) == 0
+        assert torch.equal(ov, base)
+        assert bool((out[:at] == 0).all()) and bool((out[at + n:] == 0).all())
+
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("G, hq", [(1, 4), (2, 16)])
+def test_drafts_of_long_rows(s5, G, hq, window):
+    """A few rows of each of several sequences, long and short ones, one of them padding."""
+    Case(s5, [(0, 9001, 4), (1, 130, 5), (-1, 0, 1), (2, 4092, 8), (3, 0, 2)], G, hq, 16, seed=52).check(window)
+
+
+def test_nan_in_a_block_of_two_sequences(s5):
+    """A NaN that one sequence's rows see leaves the rows of the other in their block alone."""
+    runs = [(0, 256, 9), (1, 200, 9)]
+    c = Case(s5, runs, 1, 8, 16, seed=53)
+    base = c.run().cpu()
+    for tok, first in ((10, 0), (260, 4)):  # seen by every row of the sequence; by rows from the fifth on
+        c = Case(s5, runs, 1, 8, 16, seed=53)
+        page, slot = R.place(c.table, 0, tok, 16)
+        c.v[page, 0, slot, 77] = 0xff
+        got = c.run().cpu()
+        assert status(s5) == 0
+        sees = torch.zeros(got.shape, dtype=torch.bool)
+        sees[first:9, :, 77] = True
+        assert bool(torch.isnan(got[sees]).all())
+        assert torch.equal(got[~sees], base[~sees])
+
+
+def test_two_streams_at_once(s5):
+    """Calls on two streams, each with its own workspace, none waiting for the other."""
+    cases = [Case(s5, [(0, 30000, 1)], 2, 8, 16, seed=54), Case(s5, [(0, 1000, 300)], 2, 8, 16, seed=55),
+             Case(s5, [(0, 4300, 200)], 2, 8, 16, seed=56).pick(), Case(s5, [(b, 3000, 1) for b in range(9)], 2, 8, 16, seed=57)]
+    args = [(c, c.cache(), dev(c.q, c.seq, c.pos, c.ids, c.cnt)) for c in cases]
+    first = [c.run(cache=m) for c, m, _ in args]
+    outs = [[torch.empty_like(f) for f in first] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [s5.PagedWorkspace.create(cases[0].geom) for _ in range(2)]
+    torch.cuda.synchronize()
+    for turn in range(4):
+        for i, (st, ws) in enumerate(zip(streams, spaces)):
+            for j in range(len(args)):
+                j = (j + i) % len(args)
+                c, m, (q, seq, pos, ids, cnt) = args[j]
+                if ids is None:
+                    s5.step5_paged_attn_e4m3(c.geom, q, m, seq, pos, outs[i][j], ws, stream=st)
+                else:
+                    s5.step5_sparse_attn_e4m3(c.geom, q, m, seq, pos, ids, cnt, outs[i][j], ws, stream=st)
+    assert status(s5) == 0
+    for got in outs:
+        for a, b in zip(got, first):
+            assert torch.equal(a, b)
+
+
+def test_workspace_needs_no_initialisation(s5):
+    """A workspace full of anything gives the same bits."""
+    for c in (Case(s5, [(0, 5000, 1), (1, 3, 1)], seed=58), Case(s5, [(0, 2000, 40)], seed=59), Case(s5, [(0, 5000, 3)], seed=60).pick()):
+        base = c.run()
+        c.ws.tensor.fill_(0xff)
+        assert torch.equal(c.run(), base)
+        assert status(s5) == 0
 
 
 # ------------------------------------------------------------------------------ together
