@@ -1,20 +1,21 @@
-// kv_append.cu -- the rows' keys and values into the paged cache (bf16, or e4m3 with a scale
-// for each region and KV group), with NEOX rotation of k (and of q) on the way.
+// kv_append.cu -- the rows' keys and values into the paged cache (bf16, or e4m3 with a scale for each
+// region and KV group), with NEOX rotation of k (and of q) on the way.
 //
-// Rotation is the indexer's (x1 c - x2 s, x2 c + x1 s over pairs (i, i + rot / 2) from bf16
-// cos/sin, the exact sum rounded once to bf16).  A head vector is sixteen 16-byte chunks and eight
-// lanes: since rot / 2 is a multiple of 8, a lane takes both chunks of its eight pairs (or two that are only
-// copied), so nothing is exchanged between lanes and every access is 16 bytes.  The kernel moves bytes: bound by HBM for
-// chunks (2,048 rows of 40 heads in bf16, 42 MB), by the latency of its three dependent loads for a decode row.
+// Rotation is the indexer's (x1 c - x2 s, x2 c + x1 s over pairs (i, i + rot / 2) from bf16 cos/sin,
+// the exact sum rounded once to bf16).  A head vector is sixteen 16-byte chunks and eight lanes:
+// since rot / 2 is a multiple of 8, a lane takes both chunks of its eight pairs (or two that are only
+// copied), so nothing is exchanged between lanes and every access is 16 bytes.  The kernel moves
+// bytes: bound by HBM for chunks (2,048 rows of 40 heads in bf16, 42 MB), by the latency of its three
+// dependent loads for a decode row.
 //
-// In e4m3 a region's eight tokens share a scale, so one warp (four tokens of eight lanes, twice) takes all of the
-// call's tokens of a region for one (group, k or v), from the first of them on (the leader: a row on a
-// region's first token, or one that does not continue the row before):
+// In e4m3 a region's eight tokens share a scale, so one warp (four tokens of eight lanes, twice)
+// takes all of the call's tokens of a region for one (group, k or v), from the first of them on (the
+// leader: a row on a region's first token, or one that does not continue the row before):
 //   s = max(the scale held, if the region holds earlier tokens; the smallest power of two
 //           >= max |x| / 448; 2^-126),      code = e4m3(x / s).
-// A power of two divides exactly, costs an e4m3 value no precision (it has an exponent of its
-// own), and makes the rescaling of tokens already held exact unless they leave the normal range.
-// Those are requantised only when a new token raises the scale.
+// A power of two divides exactly, costs an e4m3 value no precision (it has an exponent of its own),
+// and makes the rescaling of tokens already held exact unless they leave the normal range. Those are
+// requantised only when a new token raises the scale.
 #include "paged.cuh"
 
 namespace step5 {
@@ -29,12 +30,13 @@ struct Chunks {
     uint4 a, b;
 };
 
-// First chunk of lane l8 of a vector whose first 2 * half8 chunks are rotated, and the distance to its second.
+// First chunk of lane l8 of a vector whose first 2 * half8 chunks are rotated, and the distance to
+// its second.
 __device__ __forceinline__ int first_chunk(int l8, int half8) { return l8 < half8 ? l8 : 2 * l8; }
 __device__ __forceinline__ int second_chunk(int l8, int half8) { return l8 < half8 ? l8 + half8 : 2 * l8 + 1; }
 
-// x c + y s, products exact in fp32, rounded to odd: of the two fp32 numbers around the exact sum the one with an odd
-// last bit.  Its rounding to bf16 (16 bits shorter) is the exact sum's.
+// x c + y s, products exact in fp32, rounded to odd: of the two fp32 numbers around the exact sum the
+// one with an odd last bit.  Its rounding to bf16 (16 bits shorter) is the exact sum's.
 __device__ __forceinline__ float odd_sum(float x, float c, float y, float s) {
     const float xc = __fmul_rn(x, c), down = __fmaf_rd(y, s, xc), up = __fmaf_ru(y, s, xc);
     return (__float_as_uint(down) & 1u) ? down : up;
@@ -54,7 +56,8 @@ __device__ __forceinline__ void rotate(Chunks& x, const uint4& c, const uint4& s
                      rotate2(o.b.z, o.a.z, c.z, s.z, false), rotate2(o.b.w, o.a.w, c.w, s.w, false));
 }
 
-// The largest finite |bf16| of two packed ones, as bits (NaN left out, infinity taken as the largest finite value).
+// The largest finite |bf16| of two packed ones, as bits (NaN left out, infinity taken as the largest
+// finite value).
 __device__ __forceinline__ uint32_t amax2(uint32_t w) {
     const uint32_t a = w & 0x7fffu, b = (w >> 16) & 0x7fffu;
     return min(max(a <= 0x7f80u ? a : 0u, b <= 0x7f80u ? b : 0u), 0x7f7fu);
@@ -89,8 +92,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
     return r;
 }
 
-// Row vectors: q's heads, and in bf16 k's and v's too.  Four vectors of the row to a warp at a time, two times
-// in flight: q, k and v are asked for before the row's position is known.
+// Row vectors: q's heads, and in bf16 k's and v's too.  Four vectors of the row to a warp at a time,
+// two times in flight: q, k and v are asked for before the row's position is known.
 template <bool E4M3>
 __device__ __forceinline__ void append_row(const AppendParams& p, uint32_t id, int lane) {
     const int n = (int)(id >> p.row_shift), part = (int)(id & ((1u << p.row_shift) - 1)), l8 = lane & 7;
@@ -249,10 +252,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendPara
 
 cudaError_t launch_append(const AppendParams& params, bool e4m3, cudaStream_t stream, bool pdl) {
     AppendParams p = params;
-    // Warps to a row's vectors: 4 when the rows fill the GPU (each then takes two or three vectors a lane), 16 for few
-    // rows, whose latency counts.  Rows a region warp looks over for leaders: 8 in long chunks, one of which leads.
+    // Warps to a row's vectors: 4 when the rows fill the GPU (each then takes two or three vectors a
+    // lane; 2,048 rows in bf16 10.7 us against 15.1 with 16), 16 for few rows, whose latency counts (one
+    // row 2.2 us against 2.9 with 4).  Rows a region warp looks over for leaders: 8 in chunks, one of
+    // which leads (4 x 1,021 rows 16.3 us against 26.8 with 1), one in decode batches, where every row
+    // leads (16 rows 2.9 us against 13 with 8, 1,024 rows 9.5 against 17.3).
     p.row_shift = p.N >= 512 ? 2 : 4;
-    p.rows_per_warp = p.N >= 512 ? 8 : 1;
+    p.rows_per_warp = p.N >= 512 && p.N >= 8 * (int64_t)p.B ? 8 : 1;
     p.region_warps = e4m3 ? (uint32_t)((p.N + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.G) : 0u;
     const uint32_t warps = p.region_warps + (e4m3 && p.q == nullptr ? 0u : (uint32_t)p.N << p.row_shift);
     cudaLaunchConfig_t cfg = {};
