@@ -1,33 +1,45 @@
-// paged_attention.cu -- attention over the e4m3 paged cache on the tcgen05 tensor cores: every
-// token of a causal window, or the picked regions plus the row's own.
+// paged_attention.cu -- attention over the e4m3 paged cache on the tcgen05 tensor cores: every token
+// of a causal window, or the picked regions plus the row's own.
 //
 //   s_t = softmax_scale (q . kcode_t) kscale(region of t),  p = softmax(s),  out = sum_t p_t vscale vcode_t
 //
-// The codes go to the tensor cores as they lie in the cache (kind::f8f6f4), so nothing is
-// converted on the way and a key costs half the bytes of bf16.  The other operand of each product is then e4m3
-// too, which has 4 significant bits; q and p are therefore split into parts, each the e4m3 rounding of
-// what the parts before it left, times 2^5: two parts hold a bf16 q (8 bits) exactly down to 2^-22 of the
-// head's largest value, three hold a weight to 12 bits, down to 2^-24 of the largest.  The parts are
-// more columns of the small side of the product, which costs nothing at few heads: 128 keys are the M side,
+// The codes go to the tensor cores as they lie in the cache (kind::f8f6f4), so nothing is converted
+// on the way and a key costs half the bytes of bf16.  The other operand of each product is then e4m3
+// too, which has 4 significant bits; q and p are therefore split into parts, each the e4m3 rounding
+// of what the parts before it left, times 2^5: two parts hold a bf16 q (8 bits) exactly down to 2^-22
+// of the head's largest value, three hold the 11 bits of a weight in f16, down to 2^-24 of the
+// largest.  The parts are more columns of the small side of the product, which costs nothing at few
+// heads: 128 keys are the M side,
 //
 //   S^T [128 keys x 2 H]  = K_tile [128 x 128 dims]       . (q parts)^T     (two TMEM buffers)
 //   O^T [128 dims x 3 H] += V_tile^T [128 dims x 128 keys] . (p parts)^T
 //
-// with H query heads of one row.  A region (8 tokens x 128 B) is one
-// 128-byte-swizzle atom: K-major A for the first product, MN-major A for the second, from one TMA
-// box (pages whose length allows it come in boxes of up to 16 regions).
+// with H query heads of one row.  A region (8 tokens x 128 B) is one 128-byte-swizzle atom: K-major A
+// for the first product, MN-major A for the second, from one TMA box (pages whose length allows it
+// come in boxes of up to 16 regions).
 //
 // Scales.  kscale multiplies the fp32 score.  vscale joins the weight before it is split, relative to
-// a power of two not below any vscale so far, so that the parts' range is spent on what a key adds to the
-// output; the row sum takes the weight without it.
+// a power of two not below any vscale so far, so that the parts' range is spent on what a key adds to
+// the output; the row sum takes the weight without it.
 //
-// Work.  An item is a (row, group).  Few items are cut into equal parts, many have their tiles laid end to end
-// and cut into equal runs, so that a ragged batch, one long row and a chunk of many rows all fill the GPU; a second
-// kernel joins the items that CTAs share, in CTA order (the bits do not depend on timing).
+// Work.  An item is a (row, group).  Few items are cut into equal parts, many have their tiles laid
+// end to end and cut into equal runs, so that a ragged batch, one long row and a chunk of many rows
+// all fill the GPU; a second kernel joins the items that CTAs share, in CTA order (the bits do not
+// depend on timing).
 //
-// Roles in a CTA: four softmax warps (one thread per key of the tile), a warp for each of the two
-// products, and two that look entries up (region, pool row, scales, four tiles ahead in steps) and issue the
-// copies, K a tile ahead of V, and leave what the softmax needs of each region in a small ring.
+// A CTA: four softmax warps (a key to a thread), a warp for each product (so that neither waits for
+// what the other waits for), two warps that look the regions up (page, scales) a few tiles ahead and
+// issue the copies, K a tile ahead of V, and leave what the softmax needs of each region in a small
+// ring.
+//
+// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens, join included:
+//   one row of 1M tokens        160 us  1.08 GB, 6.73 TB/s: the copy bandwidth of HBM
+//   16 rows of 16K to 32K        68 us  404 MB, 6.0 TB/s: HBM, and the last CTA's tail
+//   one row of 4,608 tokens     9.3 us  latency: split 2, page, scale and key loads 2, one tile 1,
+//                                       second product and states 1.3, launch and join 3
+//   16 rows of 512 picks       23.7 us  the copies alone 22.3 (68 MB in boxes of 1 KB)
+//   2,048 rows of 512 picks   1,130 us  the copies alone 934: 8.6 GB in boxes of 1 KB out of L2,
+//                                       one in 32 cycles on each SM
 #include "paged_device.cuh"
 
 namespace step5 {
@@ -43,9 +55,10 @@ constexpr uint32_t kSlotBytes = kTile * 1024;
 constexpr float kSlack = 3.0f;       // log2 units a tile's maximum may pass the running one by
 constexpr float kPTop = 32.0f;       // weights are split from p * 2^(8 - slack): at most 2^8, whose parts fit e4m3
 
-// MANY: for launches of many items, three CTAs an SM with few slots, which hide one another's latency (2,048 rows
-// of 512 picks: 1,171 us against 1,411 with two); for few items two CTAs with more copies in flight and fewer states to
-// join (16 rows of 512 picks: 31 us against 36).
+// MANY: for launches of many items, three CTAs an SM with few slots, which hide one another's latency
+// (2,048 rows of 512 picks: 1,130 us against 1,380 with two, 256 rows 157 against 185); for few items
+// two CTAs with more copies in flight and fewer states to join (one row of 512 picks: 9.5 us against
+// 10.2 with three; 16 rows 23.7 against 23.4).
 template <int H_, bool PICKS_, bool MANY_>
 struct Shape {
     static constexpr int H = H_;                       // query heads of a group
@@ -167,8 +180,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     if (tid == 0) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
-        // a slot's two readers are different warps, so a copy's arrival is told by tile, not by slot: a warp
-        // that waited by slot would miss every other phase of it (tile t + 4 is not copied before tile t is used)
+        // a slot's two readers are different warps, so a copy's arrival is told by tile, not by slot:
+        // a warp that waited by slot would miss every other phase of it (tile t + 4 is not copied
+        // before tile t is used)
         for (int s = 0; s < 4; ++s) {
             mbar_init(&kfull[s], kLoadWarps);
             mbar_init(&vfull[s], kLoadWarps);
@@ -194,9 +208,9 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     int64_t start = 0, per = 1;  // (many items: the run's first tile among all, tiles of a run)
     const bool few = 2 * items <= (int)gridDim.x;
     if (few) {
-        // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the smallest L of 32 tried that needs
-        // no more CTAs than there are (2 L0 always does).  No CTA then has parts of two items.
-        // (fewer than 2^8 items of at most 2^24 tiles)
+        // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the
+        // smallest L of 32 tried that needs no more CTAs than there are (2 L0 always does).  No CTA
+        // then has parts of two items. (fewer than 2^8 items of at most 2^24 tiles)
         Item own{};
         if (tid < items) own = item_at<PICKS>(p, tid);
         const uint32_t mine = (uint32_t)own.tiles;
@@ -295,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // nothing to do
     } else if (warp >= kLoadWarp) {
         // ---------------- load warps: K_0, K_1, V_0, K_2, V_1, ... over the run's tiles, each into
-        // the next slot once the product that read it is done.  Warp lw takes entries 8 lw .. 8 lw + 7 of a tile.
+        // the next slot once the product that read it is done.  Warp lw takes entries 8 lw .. 8 lw +
+        // 7 of a tile.
         const int lw = warp - kLoadWarp;
         const int k = p.box_regions;  // (a box of 16 regions is the first warp's)
         const int q = lw * 8 + (lane & 7);                // this lane's entry
@@ -305,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         Item it{};
         int nitem = item0, at = 0;       // next item, this one's tile
         int left = run, in_seg = 0;      // tiles of the run, of the segment, not yet walked
-        // Lane l looks up its entry in tile l / 8 of four tiles, in three steps (region; pool row; scales), the
-        // next four while these go by.
+        // Lane l looks up its entry in tile l / 8 of four tiles, in three steps (region; pool row;
+        // scales), the next four while these go by.
         int b_r = 0, b_row = -1, n_r = 0, n_row = -1, batch = -1, done = 0;
         float b_ks = 0.0f, b_vs = 0.0f, n_ks = 0.0f, n_vs = 0.0f;
         bool fresh = false;  // n_ks, n_vs are the batch's
@@ -365,8 +380,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             __syncwarp();
             if (row >= 0) tma_load_2d(dst + q * 1024, isv ? &vmap : &kmap, full, 0, row);
             if (!isv) {
-                // (this slot was free, so the softmax is past tile t - 5 and the ring's entry is free too; the copies are on
-                // their way while the scales of a segment's first tile come)
+                // (this slot was free, so the softmax is past tile t - 5 and the ring's entry is free
+                // too; the copies are on their way while the scales of a segment's first tile come)
                 if (fresh) b_ks = n_ks, b_vs = n_vs, fresh = false;
                 if (lane >> 3 == (at & 3)) {
                     const int t0 = b_r * 8;
@@ -458,8 +473,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             const int j = qk ? (t == 0 ? 0 : 2 * t - 1) : (t + 1 < run ? 2 * t + 2 : 2 * t + 1), slot = j % S::kSlots;
             if (!wait(qk ? &kfull[t & 3] : &vfull[t & 3], (uint32_t)((t >> 2) & 1))) ok = false;
             const int note = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_note[t & (kRing - 1)]), 0);
-            // First product: tile t - 2 is through (its S has been read, and its P, which the softmax of tile t
-            // overwrites); q of a segment's first tile is there.  Second: P_t is there.
+            // First product: tile t - 2 is through (its S has been read, and its P, which the softmax
+            // of tile t overwrites); q of a segment's first tile is there.  Second: P_t is there.
             if (qk) {
                 if (t >= 2 && !wait(&obar[t & 1], (uint32_t)(((t - 2) >> 1) & 1))) ok = false;
                 if ((note & 256) && !wait(&qbar, (uint32_t)(seg++ & 1))) ok = false;
@@ -668,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 tc::fence_after_sync();
                 const Meta me = ring[t & (kRing - 1)][q];
                 const bool sees = (me.mask >> (key & 7) & 1u) != 0;
-                // s[h] = q . kcode kscale; its logit in log2 units is s[h] cq[h], y[h] that less the running maximum
+                // s[h] = q . kcode kscale; its logit in log2 units is s[h] cq[h], y[h] that less the
+                // running maximum
                 float2 s[H / 2], y[H / 2];
                 const uint32_t sb = lanes + (uint32_t)(S::NS * (t & 1));
                 {
@@ -688,7 +704,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     top = fmaxf(top, fmaxf(y[h / 2].x, y[h / 2].y));
                 }
                 // The running maxima move when a key passes one by more than the slack, vref when a
-                // vscale passes it; l and O are rescaled then.  Every softmax thread takes the same steps.
+                // vscale passes it; l and O are rescaled then.  Every softmax thread takes the same
+                // steps.
                 if (!w_ok) give_up();
                 if (__builtin_expect(group_or(1, kSoft, (sees && (top > kSlack || me.vs > vref)) || !w_ok), 0)) {
                     if (*reinterpret_cast<volatile int*>(&s_fail) != 0) failed = true;
@@ -751,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 for (int h = 0; h < H; h += 2) {
                     const float2 w = make_float2(ex2(y[h / 2].x), ex2(y[h / 2].y));
                     l_part[h / 2] = add2(l_part[h / 2], w);
-                    // f16 keeps 11 bits of a weight (half a step is 2^-12 of it), the parts all of them
+                    // f16 keeps 11 bits of a weight (half a step is at most 2^-11 of it), the parts
+                    // all of them
                     __half2 x = __float22half2_rn(mul2(w, vf));
                     const uint32_t a = next_part(x), b = next_part(x), c = last_part(x);
                     if (h % 4 == 0)
@@ -771,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 } else {
                     *reinterpret_cast<uint4*>(pb) = make_uint4(part[0][0], part[1][0], part[2][0], 0u);
                 }
-                // a copied V row that the row does not see is zeroed: the cache may hold anything there, and
-                // a zero weight must meet a finite value
+                // a copied V row that the row does not see is zeroed: the cache may hold anything
+                // there, and a zero weight must meet a finite value
                 if (__builtin_expect(me.loaded && !sees, 0)) {
                     const int slot = (t + 1 < run ? 2 * t + 2 : 2 * t + 1) % S::kSlots;
                     w_ok &= wait(&vfull[t & 3], (uint32_t)((t >> 2) & 1));
@@ -795,11 +813,12 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     if (warp == 0) tc::dealloc(tmem, S::kCols);
 }
 
-// Joins the items that CTAs of the launch before shared: a block per (entry of shared_items, head), its threads'
-// groups of 128 dims taking every GROUPS-th state, eight of them asked for before the weights are known
-// (the states lie in L2; the join is latency, not bandwidth).  The sums run in an order fixed by the CTAs.
-// Eight groups for few blocks, two for many (1 row of 4,608 tokens: 11.3 us in all against 13.1; 16 rows of 512 picks: 30.6
-// against 25.5).
+// Joins the items that CTAs of the launch before shared: a block per (entry of shared_items, head),
+// its threads' groups of 128 dims taking every GROUPS-th state, eight of them asked for before the
+// weights are known (the states lie in L2; the join is latency, not bandwidth).  The sums run in an
+// order fixed by the CTAs.
+// Eight groups for few blocks, two for many (one row of 4,608 tokens: 9.3 us in all against 11.4 with
+// two; 16 rows of 512 picks: 23.7 against 28.8 with eight).
 template <class S, int GROUPS>
 __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
     __shared__ float sw[kPagedMaxCtas], sm[GROUPS * 4], so[GROUPS][128], sl[GROUPS];

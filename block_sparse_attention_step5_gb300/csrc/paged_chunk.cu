@@ -1,28 +1,39 @@
-// paged_chunk.cu -- attention over the e4m3 paged cache for launches whose sequences have several rows
-// (prompt chunks, drafts): the rows of a sequence share its keys.
+// paged_chunk.cu -- attention over the e4m3 paged cache for launches whose sequences have several
+// rows (prompt chunks, drafts): the rows of a sequence share its keys.
 //
 //   s_t = softmax_scale (q . kcode_t) kscale(region of t),  p = softmax(s),  out = sum_t p_t vscale vcode_t
 //
-// A CTA takes two tiles of 128 head rows (128 / HQ consecutive rows of the call, HQ query heads each) against 128
-// keys at a time:
+// A CTA takes two tiles of 128 head rows (128 / HQ consecutive rows of the call, HQ query heads each)
+// against 128 keys at a time:
 //
 //   S [128 head rows x 128 keys]  = q_hi . K^T + q_lo . K^T   (kind::f8f6f4, K's codes as they lie in the cache)
 //   O [128 head rows x 128 dims] += P . V                     (kind::f16, P from tensor memory)
 //
-// With head rows on the M side a softmax thread owns a row: its maximum, sum and rescaling need no other thread.
-// q is two e4m3 numbers, hi + lo (lo the rounding of what hi leaves: exact for values above 2^-10 of the
-// head's largest, off by 2^-18 of that below), which share an accumulator.  V's codes are turned into f16 (exact) by
-// four warps, once for both row tiles, and P is f16 (11 bits), so that weights keep 2^-12 and a range of 2^-33: e4m3
-// parts of P would cost more here, where P is as large as S.  One tile of rows and keys is 512 cycles of
-// tensor core in either product (an e4m3 product runs twice as fast as f16 and is done twice), which bounds the
-// kernel while the softmax of one row tile runs under the products of the other.
+// With head rows on the M side a softmax thread owns a row: its maximum, sum and rescaling need no
+// other thread.  q is two e4m3 numbers, hi + lo (lo the rounding of what hi leaves: exact for values
+// above 2^-9 of the head's largest, off by at most 2^-17 of that below), which share an accumulator.
+// V's codes are turned into f16 (exact) by four warps, once for both row tiles, and P is f16 (11
+// bits), so that weights keep 2^-11 and a range of 2^-33: e4m3 parts of P would cost more here, where
+// P is as large as S.  One tile of rows and keys is 512 cycles of tensor core in either product (an
+// e4m3 product runs twice as fast as f16 and is done twice), which would bound the kernel with the
+// softmax of one row tile under the products of the other.
 //
-// Scales.  kscale goes into the factor of the exponent, eight keys at a time; vscale joins the weight, relative to a
-// power of two not below any vscale so far; the row sum takes the weight without it.
+// Scales.  kscale goes into the factor of the exponent, eight keys at a time; vscale joins the
+// weight, relative to a power of two not below any vscale so far; the row sum takes the weight
+// without it.
 //
-// Work.  As in the kernel for single rows, the tiles of all (block of rows, group) items are laid end to end and each
-// CTA takes an equal run; a second kernel joins the items that CTAs share.  A block's rows may belong to several sequences: its
-// tiles are those of each sequence in turn, with the other rows masked.
+// Work.  As in the kernel for single rows, the tiles of all (block of rows, group) items are laid end
+// to end and each CTA takes an equal run; a second kernel joins the items that CTAs share.  A block's
+// rows may belong to several sequences: its tiles are those of each sequence in turn, with the other
+// rows masked.
+//
+// What it takes, with 4 KV groups of 8 heads and pages of 64 tokens, join included:
+//   2,048 rows behind 2,048 tokens    135 us  1.03e11 flop (at 1,899 TFLOP/s: 54 us)
+//   2,048 rows, window of 512 tokens   59 us  1.7e10 flop (9 us)
+// A tile of keys takes its two row tiles 2.5 us: maximum 1,050, weights 1,400, the products and the
+// waits around them 2,200 cycles (1,024 of tensor core; the first product alone reads shared memory
+// at its full rate, which the copies and V's conversion share).  Around the tiles: start 4 us, q 3 us
+// and epilogue 2 us for each part of an item, join 3 us.
 #include <type_traits>
 
 #include "paged_device.cuh"
@@ -242,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
 
-    // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups.
+    // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the
+    // tiles of all groups.
     int64_t of_group, total, per, start;
     {
         int* tiles = reinterpret_cast<int*>(smem);  // (nothing is copied yet)
@@ -298,8 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int run = (int)(start < total ? min(per, total - start) : 0);
     const int blk0 = s_blk, off0 = s_off, g0 = run ? (int)(start / of_group) : 0;
 
-    // Every role walks the run's segments alike: item (group, block), tiles off .. off + n - 1 of it.  next()
-    // returns false when there is none (the rows have changed under the kernel).
+    // Every role walks the run's segments alike: item (group, block), tiles off .. off + n - 1 of it.
+    // next() returns false when there is none (the rows have changed under the kernel).
     struct Segment {
         int g, blk, off, n, nt;
     };
@@ -457,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ---------------- products, of the row tiles in turn: P V of a tile, then Q K of the next, whose S takes P's
-        // place (products of one thread run in order).  Behind a segment's last tile q changes: both P V go first.
+        // place (products of one thread run in order).  Behind a segment's last tile q changes: both
+        // P V go first.
         const uint32_t k_addr = smem_u32(k8), v_addr = smem_u32(v16), q_addr = smem_u32(qs);
         bool ok = true;
         int segs = 0;
@@ -527,8 +540,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kConvWarp) {
         // ---------------- V's codes to f16: a key to a thread.  In a tile of which some row does not see some key, NaN codes
-        // become zero (the cache may hold anything there, and a zero weight must meet a finite value), noted for the rows that see
-        // them.
+        // become zero (the cache may hold anything there, and a zero weight must meet a finite
+        // value), noted for the rows that see them.
         const int cw = warp - kConvWarp, key = cw * 32 + lane;
         int segs = 0;
         for (int t = 0; t < run; ++t) {
@@ -619,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int t = 0, segs = 0;
         bool ok = true;
 
-        // The warp's 32 head rows, eight lanes of 16 dims to each; the next eight rows are on their way meanwhile.
+        // The warp's 32 head rows, eight lanes of 16 dims to each; the next eight rows are on their
+        // way meanwhile.
         auto build_q = [&] {
             const int l8 = lane & 7, hr0 = (warp & 3) * 32 + (lane >> 3);
             const uint32_t rows_ok = __ballot_sync(0xffffffffu, row.b >= 0);
@@ -772,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     vref = up;
                     vinv = 1.0f / up;
                 }
-                // the columns that the row sees, unless every row sees all: from .. to - 1, of readable regions
+                // the columns that the row sees, unless every row sees all: from .. to - 1, of
+                // readable regions
                 const bool all = (tl.note & 4u) != 0;
                 int from = 0, to = 0;
                 if (!all && row.b >= 0 && (tl.rows >> j & 1u)) {
@@ -786,8 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t under = from - c >= 32 ? ~0u : (1u << max(from - c, 0)) - 1u;
                     return below & ~under & ((okr * 0x00204081u & 0x01010101u) * 0xffu);
                 };
-                // the row's largest logit in the tile (in log2 units); the running maximum follows it when it is passed by more
-                // than the slack, which rescales l and O
+                // the row's largest logit in the tile (in log2 units); the running maximum follows it
+                // when it is passed by more than the slack, which rescales l and O
                 float mx = -INFINITY;
                 uint32_t x[32];  // columns of S
                 auto largest = [&](int c, const uint32_t(&x)[32], auto edge) {
@@ -804,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mx = fmaxf(mx, m8 * tl.ks[c / 8 + g]);  // (ks > 0 where the region is readable; -inf * 0 is no maximum)
                     }
                 };
-                // (loops, not unrolled further: straight code for a whole tile ran 20 % slower, short of instructions)
+                // (loops, not unrolled further: straight code for a whole tile ran 20 % slower, short
+                // of instructions)
                 auto all_largest = [&](auto edge) {
 #pragma unroll 1
                     for (int c = 0; c < 128; c += 32) {
@@ -913,6 +929,63 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
     write_out8<S>(p, item.x, item.y, hr, d8 * 8, o);
 }
 
+// The same for few items, each shared by many CTAs (one sequence's 16 rows behind 8,192 tokens: 39 CTAs an
+// item, 31 us in all against 40).  First the states' weights, 32 threads to a row; then two groups of 256
+// threads take every other state each, eight of them asked for at a time.
+template <class S>
+__global__ void __launch_bounds__(512) join_wide_kernel(PagedAttnParams p) {
+    constexpr int kMore = kChunkMaxCtas / 32;
+    __shared__ float sw[kChunkMaxCtas][16], part[32][16], so[256][8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = blockIdx.x, tid = threadIdx.x;
+    const int4 item = p.shared_items[first];
+    if (item.w < 0) return;
+    const int n = item.w - first + 1;
+    auto state = [&](int i) { return p.states + ((int64_t)2 * (first + i) + (i == 0 ? 1 : 0)) * kStateFloats; };
+    {
+        const int row = tid & 15, hr = blockIdx.y * 16 + row, i0 = tid >> 4;
+        float2 ml[kMore];
+        float M = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kMore; ++x) {
+            ml[x] = i0 + 32 * x < n ? *reinterpret_cast<const float2*>(state(i0 + 32 * x) + 2 * hr) : make_float2(0.0f, 0.0f);
+            if (ml[x].y != 0.0f) M = fmaxf(M, ml[x].x);
+        }
+        part[i0][row] = M;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) M = fmaxf(M, part[x][row]);
+#pragma unroll
+        for (int x = 0; x < kMore; ++x)
+            if (i0 + 32 * x < n) sw[i0 + 32 * x][row] = ml[x].y == 0.0f ? 0.0f : ex2(ml[x].x - M) * ml[x].y;
+        __syncthreads();
+    }
+    const int grp = tid >> 8, at = tid & 255, row = (at >> 7) * 8 + (at & 7), d8 = (at >> 3) & 15, hr = blockIdx.y * 16 + row;
+    float w = 0.0f, o[8] = {};
+#pragma unroll 8
+    for (int i = grp; i < n; i += 2) {
+        const float4* v = reinterpret_cast<const float4*>(state(i) + 512 + d8 * 2048 + hr * 8);
+        const float4 a = v[0], b = v[1];
+        const float f = sw[i][row], x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        w += f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[d] = fmaf(f, x[d], o[d]);
+    }
+    if (grp == 1) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) so[at][d] = o[d];
+        if (d8 == 0) part[0][row] = w;
+    }
+    __syncthreads();
+    const int r = item.x + hr / S::HQ;
+    if (grp == 1 || r >= p.N || p.row_seq[r] == -1) return;
+    w += part[0][row];
+#pragma unroll
+    for (int d = 0; d < 8; ++d) o[d] = w == 0.0f ? 0.0f : (o[d] + so[at][d]) / w;
+    write_out8<S>(p, item.x, item.y, hr, d8 * 8, o);
+}
+
 template <int HQ>
 cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
                          cudaStream_t stream, bool pdl) {
@@ -935,8 +1008,13 @@ cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     e = cudaLaunchKernelEx(&cfg, paged_chunk_kernel<S>, kmap, vmap, p);
     if (e != cudaSuccess) return e;
     cfg.gridDim.y = 256 / 16;
-    cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
+    // at least 8 CTAs an item on average, or fewer (2,048 rows on 2K: 135 us against 149 with the wide one)
+    if ((int64_t)((p.N + S::NB - 1) / S::NB) * p.G * 8 <= num_sms) {
+        cfg.blockDim = dim3(512);
+        return cudaLaunchKernelEx(&cfg, join_wide_kernel<S>, p);
+    }
+    cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, join_chunk_kernel<S>, p);
 }
 

@@ -1,5 +1,5 @@
-// paged_device.cuh -- what the attention kernels over the e4m3 paged cache share: bounded waits, single-lane
-// issue, paired fp32 arithmetic, and the splitting of values into e4m3 parts.
+// paged_device.cuh -- what the attention kernels over the e4m3 paged cache share: bounded waits,
+// single-lane issue, paired fp32 arithmetic, and the splitting of values into e4m3 parts.
 #pragma once
 
 #include "paged.cuh"

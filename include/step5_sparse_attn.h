@@ -444,9 +444,9 @@ step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages*
  * or scale is bad (a scale must be positive and at most 2^126) is left out and sets
  * STEP5_DEV_RANGE; a row without keys, or out of range, gets zeros; a padding row's output
  * is left as it was.  N <= 65535.  Any order of rows.
- * With N >= 2 B the rows of a sequence that stand together (within 128 / heads of a group x 2 of
- * them) share its keys' tiles; below, every row reads its keys on its own.  So for a prompt
- * chunk of few sequences out of a large table pass those sequences' rows of the table, B of them.
+ * From N * num_q_heads / G >= max(128, 64 B) on, neighbouring rows of a sequence share its keys'
+ * tiles; below, every row reads its keys on its own.  So for a prompt chunk of few sequences
+ * out of a large table pass those sequences' rows of the table, B of them.
  * workspace: step5_paged_workspace_bytes(geom) bytes, 16-byte aligned, holding anything
  * (nothing is kept in it from call to call); any number of calls may use it one after
  * another, captured or not, but not two at once. */

@@ -574,6 +574,21 @@ def test_drafts_of_long_rows(s5, G, hq, window):
     Case(s5, [(0, 9001, 4), (1, 130, 5), (-1, 0, 1), (2, 4092, 8), (3, 0, 2)], G, hq, 16, seed=52).check(window)
 
 
+@pytest.mark.parametrize("G, hq, n", [(1, 4, 130), (2, 8, 70), (1, 16, 37)])
+@pytest.mark.parametrize("window", [0, 40])
+def test_scattered_rows_that_share_tiles(s5, G, hq, n, window):
+    """Many rows of two sequences in any order, some twice, some of them padding."""
+    gen = torch.Generator().manual_seed(n)
+    runs = [(int(b), int(p), 1) for b, p in zip(torch.randint(-1, 2, (n,), generator=gen), torch.randint(0, 700, (n,), generator=gen))]
+    Case(s5, runs + [runs[0]] + [(1, 699, 1), (0, 0, 1)], G, hq, 16, seed=n).check(window)
+
+
+@pytest.mark.parametrize("G, hq, runs", [(1, 8, [(0, 20000, 16)]), (2, 16, [(0, 9000, 9), (1, 40, 9)]), (1, 4, [(0, 40000, 33)]),
+                                         (4, 8, [(0, 2500, 33), (1, 5, 40)])])
+def test_few_rows_shared_by_many_ctas(s5, G, hq, runs):
+    Case(s5, runs, G, hq, 64, seed=len(runs) + hq).check()
+
+
 def test_nan_in_a_block_of_two_sequences(s5):
     """A NaN that one sequence's rows see leaves the rows of the other in their block alone."""
     runs = [(0, 256, 9), (1, 200, 9)]
