@@ -534,6 +534,7 @@ class PagedCache:
         if not all(t is None or t.is_contiguous() for t in (k, v, block_table, k_scales, v_scales)):
             raise ValueError("the cache's tensors must be contiguous")
         # the C calls' arguments, which stay the same as long as the tensors do
+        self._index = k.device.index if k.is_cuda else -1
         self._pages = ctypes.byref(self.pages)
         self._pools = tuple(None if t is None else t.data_ptr()
                             for t in ((k, v, k_scales, v_scales) if self.e4m3 else (k, v)) + (block_table,))
@@ -584,21 +585,25 @@ def _raise_for(what: str, t, dtype, shape, dev: int):
 
 def _arg(what: str, t, dtype, shape, dev: int) -> int:
     """Address of a dense tensor of this type and shape on the current device."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != dtype or t.shape != shape or \
-            not t.is_contiguous():
-        _raise_for(what, t, dtype, shape, dev)
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _raise_for(what, t, dtype, shape, dev)
 
 
 def _rows(what: str, t, heads: int, dim: int, dev: int, N: int):
     """Address and row stride of a bf16 [N][heads][dim] tensor whose rows may lie apart."""
     shape = (N, heads, dim)
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype != torch.bfloat16 or t.shape != shape:
-        _raise_for(what, t, torch.bfloat16, shape, dev)
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != dim):
-        _raise_for(what, t, torch.bfloat16, shape, dev)
-    return t.data_ptr(), (s[0] if N > 1 else heads * dim)
+    try:
+        if t.dtype is torch.bfloat16 and t.shape == shape and t.get_device() == dev:
+            row, head, one = t.stride()
+            if one == 1 and (head == dim or heads == 1):
+                return t.data_ptr(), (row if N > 1 else heads * dim)
+    except AttributeError:
+        pass
+    _raise_for(what, t, torch.bfloat16, shape, dev)
 
 
 # the current stream's handle without a Stream object around it (1 us of a 7 us call), where torch offers that
@@ -608,7 +613,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _device_and_stream(cache: "PagedCache", geom, stream):
     """Current device and the stream's handle, after checking that the cache is there and fits the geometry."""
     dev = torch.cuda.current_device()
-    if cache.device.type != "cuda" or cache.device.index != dev:
+    if cache._index != dev:
         raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{dev}")
     if cache.groups != geom.num_kv_groups or cache.head_dim != geom.head_dim:
         raise ValueError("the cache's groups and head dim are not the geometry's")
@@ -622,21 +627,24 @@ def _kv_append(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, row_
     dev, st = _device_and_stream(cache, g, stream)
     if cache.e4m3 != e4m3:
         raise ValueError(f"{fn} does not write this kind of pool")
-    N, G, Hq, D = k.shape[0], g.num_kv_groups, g.num_q_heads, g.head_dim
+    G, D, N = cache.groups, cache.head_dim, k.shape[0]
     kp, ks = _rows("k", k, G, D, dev, N)
     vp, vs = _rows("v", v, G, D, dev, N)
     qp, qs, qo = None, 0, None
     if q is not None or q_out is not None:
+        Hq = g.num_q_heads
         qp, qs = _rows("q", q, Hq, D, dev, N)
         qo = _arg("q_out", q_out, torch.bfloat16, (N, Hq, D), dev)
     cp, sp, t_cap, half = None, None, 1, 0
     if cos is not None or sin is not None:
-        cp = _arg("cos", cos, torch.bfloat16, cos.shape if isinstance(cos, torch.Tensor) and cos.dim() == 2 else (), dev)
-        sp = _arg("sin", sin, torch.bfloat16, cos.shape, dev)
-        t_cap, half = cos.shape
+        table = cos.shape if isinstance(cos, torch.Tensor) and cos.dim() == 2 else ()
+        cp = _arg("cos", cos, torch.bfloat16, table, dev)
+        sp = _arg("sin", sin, torch.bfloat16, table, dev)
+        t_cap, half = table
+    rows = (N,)
     st = getattr(load(), fn)(g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
-                             _arg("row_seq", row_seq, torch.int32, (N,), dev),
-                             _arg("row_pos", row_pos, torch.int32, (N,), dev), cp, sp, qo, *cache._pools, st)
+                             _arg("row_seq", row_seq, torch.int32, rows, dev),
+                             _arg("row_pos", row_pos, torch.int32, rows, dev), cp, sp, qo, *cache._pools, st)
     if st:
         raise Step5Error(fn, st)
 
