@@ -606,13 +606,15 @@ def _rows(what: str, t, heads: int, dim: int, dev: int, N: int):
     _raise_for(what, t, torch.bfloat16, shape, dev)
 
 
-# the current stream's handle without a Stream object around it (1 us of a 7 us call), where torch offers that
+# the current stream's handle without a Stream object around it (1 us of a 7 us call), and the current device without
+# looking whether CUDA is up (a tensor of the cache is there), where torch offers that
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _device_and_stream(cache: "PagedCache", geom, stream):
     """Current device and the stream's handle, after checking that the cache is there and fits the geometry."""
-    dev = torch.cuda.current_device()
+    dev = _current_device() if cache._index >= 0 else torch.cuda.current_device()
     if cache._index != dev:
         raise ValueError(f"the cache is on {cache.device}, the current device is cuda:{dev}")
     if cache.groups != geom.num_kv_groups or cache.head_dim != geom.head_dim:
