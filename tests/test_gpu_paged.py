@@ -631,6 +631,46 @@ def test_two_streams_at_once(s5):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("runs, picks", [([(0, 1001, 1), (1, 70, 1)], False), ([(0, 300, 70)], False), ([(0, 1001, 2)], True)])
+def test_attention_over_pools_past_32_bit_offsets(s5, runs, picks):
+    """The same pages at the end of pools of more than 2^31 bytes give the same bits."""
+    c = Case(s5, runs, 4, 8, 64, seed=62)
+    if picks:
+        c.pick()
+    base = c.run()
+    pages = 2 ** 31 // (4 * 64 * 128) + 50
+    first = pages - c.k.shape[0]
+    pools = []
+    for small in (c.k, c.v, c.ks, c.vs):
+        big = torch.full((pages, *small.shape[1:]), 0x7f if small.dtype == torch.uint8 else float("nan"), dtype=small.dtype, device="cuda")
+        big[first:] = small.cuda()
+        pools.append(big)
+    k, v, ks, vs = pools
+    got = c.run(cache=s5.PagedCache(k, v, (c.table + first).cuda(), ks, vs))
+    assert status(s5) == 0
+    assert torch.equal(got, base)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_append_to_pools_past_32_bit_offsets(s5, e4m3):
+    geom = geometry(s5, 4, 8)
+    gen = torch.Generator().manual_seed(63)
+    k, v = (normal(gen, 100, 4, 128).cuda() for _ in "kv")
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    seq, pos = dev(*rows_of((0, 60, 100)))
+    call = s5.step5_kv_append_e4m3 if e4m3 else s5.step5_kv_append
+    pages = 2 ** 31 // (4 * 64 * 128) + 50
+    small = s5.PagedCache.create(geom, 3, 64, table, e4m3=e4m3)
+    big = s5.PagedCache.create(geom, pages, 64, table + (pages - 3), e4m3=e4m3)
+    for cache in (small, big):
+        call(geom, k, v, cache, seq, pos)
+    assert status(s5) == 0
+    for name in ("k", "v") + (("k_scales", "v_scales") if e4m3 else ()):
+        x = getattr(big, name)
+        assert torch.equal(x[-3:], getattr(small, name)), name
+        assert bool((x[:-3] == (1 if "scales" in name else 0)).all()), name
+
+
 def test_workspace_needs_no_initialisation(s5):
     """A workspace full of anything gives the same bits."""
     for c in (Case(s5, [(0, 5000, 1), (1, 3, 1)], seed=58), Case(s5, [(0, 2000, 40)], seed=59), Case(s5, [(0, 5000, 3)], seed=60).pick()):
