@@ -54,6 +54,9 @@ constexpr uint32_t kIdescQk = tc::instr_desc(tc::kFmtE4M3, false, false, 128, 12
 constexpr uint32_t kIdescPv = tc::instr_desc(tc::kFmtF16, false, true, 128, 128);
 constexpr float kSlack = 6.0f;                  // log2 units a weight may lie above the running maximum
 constexpr float kPTop = 256.0f;                 // P = p 2^8 vscale / vref <= 2^14
+// vref is at least this, so that kPTop / vref is finite: a weight times the smallest vscale, 2^-126, is then P itself, whose finest
+// step is 2^-24
+constexpr float kVrefMin = 0x1p-118f;
 constexpr int kStateFloats = 256 * 130;         // of a partial state: (m, l) of each head row, o as [16][256 head rows][8 dims]
 
 template <int HQ_>
@@ -781,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Tile& tl = ring[t & (kRing - 1)];
                 if (__builtin_expect(tl.vmax > vref, 0)) {  // (the same for every thread)
                     const uint32_t u = __float_as_uint(tl.vmax);
-                    const float up = __uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u));
+                    const float up = fmaxf(__uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u)), kVrefMin);
                     if (i > 0) rescale(vref / up);
                     vref = up;
                     vinv = 1.0f / up;

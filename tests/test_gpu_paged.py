@@ -606,6 +606,31 @@ def test_nan_in_a_block_of_two_sequences(s5):
         assert torch.equal(got[~sees], base[~sees])
 
 
+def zero_values(c, toks):
+    """V of tokens toks (whole regions) as appending zeros leaves it: codes 0, the smallest scale."""
+    for tok in toks[::8]:
+        page, slot = R.place(c.table, 0, tok, c.k.shape[2])
+        c.v[page, :, slot:slot + 8] = 0
+        c.vs[page, :, slot // 8] = 2.0 ** -126
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("runs", [[(0, 300, 40)], [(0, 339, 1)]])
+def test_regions_whose_values_are_zero(s5, runs, window):
+    """V of zeros, which has the smallest scale: in the first tiles of a row's keys, in all of them, and beside a region
+    that cannot be read."""
+    for until in (128, 240):
+        c = Case(s5, runs, 2, 8, 16, seed=71)
+        zero_values(c, range(0, until))
+        c.check(window)
+    c = Case(s5, runs, 2, 8, 16, seed=71)
+    zero_values(c, range(0, 352))
+    assert bool((c.run(window) == 0).all()) and status(s5) == 0
+    page, slot = R.place(c.table, 0, 168, 16)
+    c.ks[page, :, slot // 8] = float("inf")
+    assert bool((c.run(window) == 0).all()) and status(s5) == s5.DEV_RANGE
+
+
 def test_two_streams_at_once(s5):
     """Calls on two streams, each with its own workspace, none waiting for the other."""
     cases = [Case(s5, [(0, 30000, 1)], 2, 8, 16, seed=54), Case(s5, [(0, 1000, 300)], 2, 8, 16, seed=55),
