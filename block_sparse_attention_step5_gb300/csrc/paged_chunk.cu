@@ -177,7 +177,7 @@ struct Tile {
     uint32_t ok;         // regions that can be read and hold keys
     int t0;              // first token
     int lo, hi;          // the pass's first and last token
-    uint32_t note;       // 1: the segment's first tile, 2: its last, 4: every row of the block sees every key
+    uint32_t note;       // 1: the segment's first tile, 2: its last, 4: every row of the block but padding sees every key
     float vmax;          // largest vscale of the ok regions
     int n0;              // first row of the block
 };
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) {
                     const int t0 = (w.r0 + w.at * kTile) * 8;
-                    const bool all = oks == 0xffffu && w.rows == w.valid && t0 >= w.max_lo && t0 + 127 <= w.min_hi;
+                    const bool all = oks == 0xffffu && w.rows == w.valid && w.bad == 0 && t0 >= w.max_lo && t0 + 127 <= w.min_hi;
                     tl.rows = w.rows;
                     tl.ok = oks;
                     tl.t0 = t0;

@@ -631,6 +631,30 @@ def test_regions_whose_values_are_zero(s5, runs, window):
     assert bool((c.run(window) == 0).all()) and status(s5) == s5.DEV_RANGE
 
 
+@pytest.mark.parametrize("B, n", [(1, 40), (40, 64)])
+@pytest.mark.parametrize("window", [0, 200])
+def test_bad_rows_in_a_block_of_good_ones(s5, B, n, window):
+    """Rows out of range between rows that see whole tiles get zeros, the others what they get beside
+    padding: items that many CTAs share (B 1), and whole ones (B 40)."""
+    c = Case(s5, [(b, 300, n) for b in range(B)], 2, 8, 16, seed=72)
+    bad = torch.zeros(c.N, dtype=torch.bool)
+    bad[17::29] = True
+    bad[-1] = True
+    seq, pos = c.seq.clone(), c.pos.clone()
+    c.seq[bad] = -1
+    want = c.run(window)
+    assert status(s5) == 0
+    assert bool((want[bad] == 5.0).all())
+    c.seq[:], c.pos[:] = seq, pos
+    c.seq[bad] = B
+    c.seq[17], c.pos[17] = seq[17], 16 * c.table.shape[1]
+    c.seq[-1], c.pos[-1] = seq[-1], -1
+    got = c.run(window)
+    assert status(s5) == s5.DEV_RANGE
+    assert bool((got[bad] == 0).all())
+    assert torch.equal(got[~bad], want[~bad])
+
+
 def test_two_streams_at_once(s5):
     """Calls on two streams, each with its own workspace, none waiting for the other."""
     cases = [Case(s5, [(0, 30000, 1)], 2, 8, 16, seed=54), Case(s5, [(0, 1000, 300)], 2, 8, 16, seed=55),
