@@ -19,8 +19,8 @@
 // softmax of one row tile under the products of the other.
 //
 // Scales.  kscale goes into the factor of the exponent, eight keys at a time; vscale joins the
-// weight, relative to a power of two not below any vscale so far; the row sum takes the weight
-// without it.
+// weight, relative to a power of two (vref) not below any vscale that the row has seen; the row sum
+// takes the weight without it.
 //
 // Work.  As in the kernel for single rows, the tiles of all (block of rows, group) items are laid end
 // to end and each CTA takes an equal run; a second kernel joins the items that CTAs share.  A block's
@@ -782,13 +782,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_after_sync();
                 const Tile& tl = ring[t & (kRing - 1)];
-                if (__builtin_expect(tl.vmax > vref, 0)) {  // (the same for every thread)
-                    const uint32_t u = __float_as_uint(tl.vmax);
-                    const float up = fmaxf(__uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u)), kVrefMin);
-                    if (i > 0) rescale(vref / up);
-                    vref = up;
-                    vinv = 1.0f / up;
-                }
                 // the columns that the row sees, unless every row sees all: from .. to - 1, of
                 // readable regions
                 const bool all = (tl.note & 4u) != 0;
@@ -837,15 +830,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                 else
                     all_largest(std::true_type{});
                 mx *= cq;
-                const bool up = mx > kSlack - neg_m || (neg_m == INFINITY && mx > -INFINITY);
-                if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {
-                    float alpha = 1.0f;
+                const bool up = mx > kSlack - neg_m || (neg_m == INFINITY && mx > -INFINITY), higher = tl.vmax > vref;
+                if (__builtin_expect(__any_sync(0xffffffffu, up || higher), 0)) {
+                    float f = 1.0f;
                     if (up) {
-                        alpha = ex2(-neg_m - mx);
-                        l *= alpha;
+                        f = ex2(-neg_m - mx);
+                        l *= f;
                         neg_m = -mx;
                     }
-                    if (i > 0) rescale(alpha);
+                    if (higher) {  // vref follows the largest vscale that the row itself sees
+                        float v = tl.vmax;
+                        if (!all) {
+                            const uint32_t regs = from < to ? (2u << ((to - 1) >> 3)) - (1u << (from >> 3)) : 0u;
+                            v = 0.0f;
+#pragma unroll 1
+                            for (uint32_t m = regs; m; m &= m - 1) v = fmaxf(v, tl.vs[__ffs(m) - 1]);  // (0 where it cannot be read)
+                        }
+                        if (v > vref) {
+                            const uint32_t u = __float_as_uint(v);
+                            const float p2 = fmaxf(__uint_as_float((u & 0x7f800000u) + ((u & 0x7fffffu) ? 0x800000u : 0u)), kVrefMin);
+                            f *= vref / p2;
+                            vref = p2;
+                            vinv = 1.0f / p2;
+                        }
+                    }
+                    if (i > 0 && __any_sync(0xffffffffu, f != 1.0f)) rescale(f);
                 }
                 // weights: P takes the first half of S's place, behind the columns already read
                 const float vtop = vinv * kPTop;
@@ -856,7 +865,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int reg = c / 8 + g;
-                        const float2 f = both(tl.ks[reg] * cq), vf = both(tl.vs[reg] * vtop), nm = both(neg_m);
+                        // (at most kPTop where the row sees the region; a weight of 0 must meet a finite factor)
+                        float vr = tl.vs[reg] * vtop;
+                        if constexpr (decltype(edge)::value) vr = fminf(vr, kPTop);
+                        const float2 f = both(tl.ks[reg] * cq), vf = both(vr), nm = both(neg_m);
 #pragma unroll
                         for (int d = 0; d < 8; d += 2) {
                             float2 y = fma2(make_float2(__uint_as_float(x[8 * g + d]), __uint_as_float(x[8 * g + d + 1])), f, nm);

@@ -655,6 +655,30 @@ def test_bad_rows_in_a_block_of_good_ones(s5, B, n, window):
     assert torch.equal(got[~bad], want[~bad])
 
 
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("big", [2.0 ** 30, 2.0 ** 110])
+def test_large_value_scales_of_unseen_regions(s5, window, big):
+    """The V scale of a later token's region, or of another sequence of the block, changes nothing in the
+    rows that do not see it."""
+    c = Case(s5, [(0, 130, 40)], 1, 8, 16, seed=73)
+    base = c.run(window)
+    page, slot = R.place(c.table, 0, 160, 16)
+    c.vs[page, :, slot // 8] = big
+    got = c.run(window)
+    assert torch.equal(got[:30], base[:30])
+    c.check(window)
+    for first in (0, 1):  # the sequence walked first, or second
+        runs = [(0, 256, 9), (1, 200, 9)]
+        c = Case(s5, runs, 1, 8, 16, seed=74)
+        base = c.run(window)
+        c.vs[c.table[first].long()] *= big
+        got = c.run(window)
+        assert status(s5) == 0
+        other = c.seq != first
+        assert torch.equal(got[other], base[other])
+        c.check(window)
+
+
 def test_two_streams_at_once(s5):
     """Calls on two streams, each with its own workspace, none waiting for the other."""
     cases = [Case(s5, [(0, 30000, 1)], 2, 8, 16, seed=54), Case(s5, [(0, 1000, 300)], 2, 8, 16, seed=55),
