@@ -505,39 +505,57 @@ class PagedCache:
     e4m3 codes with fp32 ``k_scales``, ``v_scales`` [num_pages][G][page_tokens / 8]) and the
     int32 ``block_table`` [B][table_len] of page numbers.  ``block_table`` None: sequence b owns
     page b, so that contiguous caches [B][G][t_cap][128] are a PagedCache as they are.  The
-    tensors belong to the caller, who may change the table's entries between calls; give a
-    table of another shape to a new PagedCache."""
+    tensors belong to the caller, who may change the table's entries between calls, or assign
+    another tensor to an attribute (checked again then); what follows from them is read-only."""
+
+    _TENSORS = ("k", "v", "block_table", "k_scales", "v_scales")
+    _FOLLOWS = ("e4m3", "B", "pages", "groups", "head_dim", "device", "_index", "_shape", "_pages", "_pools")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: Optional[torch.Tensor] = None,
                  k_scales: Optional[torch.Tensor] = None, v_scales: Optional[torch.Tensor] = None):
+        self._lay_out(k, v, block_table, k_scales, v_scales)
+
+    def __setattr__(self, name, value):
+        if name in self._TENSORS:
+            self._lay_out(*(value if n == name else getattr(self, n) for n in self._TENSORS))
+        elif name in self._FOLLOWS:
+            raise AttributeError(f"{name} of a PagedCache follows from its tensors")
+        else:
+            super().__setattr__(name, value)
+
+    def _lay_out(self, k, v, block_table, k_scales, v_scales):
+        """Checks the tensors, and lays out the C calls' arguments, which stay the same as long as the tensors do."""
         if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must be pools [num_pages][G][page_tokens][128] of one shape and type")
         if k.dtype not in (torch.bfloat16, torch.uint8):
             raise ValueError("pools are bf16 or e4m3 codes (uint8)")
-        self.e4m3 = k.dtype == torch.uint8
-        pages, groups, tokens, _ = k.shape
+        e4m3 = k.dtype == torch.uint8
+        pages, groups, tokens, head_dim = k.shape
         want = (pages, groups, tokens // 8)
         for s in (k_scales, v_scales):
-            if self.e4m3 != (s is not None):
+            if e4m3 != (s is not None):
                 raise ValueError("e4m3 pools come with k_scales and v_scales, bf16 pools without")
             if s is not None and (tuple(s.shape) != want or s.dtype != torch.float32):
                 raise ValueError(f"scales must be fp32 {want}")
         if block_table is not None and (block_table.dim() != 2 or block_table.dtype != torch.int32):
             raise ValueError("block_table must be int32 [B][table_len]")
-        self.k, self.v, self.block_table, self.k_scales, self.v_scales = k, v, block_table, k_scales, v_scales
-        self.B = pages if block_table is None else block_table.shape[0]
-        self.pages = Pages(pages, tokens, 1 if block_table is None else block_table.shape[1])
-        self.groups, self.head_dim, self.device = groups, k.shape[3], k.device
-        for t in (v, block_table, k_scales, v_scales):
+        tensors = (k, v, block_table, k_scales, v_scales)
+        for t in tensors:
             if t is not None and t.device != k.device:
                 raise ValueError(f"the cache's tensors are on {k.device} and {t.device}")
-        if not all(t is None or t.is_contiguous() for t in (k, v, block_table, k_scales, v_scales)):
+        if not all(t is None or t.is_contiguous() for t in tensors):
             raise ValueError("the cache's tensors must be contiguous")
-        # the C calls' arguments, which stay the same as long as the tensors do
-        self._index = k.device.index if k.is_cuda else -1
-        self._pages = ctypes.byref(self.pages)
-        self._pools = tuple(None if t is None else t.data_ptr()
-                            for t in ((k, v, k_scales, v_scales) if self.e4m3 else (k, v)) + (block_table,))
+        shape = Pages(pages, tokens, 1 if block_table is None else block_table.shape[1])
+        pools = (k, v, k_scales, v_scales, block_table) if e4m3 else (k, v, block_table)
+        self.__dict__.update(zip(self._TENSORS, tensors))
+        self.__dict__.update(e4m3=e4m3, B=pages if block_table is None else block_table.shape[0], groups=groups,
+                             head_dim=head_dim, device=k.device, _index=k.device.index if k.is_cuda else -1,
+                             _shape=shape, _pages=ctypes.byref(shape),
+                             _pools=tuple(None if t is None else t.data_ptr() for t in pools))
+
+    @property
+    def pages(self) -> Pages:
+        return Pages.from_buffer_copy(self._shape)
 
     @classmethod
     def create(cls, geom, num_pages: int, page_tokens: int, block_table: torch.Tensor, e4m3: bool = True,

@@ -679,6 +679,17 @@ def test_large_value_scales_of_unseen_regions(s5, window, big):
         c.check(window)
 
 
+def test_a_table_that_is_replaced(s5):
+    """The cache's next call reads the table assigned to it."""
+    c = Case(s5, [(0, 1001, 1), (1, 500, 1)], seed=75)
+    cache = c.cache()
+    c.table = c.table.flip(0).contiguous()
+    cache.block_table = c.table.cuda()
+    got = c.run(cache=cache).cpu()
+    assert status(s5) == 0
+    assert R.off(got, *c.want()) <= 1.0
+
+
 def test_two_streams_at_once(s5):
     """Calls on two streams, each with its own workspace, none waiting for the other."""
     cases = [Case(s5, [(0, 30000, 1)], 2, 8, 16, seed=54), Case(s5, [(0, 1000, 300)], 2, 8, 16, seed=55),

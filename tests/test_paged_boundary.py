@@ -108,6 +108,32 @@ def test_paged_cache_checks(s5):
             s5.PagedCache(*args)
 
 
+def test_paged_cache_follows_its_tensors(s5):
+    """An assigned tensor is checked and used from then on; a refused one changes nothing."""
+    u8, sc = torch.zeros((4, 2, 16, 128), dtype=torch.uint8), torch.ones((4, 2, 2))
+    tab = torch.zeros((1, 2), dtype=torch.int32)
+    tensors = dict(k=u8, v=u8.clone(), block_table=tab, k_scales=sc, v_scales=sc.clone())
+    cache = s5.PagedCache(**tensors)
+    order = ("k", "v", "k_scales", "v_scales", "block_table")
+    for name in order:
+        tensors[name] = tensors[name].clone()
+        setattr(cache, name, tensors[name])
+        assert getattr(cache, name) is tensors[name]
+        assert cache._pools == tuple(tensors[n].data_ptr() for n in order)
+    cache.block_table = tensors["block_table"] = torch.zeros((3, 5), dtype=torch.int32)
+    assert cache.B == 3 and cache.pages.table_len == 5
+    before = dict(cache.__dict__)
+    for name, bad in (("block_table", tab.long()), ("block_table", torch.zeros((2, 3), dtype=torch.int32).t()), ("k", u8[:2]), ("k", u8.bfloat16()),
+                      ("k_scales", None), ("v_scales", sc.double()), ("v", u8.transpose(0, 1))):
+        with pytest.raises(ValueError):
+            setattr(cache, name, bad)
+    for name in ("B", "pages", "e4m3", "groups", "head_dim", "device"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, 7)
+    cache.pages.num_pages = 1 << 20
+    assert cache.__dict__ == before and cache.pages.num_pages == 4
+
+
 def test_binding_refuses_cpu_tensors(s5):
     """No tensor of a call may lie elsewhere than on the current GPU."""
     g = s5.STEP5_GEOMETRY
