@@ -161,6 +161,22 @@ struct Walk {
         tiles = (regions + kTile - 1) / kTile;
         at = 0;
     }
+    // Whether some row of the pass sees a token of region r (of each lane its own): rows that lie apart leave gaps
+    // between their windows.
+    __device__ __forceinline__ bool sees(int r) const {
+        if (max_lo <= min_hi + 1) return r >= (lo >> 3) && r <= (hi >> 3);  // no gap: the rows' keys touch
+        bool any = false;
+        for (uint64_t m = rows; m; m &= m - 1) {
+            const int i = __ffsll((long long)m) - 1;
+            int l = __shfl_sync(0xffffffffu, mine[0].lo, i & 31), h = __shfl_sync(0xffffffffu, mine[0].pos, i & 31);
+            if (S::RL > 1 && i >= 32) {
+                l = __shfl_sync(0xffffffffu, mine[S::RL - 1].lo, i & 31);
+                h = __shfl_sync(0xffffffffu, mine[S::RL - 1].pos, i & 31);
+            }
+            any = any || (r >= (l >> 3) && r <= (h >> 3));
+        }
+        return any;
+    }
     __device__ __forceinline__ void skip(const PagedAttnParams& p, int n) {  // to n tiles further on
         while (n >= tiles - at && todo) {
             n -= tiles - at;
@@ -352,13 +368,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         Segment s{g0, blk0, off0, 0, 0};
         int left = run, seg_left = 0, issued_k = 0, issued_v = 0;
         int b_row = -1, n_row = -1, batch = -1, done = 0;
+        uint32_t b_seen = 0, n_seen = 0;  // lanes whose region some row sees
         float b_ks = 0.0f, b_vs = 0.0f, n_ks = 0.0f, n_vs = 0.0f;
         bool ok = true;
         auto look = [&](int of, int steps) {
-            const int e = (of * 2 + (lane >> 4)) * kTile + q, r = w.r0 + e;
+            const int r = w.r0 + (of * 2 + (lane >> 4)) * kTile + q;
             if (steps & 1) {
                 n_row = -1;
-                if (w.b >= 0 && e < (w.regions + k - 1) / k * k && (r | (k - 1)) >= (w.lo >> 3)) {
+                n_seen = __ballot_sync(0xffffffffu, w.sees(r));
+                if (n_seen >> (lane & ~(k - 1)) & ((1u << k) - 1u)) {  // (some region of its box)
                     n_row = (int)page_row(p.pages, p.G, w.b, s.g, r * 8);
                     if (n_row < 0) raise_status(p.status, kDevRange);
                 }
@@ -395,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (batch != w.at >> 1) {
                     if (done != 3) look(w.at >> 1, 3 & ~done);
                     batch = w.at >> 1;
-                    b_row = n_row, b_ks = n_ks, b_vs = n_vs, done = 0;
+                    b_row = n_row, b_seen = n_seen, b_ks = n_ks, b_vs = n_vs, done = 0;
                     if ((batch + 1) * 2 < w.tiles && (w.at & 1) == 0) {
                         look(batch + 1, 1);
                         done = 1;
@@ -407,8 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int from = (w.at & 1) * 16 + q;
                 nrow = __shfl_sync(0xffffffffu, b_row, from);
                 const float ks = __shfl_sync(0xffffffffu, b_ks, from), vs = __shfl_sync(0xffffffffu, b_vs, from);
-                const int r = w.r0 + w.at * kTile + q;
-                bool good = nrow >= 0 && r >= (w.lo >> 3) && r <= (w.hi >> 3);
+                bool good = nrow >= 0 && (b_seen >> from & 1u);
                 if (good && !(scale_ok(ks) && scale_ok(vs))) {
                     raise_status(p.status, kDevRange);
                     good = false;

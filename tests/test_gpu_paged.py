@@ -679,6 +679,30 @@ def test_large_value_scales_of_unseen_regions(s5, window, big):
         c.check(window)
 
 
+@pytest.mark.parametrize("hq, pt", [(4, 64), (8, 16), (16, 8)])
+def test_windows_of_rows_that_lie_apart(s5, hq, pt):
+    """What no row's window holds is not touched where the rows of a sequence that share tiles lie apart: freed
+    pages and bad scales there are no errors."""
+    c = Case(s5, [(0, 20, 20), (0, 900, 9), (0, 3, 1), (0, 2000, 30)], 1, hq, pt, seed=76)
+    base = c.run(16)
+    assert status(s5) == 0
+    seen = torch.zeros(c.table.shape[1] * pt, dtype=torch.bool)
+    for p in c.pos.tolist():
+        seen[max(0, p - 15):p + 1] = True
+    pages = seen.view(-1, pt).any(1)
+    regions = seen.view(-1, 8).any(1)
+    for r in (~regions).nonzero().flatten().tolist():
+        page, slot = R.place(c.table, 0, 8 * r, pt)
+        c.ks[page, :, slot // 8], c.vs[page, :, slot // 8] = float("nan"), -1.0
+    c.table[0, ~pages] = -7
+    got = c.run(16)
+    assert status(s5) == 0
+    assert torch.equal(got, base)
+    c.table[0, int(pages.nonzero()[-1])] = -7  # (and one that a row sees is)
+    c.run(16)
+    assert status(s5) == s5.DEV_RANGE
+
+
 def test_a_table_that_is_replaced(s5):
     """The cache's next call reads the table assigned to it."""
     c = Case(s5, [(0, 1001, 1), (1, 500, 1)], seed=75)
