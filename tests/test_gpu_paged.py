@@ -163,6 +163,39 @@ def test_append_e4m3_special_values(s5):
     assert torch.equal(R.decode(gk).nan_to_num(0.0), codes.nan_to_num(0.0))
 
 
+def test_append_e4m3_beside_scales_of_another_kind(s5):
+    """Scales held that are no powers of two: the new values divided by one, and the codes held multiplied by it,
+    are rounded once, ties and what lies next to them among them."""
+    ties = (17 + 2 * torch.arange(8)).double() / 16
+    geom, G = geometry(s5, 8, 4), 8
+    gen = torch.Generator().manual_seed(77)
+    table = torch.zeros((1, 1), dtype=torch.int32)
+    seq, pos = rows_of((0, 4, 4))
+    for grows in (False, True):
+        held = torch.empty(G)
+        x = normal(gen, 4, G, 128, scale=1.0)
+        codes = (torch.randn((1, G, 8, 128), generator=gen) * 8).to(torch.float8_e4m3fn)
+        for g in range(G):
+            if grows:  # held * code is next to a tie for codes of 9 / 8, 11 / 8, ...
+                code = torch.tensor([9, 11, 13, 15])[g % 4].double() / 8
+                held[g] = (ties[g] / code / 32).float()
+                codes[0, g, :4, :64] = code.to(torch.float8_e4m3fn)
+                x[0, g, 0] = 96.0  # (a scale of 1 / 4)
+            else:
+                held[g] = 1.75 * 2.0 ** -g if g < 4 else (2.0 ** -g / ties[g]).float()
+                x[:2, g, :8] = (held[g].double() * (ties if g < 4 else ties[g])).bfloat16()
+                x[:, g] = x[:, g].clamp(-float(held[g]) * 256, float(held[g]) * 256)
+        want, scales = codes.double(), held.double().view(1, G, 1).clone()
+        R.append_e4m3(x.double(), want, scales, table, seq, pos)
+        k, v = (codes.view(torch.uint8).clone().cuda() for _ in "kv")
+        ks, vs = (held.view(1, G, 1).clone().cuda() for _ in "kv")
+        s5.step5_kv_append_e4m3(geom, *dev(x, x), s5.PagedCache(k, v, table.cuda(), ks, vs), *dev(seq, pos))
+        assert status(s5) == 0
+        for c, sc in ((k, ks), (v, vs)):
+            assert torch.equal(sc.cpu().double(), scales)
+            assert torch.equal(R.decode(c), want)
+
+
 def test_append_refuses_rows_on_the_device(s5):
     """Rows out of range, out of order or without a page write nothing and raise the range flag."""
     geom = geometry(s5, 2, 4)
