@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kSeenWords = 1024;  // of a bit for each sequence
 
 // Two chunks (8 bf16 each) of a head vector.
 struct Chunks {
@@ -266,12 +267,34 @@ __device__ __forceinline__ void append_region(const AppendParams& p, int n, int 
     if (lane == 0) *scale_at = s;
 }
 
+// Two runs of one sequence in the call may meet in a region, whose warps do not know of each other: a
+// block looks the rows over for that beside the others' work (a bit for each sequence, 2^15 sequences at a time).
+__device__ __forceinline__ void check_runs(const AppendParams& p) {
+    __shared__ uint32_t seen[kSeenWords];
+    for (int64_t base = 0; base < p.B; base += kSeenWords * 32) {
+        const int here = (int)min((int64_t)kSeenWords * 32, p.B - base);
+        for (int i = threadIdx.x; i < (here + 31) / 32; i += kAppendThreads) seen[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int n = threadIdx.x; n < p.N; n += kAppendThreads) {
+            const int b = p.row_seq[n], before = n > 0 ? p.row_seq[n - 1] : -1;
+            const int64_t i = b - base;
+            if (b == before || i < 0 || i >= here) continue;
+            const uint32_t bit = 1u << (i & 31);
+            if (atomicOr(&seen[i >> 5], bit) & bit) raise_status(p.status, kDevRange);
+        }
+        __syncthreads();
+    }
+}
+
 template <bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(AppendParams p) {
     pdl_wait();
     pdl_launch_dependents();
+    if constexpr (E4M3)
+        if (blockIdx.x < p.check_blocks) return check_runs(p);
     const int lane = threadIdx.x & 31;
-    const uint32_t id = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const uint32_t id = (blockIdx.x - (E4M3 ? p.check_blocks : 0u)) * kAppendWarps + (threadIdx.x >> 5);
     if (!E4M3 || id >= p.region_warps) {
         append_row<E4M3>(p, E4M3 ? id - p.region_warps : id, lane);
         return;
@@ -313,7 +336,8 @@ cudaError_t launch_append(const AppendParams& params, bool e4m3, cudaStream_t st
     p.region_warps = e4m3 ? (uint32_t)((p.N + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.G) : 0u;
     const uint32_t warps = p.region_warps + (e4m3 && p.q == nullptr ? 0u : (uint32_t)p.N << p.row_shift);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((warps + kAppendWarps - 1) / kAppendWarps);
+    p.check_blocks = e4m3 && p.N > 1 ? 1u : 0u;
+    cfg.gridDim = dim3((warps + kAppendWarps - 1) / kAppendWarps + p.check_blocks);
     cfg.blockDim = dim3(kAppendThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

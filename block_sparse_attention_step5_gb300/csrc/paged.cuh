@@ -43,7 +43,7 @@ struct AppendParams {
     uint32_t* status;
     int N, B, G, Hq, rot, pos_cap;
     int row_shift, rows_per_warp;  // the launch's split of the work: N <= 2^24 keeps it in 32 bits
-    uint32_t region_warps;
+    uint32_t region_warps, check_blocks;
 };
 cudaError_t launch_append(const AppendParams& p, bool e4m3, cudaStream_t stream, bool pdl);
 

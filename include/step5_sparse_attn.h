@@ -421,7 +421,8 @@ step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* page
  * The rows of one sequence must stand together in a call, at consecutive ascending
  * positions (a chunk, or one decode row); a row that follows one of its own sequence at
  * any other position sets STEP5_DEV_RANGE, and neither its k and v are written nor those of
- * the rows behind it up to the next region. */
+ * the rows behind it up to the next region.  Rows of one sequence with others (or padding) between
+ * them set STEP5_DEV_RANGE too; the regions that such runs of it share then hold anything. */
 step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                                   int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
                                   const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,

@@ -227,6 +227,34 @@ def test_append_refuses_rows_on_the_device(s5):
     assert bool((kc[1, :, 5] != 9).any()) and bool((kc[1, :, 2] == 9).all())
 
 
+@pytest.mark.parametrize("B", [2, 40000])
+def test_append_e4m3_flags_sequences_that_are_split(s5, B):
+    """Rows of a sequence with others between them raise the range flag (here they share no region)."""
+    geom = geometry(s5, 1, 4)
+    table = torch.arange(4, dtype=torch.int32).repeat(B, 1).cuda()
+    cache = s5.PagedCache.create(geom, 4, 64, table)
+    for runs, want in (([(B - 1, 8, 1), (0, 40, 1), (B - 1, 16, 1), (0, 48, 1)], s5.DEV_RANGE),
+                       ([(0, 8, 4), (-1, 0, 1), (0, 16, 1)], s5.DEV_RANGE),
+                       ([(0, 0, 100), (B - 1, 128, 100), (-1, 0, 60), (0, 104, 7)], s5.DEV_RANGE),
+                       ([(B - 1, 8, 1), (0, 40, 1), (-1, 0, 1), (-1, 0, 1)], 0),
+                       ([(-1, 0, 1), (B - 1, 8, 100), (-1, 0, 300), (0, 120, 100), (-1, 0, 1)], 0)):
+        seq, pos = rows_of(*runs)
+        x = torch.ones((len(seq), 1, 128), dtype=torch.bfloat16).cuda()
+        s5.step5_kv_append_e4m3(geom, x, x, cache, *dev(seq, pos))
+        assert status(s5) == want, runs
+    if B > 2:  # a decode batch of many sequences, in any order, and with one of them twice
+        seq = torch.randperm(B, generator=torch.Generator().manual_seed(78)).int()
+        pos = torch.zeros(B, dtype=torch.int32)
+        cache = s5.PagedCache.create(geom, B, 16, torch.arange(B, dtype=torch.int32, device="cuda").view(B, 1))
+        x = torch.ones((B, 1, 128), dtype=torch.bfloat16).cuda()
+        for twice in (False, True):
+            if twice:
+                seq[100], seq[-100] = seq[200], -1
+                pos[100] = 8  # (in the next region)
+            s5.step5_kv_append_e4m3(geom, x, x, cache, *dev(seq, pos))
+            assert status(s5) == (s5.DEV_RANGE if twice else 0)
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_append_rotates_q_in_place(s5, e4m3):
     geom = geometry(s5, 2, 8)
