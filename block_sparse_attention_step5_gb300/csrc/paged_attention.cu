@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 L[h] = (rd[0][h] + rd[1][h]) + (rd[2][h] + rd[3][h]);
-                o[h] = L[h] == 0.0f ? 0.0f : o[h] * __fdividef(vref * (1.0f / kPTop), L[h]);
+                // (vref apart: the quotient may underflow with it)
+                o[h] = L[h] == 0.0f ? 0.0f : o[h] * __fdividef(1.0f / kPTop, L[h]) * vref;
             }
             if (whole) {
                 const int64_t at = (int64_t)done.n * p.Hq + (int64_t)done.g * H;

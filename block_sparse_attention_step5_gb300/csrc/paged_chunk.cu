@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::fence_after_sync();
             const bool any_nan = s_any_nan[i & 7] != 0, whole = e.n == e.nt;
-            float f = l == 0.0f ? 0.0f : vref * (1.0f / kPTop) / l;
+            float f = l == 0.0f ? 0.0f : (1.0f / kPTop) / l;  // (times vref below: their product may underflow)
             const int hr = w * 128 + r;
             const int64_t at = (int64_t)(e.blk * NB + j) * p.Hq + (int64_t)e.g * HQ + r % HQ;
             float* st = p.states + ((int64_t)2 * blockIdx.x + (e_begin >= start ? 1 : 0)) * kStateFloats;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tc::ld32(o_at + c, o);
 #pragma unroll
-                for (int d = 0; d < 32; ++d) o[d] = l == 0.0f ? 0.0f : o[d] * f;
+                for (int d = 0; d < 32; ++d) o[d] = l == 0.0f ? 0.0f : o[d] * f * vref;
                 if (any_nan)
 #pragma unroll
                     for (int d = 0; d < 32; ++d)

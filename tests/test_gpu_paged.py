@@ -764,6 +764,27 @@ def test_windows_of_rows_that_lie_apart(s5, hq, pt):
     assert status(s5) == s5.DEV_RANGE
 
 
+@pytest.mark.parametrize("runs, low, gate", [([20000 - b for b in range(40)], -126, 0.0), ([300 + i for _ in range(40) for i in range(64)], -118, -8.0)])
+def test_values_near_the_smallest(s5, runs, low, gate):
+    """Values of 2^-126 times their codes keep their bits beside large row sums and small gates.  q is zero and the codes are
+    positive, so that each result is the mean of its keys' values: one rounding (2^-8), sums of 20,000 positive terms in fp32
+    (below 2^-9) and a gate in fp32."""
+    c = Case(s5, [(0, p, 1) for p in runs], 4, 8, 64, seed=79)
+    c.seq = torch.arange(40).repeat_interleave(c.N // 40).int()
+    c.table = c.table.repeat(40, 1)
+    c.q[:] = 0.0
+    c.v &= 0x7f
+    c.vs = torch.exp2(torch.randint(low, low + 3, c.vs.shape, generator=c.gen).float())
+    c.gate = torch.full((c.N, 32), gate, dtype=torch.bfloat16) if gate else None
+    got = c.run().cpu().double()
+    assert status(s5) == 0
+    v = (R.decode(c.v) * c.vs.double().repeat_interleave(8, 2)[..., None])[c.table[0].long()]  # [pages][G][64][128]
+    mean = v.transpose(1, 2).reshape(-1, 4, 128).cumsum(0) / torch.arange(1, c.table.shape[1] * 64 + 1)[:, None, None]
+    want = mean[c.pos.long()].repeat_interleave(8, 1) * (1.0 / (1.0 + np.exp(-gate)) if gate else 1.0)
+    assert float(want.min()) > 2.0 ** -125
+    assert float(((got - want).abs() / want).max()) <= 2.0 ** -8 + 2.0 ** -9
+
+
 def test_a_table_that_is_replaced(s5):
     """The cache's next call reads the table assigned to it."""
     c = Case(s5, [(0, 1001, 1), (1, 500, 1)], seed=75)
