@@ -718,7 +718,7 @@ def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, wor
     cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
     sigmoid gate [N][Hq] when given."""
     _attend_e4m3("step5_paged_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                 window=int(window))
+                 window=max(-1, min(int(window), 2 ** 31 - 1)))  # (within the C call's 32 bits)
 
 
 def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,

@@ -380,6 +380,14 @@ def test_paged_attention_window(s5, rows, window):
     Case(s5, ROWS[rows], 2, 8, 24, seed=window).check(window)
 
 
+def test_windows_past_32_bits(s5):
+    """A window of 2^32 + 1 tokens is every token, one of -2^32 none that is allowed."""
+    c = Case(s5, [(0, 1001, 1)], 2, 8, 24, seed=80)
+    assert torch.equal(c.run(2 ** 32 + 1), c.run(0))
+    with pytest.raises(s5.Step5Error):
+        c.run(-2 ** 32)
+
+
 def test_paged_attention_scattered_rows(s5):
     """Rows of one sequence in any order, some twice, beside others."""
     c = Case(s5, [(0, 900, 1)] * 2 + [(0, 3, 1), (1, 77, 2), (0, 901, 3), (1, 12, 1), (0, 10, 1)], seed=9)
