@@ -17,9 +17,10 @@
 // and makes the rescaling of tokens already held exact unless they leave the normal range. Those are
 // requantised only when a new token raises the scale.
 //
-// With 4 KV groups, 32 query heads and pages of 64 tokens: one bf16 row 2.2 us; 2,048 rows in bf16
-// 10.7 us (42 MB, 4.0 TB/s; 6.2 us at the copy bandwidth); 16 e4m3 rows 2.9 us; 4 x 1,021 rows in
-// e4m3 16.3 us (80 MB, 4.9 TB/s; 11.8 us), the exact rotation keeping the issue slots 58 % busy.
+// With 4 KV groups, 32 query heads and pages of 64 tokens: one bf16 row 2.1 us; 2,048 rows in bf16
+// 10.7 us (42 MB, 4.0 TB/s; 6.2 us at the copy bandwidth; 8,192 warps, 1.7 of the GPU's fill); 16 e4m3
+// rows 3.0 us; 4 x 1,021 rows in e4m3 16.5 us (80 MB, 4.9 TB/s; 11.8 us), the exact rotation keeping the
+// issue slots 60 % busy.
 #include "paged.cuh"
 
 namespace step5 {
@@ -328,9 +329,9 @@ cudaError_t launch_append(const AppendParams& params, bool e4m3, cudaStream_t st
     AppendParams p = params;
     // Warps to a row's vectors: 4 when the rows fill the GPU (each then takes two or three vectors a
     // lane; 2,048 rows in bf16 10.7 us against 15.1 with 16), 16 for few rows, whose latency counts (one
-    // row 2.2 us against 2.9 with 4).  Rows a region warp looks over for leaders: 8 in chunks, one of
-    // which leads (4 x 1,021 rows 16.3 us against 26.8 with 1), one in decode batches, where every row
-    // leads (16 rows 2.9 us against 13 with 8, 1,024 rows 9.5 against 17.3).
+    // row 2.1 us against 2.9 with 4).  Rows a region warp looks over for leaders: 8 in chunks, one of
+    // which leads (4 x 1,021 rows 16.5 us against 26.8 with 1), one in decode batches, where every row
+    // leads (16 rows 3.0 us against 13 with 8, 1,024 rows 9.6 against 17.3).
     p.row_shift = p.N >= 512 ? 2 : 4;
     p.rows_per_warp = p.N >= 512 && p.N >= 8 * (int64_t)p.B ? 8 : 1;
     p.region_warps = e4m3 ? (uint32_t)((p.N + p.rows_per_warp - 1) / p.rows_per_warp * 2 * p.G) : 0u;

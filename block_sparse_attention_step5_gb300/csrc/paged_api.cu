@@ -133,9 +133,10 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))
         return STEP5_ERR_CUDA;
     // Rows of a sequence share its keys' tiles from 64 head rows a sequence and 128 head rows in all on.  With 8
-    // heads a group, microseconds shared and alone: 4 rows of each of 8 sequences of 8,192 tokens 80 and 46, 8 rows of each
-    // of 4 50 and 45, 8 of 16 107 and 140; one sequence's 8 rows 31 and 19 (behind 65,536 tokens 61 and 72), its 16 rows 31 and
-    // 27 (62 and 144), its 32 rows 33 and 45.
+    // heads a group, microseconds shared and alone: 4 rows of each of 8 sequences of 8,192 tokens 74 and 45, 8 rows of each
+    // of 4 52 and 45, 8 of 16 111 and 140; one sequence's 8 rows 32 and 19 (behind 65,536 tokens 62 and 72), its 16 rows 32 and
+    // 27 (63 and 144), its 32 rows 33 and 45.  With 16 heads, 16 rows of one 33 and 38, 8 of 4 49 and 59; with 4 heads, 32 of one 32 and
+    // 42, 16 of 4 54 and 66.
     const int64_t head_rows = (int64_t)N * (geom->num_q_heads / geom->num_kv_groups);
     const bool chunk = sel_ids == nullptr && head_rows >= 64 * (int64_t)B && head_rows >= 128;
     const cudaError_t e = chunk ? launch_paged_chunk(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true)

@@ -28,8 +28,8 @@
 // rows masked.
 //
 // What it takes, with 4 KV groups of 8 heads and pages of 64 tokens, join included:
-//   2,048 rows behind 2,048 tokens    135 us  1.03e11 flop (at 1,899 TFLOP/s: 54 us)
-//   2,048 rows, window of 512 tokens   59 us  1.7e10 flop (9 us)
+//   2,048 rows behind 2,048 tokens    138 us  1.03e11 flop (at 1,899 TFLOP/s: 54 us)
+//   2,048 rows, window of 512 tokens   61 us  1.7e10 flop (9 us)
 // A tile of keys takes its two row tiles 2.5 us: maximum 1,050, weights 1,400, the products and the
 // waits around them 2,200 cycles (1,024 of tensor core; the first product alone reads shared memory
 // at its full rate, which the copies and V's conversion share).  Around the tiles: start 4 us, q 3 us
@@ -962,7 +962,7 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
 }
 
 // The same for few items, each shared by many CTAs (one sequence's 16 rows behind 8,192 tokens: 39 CTAs an
-// item, 31 us in all against 40).  First the states' weights, 32 threads to a row; then two groups of 256
+// item, 32 us in all against 40).  First the states' weights, 32 threads to a row; then two groups of 256
 // threads take every other state each, eight of them asked for at a time.
 template <class S>
 __global__ void __launch_bounds__(512) join_wide_kernel(PagedAttnParams p) {
@@ -1041,7 +1041,7 @@ cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     if (e != cudaSuccess) return e;
     cfg.gridDim.y = 256 / 16;
     cfg.dynamicSmemBytes = 0;
-    // at least 8 CTAs an item on average, or fewer (2,048 rows on 2K: 135 us against 149 with the wide one)
+    // at least 8 CTAs an item on average, or fewer (2,048 rows on 2K: 138 us against 152 with the wide one)
     if ((int64_t)((p.N + S::NB - 1) / S::NB) * p.G * 8 <= num_sms) {
         cfg.blockDim = dim3(512);
         return cudaLaunchKernelEx(&cfg, join_wide_kernel<S>, p);

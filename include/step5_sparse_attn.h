@@ -397,8 +397,9 @@ typedef struct {
  * NULL: no rotation (rot_dims and t_cap are then unused, t_cap still positive).  q, k and
  * v rows are q_stride, k_stride and v_stride elements apart (multiples of 8, at least a
  * row's heads), each row's heads dense: slices of one projection's output will do.
- * q_out [N][num_q_heads][head_dim].  Rows are independent; two rows of a call with the
- * same sequence and position leave one of the two behind.  A row out of range, or at or past
+ * q_out [N][num_q_heads][head_dim].  Rows are independent; two rows of a call that write the same
+ * token (the same sequence and position, or a page that several sequences' tables name) leave some 16-byte pieces
+ * of one and some of the other.  A row out of range, or at or past
  * min(t_cap, table_len * page_tokens), writes nothing.  Pointers 16-byte aligned.
  * N <= 2^24. */
 step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
@@ -422,7 +423,8 @@ step5_status step5_kv_append(const step5_geometry* geom, const step5_pages* page
  * positions (a chunk, or one decode row); a row that follows one of its own sequence at
  * any other position sets STEP5_DEV_RANGE, and neither its k and v are written nor those of
  * the rows behind it up to the next region.  Rows of one sequence with others (or padding) between
- * them set STEP5_DEV_RANGE too; the regions that such runs of it share then hold anything. */
+ * them set STEP5_DEV_RANGE too; the regions that such runs of it share then hold anything, as does a region
+ * of a page that several sequences' tables name and a call writes through more than one of them. */
 step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                                   int32_t rot_dims, int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride,
                                   const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride,
@@ -437,7 +439,7 @@ step5_status step5_kv_append_e4m3(const step5_geometry* geom, const step5_pages*
  *   out[n][h] = sigmoid(gate[n][h]) * softmax(softmax_scale * q[n][h] . K^T) V
  * with K and V the values code * scale, every score, weight and sum in fp32 (a weight times
  * its V scale meets V's codes with 11 significant bits or more, or within 2^-24 of the row's largest
- * weight times the largest V scale; q meets K's codes exactly, or within 2^-17 of the head's
+ * weight times the row's largest V scale, 2^-126 or more; q meets K's codes exactly, or within 2^-17 of the head's
  * largest value), one rounding to bf16; the factor is 1 with gate NULL
  * (gate [N][num_q_heads] bf16 logits).  q, out: [N][num_q_heads][head_dim] bf16.  Tokens
  * outside a row's keys never reach its result, whatever their codes, scales and table entries hold (a
