@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             }
             if (whole) {
                 const int64_t at = (int64_t)done.n * p.Hq + (int64_t)done.g * H;
-                if (p.gate != nullptr)
+                if (p.gate != nullptr && L[0] != 0.0f)  // (without keys no head has a weight, and zero stays zero)
 #pragma unroll
                     for (int h = 0; h < H; ++h) o[h] = gated(p, at + h, o[h]);
 #pragma unroll
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
         }
         const int64_t at = (int64_t)item.x * p.Hq + (int64_t)item.y * S::H + c;
         o = w == 0.0f ? 0.0f : o / w;
-        if (p.gate != nullptr) o = gated(p, at, o);
+        if (p.gate != nullptr && w != 0.0f) o = gated(p, at, o);
         p.out[at * 128 + d] = f32_to_bf16_bits(o);
     }
 }

@@ -198,13 +198,13 @@ struct Tile {
     int n0;              // first row of the block
 };
 
-// Head row r (of 256) of the block from row n0: dims d0 .. d0 + 7 of its output, gated and rounded.
+// Head row r (of 256) of the block from row n0: dims d0 .. d0 + 7 of its output, gated (where it has keys) and rounded.
 template <class S>
-__device__ __forceinline__ void write_out8(const PagedAttnParams& p, int n0, int g, int r, int d0, const float (&v)[8]) {
+__device__ __forceinline__ void write_out8(const PagedAttnParams& p, int n0, int g, int r, int d0, bool keys, const float (&v)[8]) {
     const int n = n0 + r / S::HQ;
     const int64_t at = (int64_t)n * p.Hq + (int64_t)g * S::HQ + r % S::HQ;
     float f = 1.0f;
-    if (p.gate != nullptr) f = 1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at])));
+    if (p.gate != nullptr && keys) f = 1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at])));
     *reinterpret_cast<uint4*>(p.out + at * 128 + d0) =
         make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f), pack_bf16x2(v[4] * f, v[5] * f),
                    pack_bf16x2(v[6] * f, v[7] * f));
@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(256) join_chunk_kernel(PagedAttnParams p) {
     }
 #pragma unroll
     for (int d = 0; d < 8; ++d) o[d] = w == 0.0f ? 0.0f : o[d] / w;
-    write_out8<S>(p, item.x, item.y, hr, d8 * 8, o);
+    write_out8<S>(p, item.x, item.y, hr, d8 * 8, w != 0.0f, o);
 }
 
 // The same for few items, each shared by many CTAs (one sequence's 16 rows behind 8,192 tokens: 39 CTAs an
@@ -1015,7 +1015,7 @@ __global__ void __launch_bounds__(512) join_wide_kernel(PagedAttnParams p) {
     w += part[0][row];
 #pragma unroll
     for (int d = 0; d < 8; ++d) o[d] = w == 0.0f ? 0.0f : (o[d] + so[at][d]) / w;
-    write_out8<S>(p, item.x, item.y, hr, d8 * 8, o);
+    write_out8<S>(p, item.x, item.y, hr, d8 * 8, w != 0.0f, o);
 }
 
 template <int HQ>

@@ -793,6 +793,20 @@ def test_values_near_the_smallest(s5, runs, low, gate):
     assert float(((got - want).abs() / want).max()) <= 2.0 ** -8 + 2.0 ** -9
 
 
+@pytest.mark.parametrize("runs", [[(0, 5, 1), (0, 900, 1)], [(b, 40 * b, 1) for b in range(60)], [(0, 300, 40)], [(b, 300, 64) for b in range(40)]])
+def test_rows_without_keys_are_zero_whatever_their_gate(s5, runs):
+    """NaN as the gate of a row out of range."""
+    c = Case(s5, runs, 4, 8, 16, seed=81)
+    c.gate = normal(c.gen, c.N, 32)
+    bad = torch.zeros(c.N, dtype=torch.bool)
+    bad[::7] = True
+    c.gate[bad] = float("nan")
+    c.pos[bad] = 16 * c.table.shape[1]
+    got = c.run()
+    assert status(s5) == s5.DEV_RANGE
+    assert bool((got[bad] == 0).all()) and bool(torch.isfinite(got[~bad]).all())
+
+
 def test_a_table_that_is_replaced(s5):
     """The cache's next call reads the table assigned to it."""
     c = Case(s5, [(0, 1001, 1), (1, 500, 1)], seed=75)
