@@ -38,7 +38,7 @@
 //   one row of 4,608 tokens     9.3 us  latency: split 2, page, scale and key loads 2, one tile 1,
 //                                       second product and states 1.3, launch and join 3
 //   16 rows of 512 picks       23.7 us  the copies alone 22.3 (68 MB in boxes of 1 KB)
-//   2,048 rows of 512 picks   1,139 us  the copies alone 934: 8.6 GB in boxes of 1 KB out of L2,
+//   2,048 rows of 512 picks   1,135 us  the copies alone 934: 8.6 GB in boxes of 1 KB out of L2,
 //                                       one in 32 cycles on each SM
 #include "paged_device.cuh"
 
