@@ -13,10 +13,11 @@ Steps (TensorFold PR #903, "Step-5-Preview on one 256 GB Mac", CSA-indexer commi
   step5_sparse_attn_gated -- the same, followed by the per-head sigmoid output gate
   step5_indexer_front     -- decode front end: q/k norms, k/z cache write, summary on completion
 
-The paged KV cache that step (4) can read in 8 bits (``PagedCache``):
+The paged KV cache, in bf16 or 8 bits (``PagedCache``):
+  step5_paged_plan        -- a step's pages, block tables, rows and regions, made on the GPU
   step5_kv_append, step5_kv_append_e4m3 -- rotate and append the rows' keys and values
-  step5_paged_attn_e4m3   -- causal (or sliding-window) attention over the e4m3 pages
-  step5_sparse_attn_e4m3  -- step (4) over the e4m3 pages
+  step5_paged_attn, step5_paged_attn_e4m3 -- causal (or sliding-window) attention over the pages
+  step5_sparse_attn_paged, step5_sparse_attn_e4m3 -- step (4) over the pages
 """
 from __future__ import annotations
 
@@ -43,6 +44,7 @@ __all__ = [
     "Workspace", "decode_step",
     "Pages", "PagedCache", "PagedWorkspace", "step5_kv_append", "step5_kv_append_e4m3", "step5_paged_attn_e4m3",
     "step5_sparse_attn_e4m3", "step5_paged_workspace_bytes", "decode_step_paged",
+    "step5_paged_attn", "step5_sparse_attn_paged", "PagedTable", "PagedRows", "step5_paged_plan",
 ]
 
 STATUS = {0: "STEP5_OK", 1: "STEP5_ERR_INVALID_ARGUMENT", 2: "STEP5_ERR_UNSUPPORTED",
@@ -125,6 +127,9 @@ def load():
                                        P, P]),
         "step5_paged_attn_e4m3": (i32, [G, PG, i32, i32, i32, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
         "step5_sparse_attn_e4m3": (i32, [G, PG, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "step5_paged_attn": (i32, [G, PG, i32, i32, i32, P, i64, P, P, P, P, P, P, P, P, sz, P]),
+        "step5_sparse_attn_paged": (i32, [G, PG, i32, i32, P, i64, P, P, P, P, P, P, P, P, P, P, sz, P]),
+        "step5_paged_plan": (i32, [G, PG, i32, i32, P, P, P, P, P, P, P, P, P, P, P, P, P, P]),
         "step5_paged_workspace_bytes": (sz, [G]),
         "step5_workspace_bytes": (sz, [G, i32, i32]),
         "step5_workspace_init": (i32, [P, sz, P]),
@@ -577,7 +582,7 @@ def step5_paged_workspace_bytes(geom) -> int:
 
 @dataclass
 class PagedWorkspace:
-    """Device workspace of the attention calls over e4m3 pages (it may hold anything)."""
+    """Device workspace of the attention calls over pages (it may hold anything)."""
     tensor: torch.Tensor
 
     @classmethod
@@ -685,12 +690,12 @@ def step5_kv_append_e4m3(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=No
     _kv_append("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
 
 
-def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None, sel_ids=None,
-                 sel_count=None):
+def _attend_paged(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None,
+                  sel_ids=None, sel_count=None):
     g = Geometry.of(geom)
     dev, st = _device_and_stream(cache, g, stream)
-    if not cache.e4m3:
-        raise ValueError(f"{fn} reads e4m3 pools")
+    if cache.e4m3 != e4m3:
+        raise ValueError(f"{fn} reads {'e4m3' if e4m3 else 'bf16'} pools")
     N, Hq = q.shape[0], g.num_q_heads
     shape = (N, Hq, g.head_dim)
     w = ws.tensor if isinstance(ws, PagedWorkspace) else ws
@@ -702,7 +707,8 @@ def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws,
                  _arg("sel_count", sel_count, torch.int32, (N, g.num_kv_groups), dev))
     else:
         before, after = (window,), ()
-    st = getattr(load(), fn)(g, cache._pages, N, cache.B, *before, _arg("q", q, torch.bfloat16, shape, dev), *cache._pools,
+    rows = (_arg("q", q, torch.bfloat16, shape, dev),) if e4m3 else _rows("q", q, Hq, g.head_dim, dev, N)
+    st = getattr(load(), fn)(g, cache._pages, N, cache.B, *before, *rows, *cache._pools,
                              _arg("row_seq", row_seq, torch.int32, (N,), dev),
                              _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
                              None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
@@ -712,32 +718,124 @@ def _attend_e4m3(fn: str, geom, q, cache: PagedCache, row_seq, row_pos, out, ws,
         raise Step5Error(fn, st)
 
 
+def _window(window) -> int:
+    return max(-1, min(int(window), 2 ** 31 - 1))  # (within the C call's 32 bits)
+
+
 def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
                           stream=None):
     """Causal attention of rows q [N][Hq][128] bf16 at (row_seq, row_pos) over the e4m3
     cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
     sigmoid gate [N][Hq] when given."""
-    _attend_e4m3("step5_paged_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                 window=max(-1, min(int(window), 2 ** 31 - 1)))  # (within the C call's 32 bits)
+    _attend_paged("step5_paged_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                  window=_window(window))
+
+
+def step5_paged_attn(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
+                     stream=None):
+    """step5_paged_attn_e4m3 over the bf16 cache.  q may be a slice of one [N][heads][128]
+    tensor (rows apart, heads together)."""
+    _attend_paged("step5_paged_attn", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                  window=_window(window))
 
 
 def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                            gate=None, stream=None):
     """step5_sparse_attn over the e4m3 cache: the picked regions sel_ids [N][G][top_k],
     sel_count [N][G] and the row's own region."""
-    _attend_e4m3("step5_sparse_attn_e4m3", geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                 sel_ids=sel_ids, sel_count=sel_count)
+    _attend_paged("step5_sparse_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                  sel_ids=sel_ids, sel_count=sel_count)
+
+
+def step5_sparse_attn_paged(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
+                            gate=None, stream=None):
+    """step5_sparse_attn over the bf16 cache's pages, as step5_sparse_attn_e4m3 over the e4m3
+    ones.  q as in step5_paged_attn."""
+    _attend_paged("step5_sparse_attn_paged", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                  sel_ids=sel_ids, sel_count=sel_count)
+
+
+@dataclass
+class PagedTable:
+    """The pages of a cache's sequences, all int32 on the GPU: the block table [B][table_len] (the tensor
+    that the PagedCache has), the pages that each sequence holds [B], and the stack of free pages: free_pages
+    [num_pages], of which the first free_count [1] are free, the last of them its top."""
+    block_table: torch.Tensor
+    held: torch.Tensor
+    free_pages: torch.Tensor
+    free_count: torch.Tensor
+    page_tokens: int
+
+    @classmethod
+    def create(cls, num_pages: int, page_tokens: int, table_len: int, B: int, device="cuda") -> "PagedTable":
+        """Every page free, no sequence holding any."""
+        zeros = lambda *shape: torch.zeros(shape, dtype=torch.int32, device=device)
+        return cls(zeros(B, table_len), zeros(B), torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   zeros(1) + num_pages, page_tokens)
+
+
+@dataclass
+class PagedRows:
+    """What step5_paged_plan writes of a step, all int32: of each row its sequence and position [N] (-1:
+    padding), of each sequence its first row [B + 1], its tokens after the step, those granted, and the regions
+    [region_begin, region_end) that the step completes [B]."""
+    row_seq: torch.Tensor
+    row_pos: torch.Tensor
+    row_start: torch.Tensor
+    ends: torch.Tensor
+    granted: torch.Tensor
+    region_begin: torch.Tensor
+    region_end: torch.Tensor
+
+    @classmethod
+    def create(cls, B: int, N: int, device="cuda") -> "PagedRows":
+        empty = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        return cls(empty(N), empty(N), empty(B + 1), *(empty(B) for _ in range(4)))
+
+
+def step5_paged_plan(table: PagedTable, rows: PagedRows, lengths, new_tokens, stream=None, geom=STEP5_GEOMETRY):
+    """Plans a step of sequences that have ``lengths`` [B] tokens in the cache and get ``new_tokens`` [B] (int32):
+    pages move between the table and its free ones, and ``rows`` is filled in (see the header).  lengths may be
+    rows.ends, so that a captured step goes on from the one before."""
+    bt = table.block_table
+    B, table_len = bt.shape
+    dev = torch.cuda.current_device()
+    if table.free_pages.dim() != 1 or rows.row_seq.dim() != 1:
+        raise ValueError("free_pages and row_seq must be one-dimensional")
+    pages = Pages(table.free_pages.shape[0], int(table.page_tokens), table_len)
+    N = rows.row_seq.shape[0]
+    i32 = lambda what, t, *shape: _arg(what, t, torch.int32, shape, dev)
+    st = load().step5_paged_plan(
+        Geometry.of(geom), pages, N, B, i32("lengths", lengths, B), i32("new_tokens", new_tokens, B),
+        i32("block_table", bt, B, table_len), i32("held", table.held, B),
+        i32("free_pages", table.free_pages, pages.num_pages), i32("free_count", table.free_count, 1),
+        i32("row_seq", rows.row_seq, N), i32("row_pos", rows.row_pos, N), i32("row_start", rows.row_start, B + 1),
+        i32("ends", rows.ends, B), i32("granted", rows.granted, B), i32("region_begin", rows.region_begin, B),
+        i32("region_end", rows.region_end, B),
+        stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        raise Step5Error("step5_paged_plan", st)
 
 
 def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws: PagedWorkspace, k, v, sel_ids,
-                      sel_count, q_rot, out, max_regions_per_seq, cos=None, sin=None, gate=None, stream=None):
-    """One pass of the whole path over an e4m3 paged cache: the rows' k and v appended (and
+                      sel_count, q_rot, out, max_regions_per_seq, cos=None, sin=None, gate=None, stream=None,
+                      plan=None):
+    """One pass of the whole path over a paged cache, e4m3 or bf16: the rows' k and v appended (and
     t["q"] rotated into q_rot by cos/sin), then summarise, score + select over the indexer
-    tensors of ``t`` as decode_step does, and attend over the picked regions of the cache."""
-    step5_kv_append_e4m3(geom, k, v, cache, t["row_seq"], t["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)
-    step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], t["sum_begin"], t["sum_end"],
+    tensors of ``t`` as decode_step does, and attend over the picked regions of the cache.  With ``plan``,
+    (table, rows, lengths, new_tokens) as step5_paged_plan takes them, the step is planned first, and its
+    rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end."""
+    rows = t
+    if plan is not None:
+        step5_paged_plan(*plan, stream=stream, geom=geom)
+        p = plan[1]
+        rows = {"row_seq": p.row_seq, "row_pos": p.row_pos, "sum_begin": p.region_begin, "sum_end": p.region_end}
+    append = step5_kv_append_e4m3 if cache.e4m3 else step5_kv_append
+    append(geom, k, v, cache, rows["row_seq"], rows["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)
+    step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], rows["sum_begin"], rows["sum_end"],
                            t["summaries"], max_regions_per_seq=max_regions_per_seq, stream=stream)
-    step5_index_score_topk(geom, t["idx_q"], t["w"], t["row_seq"], t["row_pos"], t["cos"], t["sin"], t["summaries"],
-                           sel_ids, sel_count, ws.tensor, t_cap=t["idx_k"].shape[2], stream=stream)
-    step5_sparse_attn_e4m3(geom, q_rot, cache, t["row_seq"], t["row_pos"], sel_ids, sel_count, out, paged_ws, gate=gate,
-                           stream=stream)
+    step5_index_score_topk(geom, t["idx_q"], t["w"], rows["row_seq"], rows["row_pos"], t["cos"], t["sin"],
+                           t["summaries"], sel_ids, sel_count, ws.tensor, t_cap=t["idx_k"].shape[2], stream=stream)
+    attend = step5_sparse_attn_e4m3 if cache.e4m3 else step5_sparse_attn_paged
+    attend(geom, q_rot, cache, rows["row_seq"], rows["row_pos"], sel_ids, sel_count, out, paged_ws, gate=gate,
+           stream=stream)

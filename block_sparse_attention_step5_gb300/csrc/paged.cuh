@@ -49,9 +49,9 @@ cudaError_t launch_append(const AppendParams& p, bool e4m3, cudaStream_t stream,
 
 struct PagedAttnParams {
     const uint16_t* q;       // [N][Hq][128]
-    const uint8_t* k_pages;
+    const uint8_t* k_pages;  // (of bf16 pools the bytes)
     const uint8_t* v_pages;
-    const float* k_scales;
+    const float* k_scales;   // null: bf16 pools
     const float* v_scales;
     PageMap pages;
     const int32_t* row_seq;
@@ -66,6 +66,7 @@ struct PagedAttnParams {
     int N, B, G, Hq, top_k, window;
     int box_regions;           // regions of one TMA box (a power of two <= 16 that divides a page's)
     float scale_log2;          // softmax_scale * log2(e)
+    int64_t q_stride;          // bf16 pools: elements between rows of q (Hq * 128 otherwise)
 };
 constexpr int kPagedMaxCtas = 480;           // of one launch
 constexpr size_t kPagedItemBytes = 16 * 512;
@@ -80,6 +81,29 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& 
 // The same for launches whose sequences have several rows (no picks).
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
                                cudaStream_t stream, bool pdl);
+
+// Over bf16 pools: a (row, group)'s keys, all of its window's or those of its picks.
+cudaError_t launch_paged_attention_bf16(const PagedAttnParams& p, int num_sms, cudaStream_t stream, bool pdl);
+
+struct PlanParams {
+    const int32_t* lengths;      // [B] tokens that each sequence has in the cache
+    const int32_t* new_tokens;   // [B]
+    int32_t* block_table;        // [B][table_len]
+    int32_t* held;               // [B] pages of each sequence: entries 0 .. held - 1 of its table
+    int32_t* free_pages;         // [num_pages], a stack: entries 0 .. free_count - 1
+    int32_t* free_count;         // [1]
+    int32_t* row_seq;            // [N]
+    int32_t* row_pos;            // [N]
+    int32_t* row_start;          // [B + 1]
+    int32_t* ends;               // [B], may be the lengths
+    int32_t* granted;            // [B]
+    int32_t* region_begin;       // [B]
+    int32_t* region_end;         // [B]
+    uint32_t* status;
+    int N, B, num_pages, page_tokens, table_len;
+};
+constexpr int kPlanMaxSeqs = 8192;  // their sums lie in shared memory
+cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream, bool pdl);
 
 // A scale that can be used: positive and at most 2^126 (so that the power of two above it is finite).
 __device__ __forceinline__ bool scale_ok(float s) { return s > 0.0f && s <= 8.507059173e37f; }

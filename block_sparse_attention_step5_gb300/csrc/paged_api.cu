@@ -85,26 +85,29 @@ step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, i
     return launch_append(p, e4m3, (cudaStream_t)stream, true) == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 
-step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
-                         const void* q_bf16, const uint8_t* k_pages, const uint8_t* v_pages, const float* k_scales,
-                         const float* v_scales, const int32_t* block_table, const int32_t* row_seq,
-                         const int32_t* row_pos, const int32_t* sel_ids, const int32_t* sel_count, const void* gate,
-                         void* out_bf16, void* workspace, size_t workspace_bytes, step5_stream_t stream) {
+// Checks the arguments of an attention call over either kind of pool and lays them out (scales: e4m3 pools).
+step5_status attend_params(PagedAttnParams& p, const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                           int32_t window, const void* q_bf16, int64_t q_stride, const void* k_pages, const void* v_pages,
+                           bool scales, const float* k_scales, const float* v_scales, const int32_t* block_table,
+                           const int32_t* row_seq, const int32_t* row_pos, const int32_t* sel_ids,
+                           const int32_t* sel_count, const void* gate, void* out_bf16, void* workspace,
+                           size_t workspace_bytes) {
     step5_status s = check_pages(geom, pages, N, B, block_table);
     if (s != STEP5_OK) return s;
     if (window < 0) return STEP5_ERR_INVALID_ARGUMENT;
     if (N > 65535) return STEP5_ERR_UNSUPPORTED;
-    if (!q_bf16 || !k_pages || !v_pages || !k_scales || !v_scales || !row_seq || !row_pos || !out_bf16)
+    if (!q_bf16 || !k_pages || !v_pages || (scales && (!k_scales || !v_scales)) || !row_seq || !row_pos || !out_bf16)
         return STEP5_ERR_INVALID_ARGUMENT;
+    if (q_stride < (int64_t)geom->num_q_heads * geom->head_dim || q_stride % 8) return STEP5_ERR_INVALID_ARGUMENT;
     if (!aligned16(q_bf16) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out_bf16) || !aligned16(workspace))
         return STEP5_ERR_INVALID_ARGUMENT;
     if (workspace == nullptr || workspace_bytes < step5_paged_workspace_bytes(geom)) return STEP5_ERR_WORKSPACE;
     uint32_t* st = status_ptr();
     if (!st) return STEP5_ERR_CUDA;
-    PagedAttnParams p;
     p.q = static_cast<const uint16_t*>(q_bf16);
-    p.k_pages = k_pages;
-    p.v_pages = v_pages;
+    p.q_stride = q_stride;
+    p.k_pages = static_cast<const uint8_t*>(k_pages);
+    p.v_pages = static_cast<const uint8_t*>(v_pages);
     p.k_scales = k_scales;
     p.v_scales = v_scales;
     p.pages = {block_table, pages->num_pages, pages->page_tokens, pages->table_len};
@@ -128,6 +131,19 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     p.box_regions = 1;
     if (sel_ids == nullptr)
         while (p.box_regions < 16 && (pages->page_tokens / 8) % (2 * p.box_regions) == 0) p.box_regions *= 2;
+    return STEP5_OK;
+}
+
+step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
+                         const void* q_bf16, const uint8_t* k_pages, const uint8_t* v_pages, const float* k_scales,
+                         const float* v_scales, const int32_t* block_table, const int32_t* row_seq,
+                         const int32_t* row_pos, const int32_t* sel_ids, const int32_t* sel_count, const void* gate,
+                         void* out_bf16, void* workspace, size_t workspace_bytes, step5_stream_t stream) {
+    PagedAttnParams p;
+    const step5_status s = attend_params(p, geom, pages, N, B, window, q_bf16, geom ? (int64_t)geom->num_q_heads * 128 : 0,
+                                         k_pages, v_pages, true, k_scales, v_scales, block_table, row_seq, row_pos,
+                                         sel_ids, sel_count, gate, out_bf16, workspace, workspace_bytes);
+    if (s != STEP5_OK) return s;
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)pages->num_pages * geom->num_kv_groups * pages->page_tokens;
     if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))
@@ -141,6 +157,20 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     const bool chunk = sel_ids == nullptr && head_rows >= 64 * (int64_t)B && head_rows >= 128;
     const cudaError_t e = chunk ? launch_paged_chunk(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true)
                                 : launch_paged_attention(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
+    return e == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
+}
+
+step5_status attend_bf16_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
+                              const void* q_bf16, int64_t q_stride, const void* k_pages, const void* v_pages,
+                              const int32_t* block_table, const int32_t* row_seq, const int32_t* row_pos,
+                              const int32_t* sel_ids, const int32_t* sel_count, const void* gate, void* out_bf16,
+                              void* workspace, size_t workspace_bytes, step5_stream_t stream) {
+    PagedAttnParams p;
+    const step5_status s = attend_params(p, geom, pages, N, B, window, q_bf16, q_stride, k_pages, v_pages, false, nullptr,
+                                         nullptr, block_table, row_seq, row_pos, sel_ids, sel_count, gate, out_bf16,
+                                         workspace, workspace_bytes);
+    if (s != STEP5_OK) return s;
+    const cudaError_t e = launch_paged_attention_bf16(p, num_sms(), (cudaStream_t)stream, true);
     return e == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 
@@ -196,6 +226,64 @@ step5_status step5_sparse_attn_e4m3(const step5_geometry* geom, const step5_page
     return attend_impl(geom, pages, N, B, 0, q_bf16, k_pages_e4m3, v_pages_e4m3, k_scales_f32, v_scales_f32,
                        block_table_or_null, row_seq, row_pos, sel_ids, sel_count, gate_bf16_or_null, out_bf16,
                        workspace, workspace_bytes, stream);
+}
+
+step5_status step5_paged_attn(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
+                              const void* q_bf16, int64_t q_stride, const void* k_pages_bf16, const void* v_pages_bf16,
+                              const int32_t* block_table_or_null, const int32_t* row_seq, const int32_t* row_pos,
+                              const void* gate_bf16_or_null, void* out_bf16, void* workspace, size_t workspace_bytes,
+                              step5_stream_t stream) {
+    return attend_bf16_impl(geom, pages, N, B, window, q_bf16, q_stride, k_pages_bf16, v_pages_bf16, block_table_or_null,
+                            row_seq, row_pos, nullptr, nullptr, gate_bf16_or_null, out_bf16, workspace, workspace_bytes,
+                            stream);
+}
+
+step5_status step5_sparse_attn_paged(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                                     const void* q_bf16, int64_t q_stride, const void* k_pages_bf16,
+                                     const void* v_pages_bf16, const int32_t* block_table_or_null, const int32_t* row_seq,
+                                     const int32_t* row_pos, const int32_t* sel_ids, const int32_t* sel_count,
+                                     const void* gate_bf16_or_null, void* out_bf16, void* workspace,
+                                     size_t workspace_bytes, step5_stream_t stream) {
+    if (sel_ids == nullptr || sel_count == nullptr) return STEP5_ERR_INVALID_ARGUMENT;
+    return attend_bf16_impl(geom, pages, N, B, 0, q_bf16, q_stride, k_pages_bf16, v_pages_bf16, block_table_or_null,
+                            row_seq, row_pos, sel_ids, sel_count, gate_bf16_or_null, out_bf16, workspace,
+                            workspace_bytes, stream);
+}
+
+step5_status step5_paged_plan(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                              const int32_t* lengths, const int32_t* new_tokens, int32_t* block_table, int32_t* held_pages,
+                              int32_t* free_pages, int32_t* free_count, int32_t* row_seq, int32_t* row_pos,
+                              int32_t* row_start, int32_t* ends, int32_t* granted, int32_t* region_begin,
+                              int32_t* region_end, step5_stream_t stream) {
+    const step5_status s = check_pages(geom, pages, N, B, block_table);
+    if (s != STEP5_OK) return s;
+    if (!lengths || !new_tokens || !block_table || !held_pages || !free_pages || !free_count || !row_seq || !row_pos ||
+        !row_start || !ends || !granted || !region_begin || !region_end)
+        return STEP5_ERR_INVALID_ARGUMENT;
+    if (N > 1 << 24 || B > kPlanMaxSeqs) return STEP5_ERR_UNSUPPORTED;
+    uint32_t* st = status_ptr();
+    if (!st) return STEP5_ERR_CUDA;
+    PlanParams p;
+    p.lengths = lengths;
+    p.new_tokens = new_tokens;
+    p.block_table = block_table;
+    p.held = held_pages;
+    p.free_pages = free_pages;
+    p.free_count = free_count;
+    p.row_seq = row_seq;
+    p.row_pos = row_pos;
+    p.row_start = row_start;
+    p.ends = ends;
+    p.granted = granted;
+    p.region_begin = region_begin;
+    p.region_end = region_end;
+    p.status = st;
+    p.N = N;
+    p.B = B;
+    p.num_pages = pages->num_pages;
+    p.page_tokens = pages->page_tokens;
+    p.table_len = pages->table_len;
+    return launch_paged_plan(p, (cudaStream_t)stream, true) == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 
 }  // extern "C"

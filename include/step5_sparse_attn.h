@@ -470,7 +470,64 @@ step5_status step5_sparse_attn_e4m3(const step5_geometry* geom, const step5_page
                                     const int32_t* sel_ids, const int32_t* sel_count, const void* gate_bf16_or_null,
                                     void* out_bf16, void* workspace, size_t workspace_bytes, step5_stream_t stream);
 
-/* Bytes of device workspace that the attention calls over an e4m3 pool need, whatever N,
+/* Causal attention over a bf16 pool: step5_paged_attn_e4m3 with K and V the pool's values.  For every row n
+ * (b = row_seq[n], p = row_pos[n]) and query head h of KV group g = h / (num_q_heads / G):
+ *   keys  = tokens max(0, p - window + 1) .. p  (window 0: 0 .. p)
+ *   out[n][h] = sigmoid(gate[n][h]) * softmax(softmax_scale * q[n][h] . K^T) V
+ * with bf16 products, every score and sum in fp32, the weights that meet V in bf16 (8 bits) where rows of a
+ * sequence share its keys' tiles and in two bf16 parts (16 bits) elsewhere, and one rounding to bf16; the factor
+ * is 1 with gate NULL (gate [N][num_q_heads] bf16 logits).  q rows are q_stride elements apart (a multiple of 8, at
+ * least a row's heads), each row's heads dense; out: [N][num_q_heads][head_dim] bf16.  Tokens outside a row's keys
+ * never reach its result, whatever the pages hold there (infinities and NaN too).  A region of the keys whose table
+ * entry is bad is left out and sets STEP5_DEV_RANGE; a row without keys, or out of range, gets zeros, as does one whose
+ * every score is -infinity; a padding row's output is left as it was.  N <= 65535.  Any order of rows.
+ * When rows share tiles, and the workspace: as step5_paged_attn_e4m3. */
+step5_status step5_paged_attn(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
+                              const void* q_bf16, int64_t q_stride, const void* k_pages_bf16, const void* v_pages_bf16,
+                              const int32_t* block_table_or_null, const int32_t* row_seq, const int32_t* row_pos,
+                              const void* gate_bf16_or_null, void* out_bf16, void* workspace, size_t workspace_bytes,
+                              step5_stream_t stream);
+
+/* Step (4) over a bf16 pool: step5_paged_attn with the keys of step5_sparse_attn, the regions
+ * sel_ids[n][g][0 .. sel_count[n][g]) (distinct candidates of the row) and the own-region tokens up to p. */
+step5_status step5_sparse_attn_paged(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                                     const void* q_bf16, int64_t q_stride, const void* k_pages_bf16,
+                                     const void* v_pages_bf16, const int32_t* block_table_or_null, const int32_t* row_seq,
+                                     const int32_t* row_pos, const int32_t* sel_ids, const int32_t* sel_count,
+                                     const void* gate_bf16_or_null, void* out_bf16, void* workspace,
+                                     size_t workspace_bytes, step5_stream_t stream);
+
+/* A serving step's plan: from each sequence's tokens in the cache and the tokens it gets, the pages it takes or
+ * gives back, and the rows' sequences and positions as the calls above take them.  Nothing passes the host, so that a
+ * captured graph can run step after step.  Of sequence b, in the order of the sequences:
+ *   row_start[b] = sum of new_tokens[0 .. b), at most N (row_start [B + 1]: the last is the sum of all)
+ *   want         = ceil((lengths[b] + new_tokens[b]) / page_tokens)
+ *   want < held_pages[b]: the table's entries want .. held_pages[b] - 1 go onto the stack free_pages
+ *           [num_pages] (entries 0 .. free_count[0] - 1, the last its top)
+ *   want > held_pages[b]: the entries held_pages[b] .. want - 1 are taken off it
+ *   granted[b] = new_tokens[b], or 0 where the free pages do not suffice
+ *   ends[b] = lengths[b] + granted[b];  held_pages[b] = want, unless nothing was granted for want of pages
+ *   region_begin[b] = lengths[b] / region_tokens, region_end[b] = ends[b] / region_tokens (the regions that the
+ *           step completes, as step5_region_summarize takes them)
+ *   rows row_start[b] .. row_start[b] + new_tokens[b] - 1: row_seq = b, row_pos = lengths[b] + 0, 1, ...; both
+ *           -1 (padding) where nothing was granted, and behind the last row
+ * Pages given back come first, sequence after sequence in the table's order; the pages taken are then the stack's
+ * topmost, handed out from the lowest of them on in the order of the sequences and of their tables.  From the first
+ * sequence whose need is not met on, no sequence that needs pages gets any (none is passed over for long).  So a
+ * step that is rolled back (the same lengths, no new tokens) puts the stack back as it was, and a sequence that is
+ * through gives its pages back at length 0.  Table entries at or past held_pages[b] are left as they were.
+ * A sequence out of range (a negative length or count, tokens past table_len * page_tokens, held_pages outside
+ * [0, table_len]) or whose rows end past N keeps its pages, is granted nothing and sets STEP5_DEV_RANGE, as do a
+ * free_count outside [0, num_pages], more pages given back than the stack has room for (those are lost) and page
+ * numbers outside [0, num_pages] (which are moved as they are).  ends may be the same buffer as lengths; the others lie apart.
+ * All pointers are device pointers; block_table is required.  N <= 2^24 rows, B <= 8192 sequences. */
+step5_status step5_paged_plan(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
+                              const int32_t* lengths, const int32_t* new_tokens, int32_t* block_table,
+                              int32_t* held_pages, int32_t* free_pages, int32_t* free_count, int32_t* row_seq,
+                              int32_t* row_pos, int32_t* row_start, int32_t* ends, int32_t* granted,
+                              int32_t* region_begin, int32_t* region_end, step5_stream_t stream);
+
+/* Bytes of device workspace that the attention calls over a pool need, whatever N,
  * the pool and the lengths.  Returns 0 for an unsupported geometry. */
 size_t step5_paged_workspace_bytes(const step5_geometry* geom);
 

@@ -1,0 +1,77 @@
+"""The bf16 paged cache's attention and the step's plan without a GPU: every bad argument is refused on the
+host before anything is enqueued, and the binding checks types, shapes and devices."""
+import ctypes
+
+import pytest
+import torch
+
+from test_paged_boundary import FAKE, ODD, s5  # noqa: F401
+
+
+def attend(s5, sparse, geom=None, pages=(8, 64, 4), N=1, B=1, window=0, q=FAKE, qs=4096, kp=FAKE, vp=FAKE, table=FAKE,  # noqa: F811
+           seq=FAKE, pos=FAKE, ids=FAKE, cnt=FAKE, gate=None, out=FAKE, ws=FAKE, nbytes=None):
+    geom = geom or s5.STEP5_GEOMETRY
+    pg = None if pages is None else ctypes.byref(s5.Pages(*pages))
+    nbytes = s5.step5_paged_workspace_bytes(geom) if nbytes is None else nbytes
+    g = ctypes.byref(geom)
+    if sparse:
+        return s5.load().step5_sparse_attn_paged(g, pg, N, B, q, qs, kp, vp, table, seq, pos, ids, cnt, gate, out, ws, nbytes, None)
+    return s5.load().step5_paged_attn(g, pg, N, B, window, q, qs, kp, vp, table, seq, pos, gate, out, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("bad, want", [
+    (dict(pages=None), 1), (dict(pages=(8, 12, 4)), 1), (dict(pages=(-1, 64, 4)), 1),
+    (dict(pages=(1 << 24, 64, 4)), 1), (dict(pages=(8, 64, 1 << 26)), 1), (dict(table=None), 1),
+    (dict(N=0), 1), (dict(B=0), 1), (dict(N=65536), 2),
+    (dict(q=None), 1), (dict(kp=None), 1), (dict(vp=None), 1), (dict(seq=None), 1), (dict(pos=None), 1), (dict(out=None), 1),
+    (dict(q=ODD), 1), (dict(kp=ODD), 1), (dict(vp=ODD), 1), (dict(out=ODD), 1), (dict(ws=ODD), 1),
+    (dict(qs=4088), 1), (dict(qs=4100), 1), (dict(qs=0), 1), (dict(qs=-4096), 1),
+    (dict(ws=None), 3), (dict(nbytes=0), 3), (dict(nbytes=16), 3),
+])
+def test_attention_refusals(s5, sparse, bad, want):  # noqa: F811
+    assert attend(s5, sparse, **bad) == want
+
+
+def test_more_refusals(s5):  # noqa: F811
+    assert attend(s5, False, window=-1) == 1
+    assert attend(s5, True, ids=None) == 1 and attend(s5, True, cnt=None) == 1
+    bad = s5.Geometry.step5(head_dim=64)
+    assert attend(s5, False, geom=bad, nbytes=1 << 30) == 2 and attend(s5, True, geom=bad, nbytes=1 << 30) == 2
+    assert s5.load().step5_paged_attn(None, None, 1, 1, 0, *[None] * 1, 0, *[None] * 8, 0, None) == 1
+
+
+PLAN = ("lengths", "new", "table", "held", "free_pages", "free_count", "row_seq", "row_pos", "row_start", "ends", "granted",
+        "region_begin", "region_end")
+
+
+def plan(s5, geom=None, pages=(8, 64, 4), N=4, B=2, **over):  # noqa: F811
+    pg = None if pages is None else ctypes.byref(s5.Pages(*pages))
+    return s5.load().step5_paged_plan(ctypes.byref(geom or s5.STEP5_GEOMETRY), pg, N, B, *(over.get(n, FAKE) for n in PLAN), None)
+
+
+@pytest.mark.parametrize("bad, want", [(dict(pages=None), 1), (dict(pages=(0, 64, 4)), 1), (dict(pages=(8, 60, 4)), 1),
+                                       (dict(pages=(8, 64, 1 << 26)), 1), (dict(N=0), 1), (dict(B=0), 1),
+                                       (dict(N=(1 << 24) + 1), 2), (dict(B=8193), 2)] + [({n: None}, 1) for n in PLAN])
+def test_plan_refusals(s5, bad, want):  # noqa: F811
+    assert plan(s5, **bad) == want
+
+
+def test_plan_without_a_table_is_refused(s5):  # noqa: F811
+    assert plan(s5, table=None, pages=(8, 64, 1)) == 1
+
+
+def test_the_binding_checks_kinds_and_devices(s5):  # noqa: F811
+    geom = s5.STEP5_GEOMETRY
+    k = torch.zeros((2, 4, 64, 128), dtype=torch.bfloat16)
+    cache = s5.PagedCache(k, k.clone())
+    q, out = (torch.zeros((1, 32, 128), dtype=torch.bfloat16) for _ in range(2))
+    row = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        s5.step5_paged_attn(geom, q, cache, row, row, out, None)
+    table = s5.PagedTable.create(4, 64, 2, 1, device="cpu")
+    rows = s5.PagedRows.create(1, 4, device="cpu")
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        s5.step5_paged_plan(table, rows, row, row)
+    assert table.free_pages.tolist() == [3, 2, 1, 0] and table.free_count.tolist() == [4]
+    assert rows.row_start.shape == (2,) and rows.row_seq.shape == (4,)
