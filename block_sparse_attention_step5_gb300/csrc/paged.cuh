@@ -82,8 +82,9 @@ cudaError_t launch_paged_attention(const PagedAttnParams& p, const CUtensorMap& 
 cudaError_t launch_paged_chunk(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
                                cudaStream_t stream, bool pdl);
 
-// Over bf16 pools: a (row, group)'s keys, all of its window's or those of its picks.
-cudaError_t launch_paged_attention_bf16(const PagedAttnParams& p, int num_sms, cudaStream_t stream, bool pdl);
+// The same over bf16 pools; kmap, vmap: the pools as [regions][2 halves][8 tokens][64 dims], boxes of box_regions, 128-byte swizzle.
+cudaError_t launch_paged_attention_bf16(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                        int num_sms, cudaStream_t stream, bool pdl);
 
 struct PlanParams {
     const int32_t* lengths;      // [B] tokens that each sequence has in the cache

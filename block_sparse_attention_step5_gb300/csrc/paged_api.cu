@@ -35,6 +35,19 @@ bool encode_pool_map(CUtensorMap* map, const void* base, uint64_t rows, int box_
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A bf16 pool as [regions][2 halves of the dims][8 tokens][64 dims], boxes of box_regions regions, 128-byte swizzle.
+bool encode_bf16_map(CUtensorMap* map, const void* base, uint64_t regions, int box_regions) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {64, 8, 2, regions};
+    cuuint64_t strides[3] = {256, 128, 2048};
+    cuuint32_t box[4] = {64, 8, 2, (cuuint32_t)box_regions};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t rot_dims,
                          int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride, const void* k_bf16,
                          int64_t k_stride, const void* v_bf16, int64_t v_stride, const int32_t* row_seq,
@@ -170,7 +183,11 @@ step5_status attend_bf16_impl(const step5_geometry* geom, const step5_pages* pag
                                          nullptr, block_table, row_seq, row_pos, sel_ids, sel_count, gate, out_bf16,
                                          workspace, workspace_bytes);
     if (s != STEP5_OK) return s;
-    const cudaError_t e = launch_paged_attention_bf16(p, num_sms(), (cudaStream_t)stream, true);
+    CUtensorMap kmap, vmap;
+    const uint64_t regions = (uint64_t)pages->num_pages * geom->num_kv_groups * (pages->page_tokens / 8);
+    if (!encode_bf16_map(&kmap, k_pages, regions, p.box_regions) || !encode_bf16_map(&vmap, v_pages, regions, p.box_regions))
+        return STEP5_ERR_CUDA;
+    const cudaError_t e = launch_paged_attention_bf16(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
     return e == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 

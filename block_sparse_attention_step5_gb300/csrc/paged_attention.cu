@@ -40,13 +40,12 @@
 //   16 rows of 512 picks       23.7 us  the copies alone 22.3 (68 MB in boxes of 1 KB)
 //   2,048 rows of 512 picks   1,135 us  the copies alone 934: 8.6 GB in boxes of 1 KB out of L2,
 //                                       one in 32 cycles on each SM
-#include "paged_device.cuh"
+#include "paged_items.cuh"
 
 namespace step5 {
 
 namespace {
 
-constexpr int kTile = 16;            // regions of a tile
 constexpr int kSoft = 128;           // softmax threads
 constexpr int kThreads = kSoft + 64 + 64;
 constexpr int kQkWarp = 4, kLoadWarp = 6, kLoadWarps = 2;  // (the second product's warp is 5)
@@ -77,79 +76,12 @@ struct Shape {
     static constexpr int kState = H * 130;             // floats of a partial state: m[H], l[H], o[H][128]
 };
 
-// Reduction of NV values per lane (a power of two <= 32) over the warp, one shuffle per halving:
-// lane pairs split the values between them.  *idx: which value this lane ends up with.
-template <int NV, int M, class Op>
-__device__ __forceinline__ float fold(float* w, int lane, int* idx, Op op) {
-    if constexpr (M == 0) {
-        return w[0];
-    } else if constexpr (NV > 1) {
-        const bool up = (lane & M) != 0;
-#pragma unroll
-        for (int j = 0; j < NV / 2; ++j) {
-            const float send = up ? w[j] : w[j + NV / 2];
-            const float keep = up ? w[j + NV / 2] : w[j];
-            w[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, M));
-        }
-        if (up) *idx += NV / 2;
-        return fold<NV / 2, M / 2>(w, lane, idx, op);
-    } else {
-        w[0] = op(w[0], __shfl_xor_sync(0xffffffffu, w[0], M));
-        return fold<1, M / 2>(w, lane, idx, op);
-    }
-}
-struct Max {
-    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
-};
-struct Add {
-    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
-};
-
-// An item: the keys of row n in group g, tiles of 16 entries.  Without picks entry e is region
-// r0 + e (r0 a multiple of the box), with picks the e-th pick and the own region behind them.
-struct Item {
-    int n, g;
-    int b;               // sequence; -1: padding (no tiles), -2: out of range (one empty tile, its output zero)
-    int lo, hi;          // first and last token
-    int r0, entries, tiles;
-};
-
-template <bool PICKS>
-__device__ __forceinline__ Item item_at(const PagedAttnParams& p, int i) {
-    Item it;
-    it.g = i / p.N;
-    it.n = i - it.g * p.N;
-    it.b = p.row_seq[it.n];
-    it.hi = p.row_pos[it.n];
-    it.lo = it.r0 = it.entries = it.tiles = 0;
-    if (it.b == -1) return it;
-    if (it.b < 0 || it.b >= p.B || it.hi < 0 || it.hi >= p.pages.page_tokens * p.pages.table_len) {  // (fits int32)
-        it.b = -2;
-        it.tiles = 1;
-        return it;
-    }
-    if (PICKS) {
-        it.entries = min(max(p.sel_count[(int64_t)it.n * p.G + it.g], 0), p.top_k) + 1;
-    } else {
-        it.lo = p.window > 0 ? max(0, it.hi - p.window + 1) : 0;
-        it.r0 = (it.lo >> 3) & ~(p.box_regions - 1);
-        it.entries = (it.hi >> 3) - it.r0 + 1;
-    }
-    it.tiles = (it.entries + kTile - 1) / kTile;
-    return it;
-}
-
 // What the softmax needs of a region of the tile.
 struct __align__(16) Meta {
     float ks, vs;
     uint32_t mask;    // its tokens that the row sees
     uint32_t loaded;  // 1: a copy brings its codes
 };
-
-// The output v of a (row, head), number `at` of them, through its gate.
-__device__ __forceinline__ float gated(const PagedAttnParams& p, int64_t at, float v) {
-    return v * (1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at]))));
-}
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, S::kCtas)
@@ -169,10 +101,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __shared__ int s_note[kRing];  // of a tile: MMA steps | first tile of a segment << 8
     __shared__ float red[3][4][H + 1];
     __shared__ __align__(16) float s_cq[2][H];
-    __shared__ int64_t s_scan[kThreads / 32];
-    __shared__ int s_tiles[kThreads], s_item, s_off, s_run, s_first, s_last;
-    __shared__ Item s_it;  // item s_item
-    __shared__ uint32_t s_ctas[kThreads / 32][32];
+    __shared__ RunSmem<kThreads> rs;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int items = p.N * p.G;
@@ -204,106 +133,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     pdl_wait();
     pdl_launch_dependents();
 
-    // This CTA's run of tiles, from tile off0 of item item0 on.
-    int64_t start = 0, per = 1;  // (many items: the run's first tile among all, tiles of a run)
-    const bool few = 2 * items <= (int)gridDim.x;
-    if (few) {
-        // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the
-        // smallest L of 32 tried that needs no more CTAs than there are (2 L0 always does).  No CTA
-        // then has parts of two items. (fewer than 2^8 items of at most 2^24 tiles)
-        Item own{};
-        if (tid < items) own = item_at<PICKS>(p, tid);
-        const uint32_t mine = (uint32_t)own.tiles;
-        s_tiles[tid] = own.tiles;
-        const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) s_scan[warp] = sum;
-        if (tid == 0) s_run = 0;
-        __syncthreads();
-        uint32_t total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) total += (uint32_t)s_scan[w];
-        const uint32_t least = max(1u, total / gridDim.x + (total % gridDim.x ? 1u : 0u));
-        uint32_t most = least + (least * (uint32_t)lane + 30u) / 31u;  // this lane's L
-        uint32_t ctas = 0;
-        for (int i = warp; i < items; i += kThreads / 32) ctas += ((uint32_t)s_tiles[i] + most - 1u) / most;
-        s_ctas[warp][lane] = ctas;
-        __syncthreads();
-        ctas = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) ctas += s_ctas[w][lane];
-        most = __shfl_sync(0xffffffffu, most, __ffs(__ballot_sync(0xffffffffu, ctas <= gridDim.x)) - 1);
-        const int parts = (int)((mine + most - 1u) / most);
-        int inc = parts;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        int first = inc - parts;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w)
-            if (w < warp) first += (int)s_scan[w];
-        const int part = (int)blockIdx.x - first;
-        if (part >= 0 && part < parts) {
-            s_item = tid;
-            s_it = own;
-            const uint32_t each = mine / (uint32_t)parts, more = mine % (uint32_t)parts;  // (the first ones take one more)
-            s_off = (int)((uint32_t)part * each + min((uint32_t)part, more));
-            s_run = (int)(each + ((uint32_t)part < more ? 1u : 0u));
-            s_first = first;
-            s_last = first + parts - 1;
-            if (part == 0) p.shared_items[tid] = make_int4(0, 0, 0, -1);  // (again below if it has several parts)
-        }
-        if (blockIdx.x == 0 && tid < items && mine == 0) p.shared_items[tid] = make_int4(0, 0, 0, -1);
-    } else {
-        // Many: the items' tiles are laid end to end and every CTA takes an equal run of them.
-        if (tid == 0) {
-            p.shared_items[blockIdx.x] = make_int4(0, 0, 0, -1);  // (again below if an item that other CTAs share begins here)
-            s_run = 0;
-        }
-        const int chunk = (items + kThreads - 1) / kThreads;
-        const int i0 = min(items, tid * chunk), i1 = min(items, i0 + chunk);
-        int64_t sum = 0;
-        for (int i = i0; i < i1; ++i) sum += item_at<PICKS>(p, i).tiles;
-        int64_t inc = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
-        }
-        if (lane == 31) s_scan[warp] = inc;
-        __syncthreads();
-        int64_t before = inc - sum, total = 0;
-#pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += s_scan[w];
-            total += s_scan[w];
-        }
-        per = (total + gridDim.x - 1) / gridDim.x;
-        start = blockIdx.x * per;
-        if (start >= before && start < before + sum) {
-            int64_t at = before;
-            for (int i = i0; i < i1; ++i) {
-                const Item it = item_at<PICKS>(p, i);
-                const int t = it.tiles;
-                if (start < at + t) {
-                    s_item = i;
-                    s_it = it;
-                    s_off = (int)(start - at);
-                    s_run = (int)min(per, total - start);
-                    break;
-                }
-                at += t;
-            }
-        }
-    }
+    int64_t start, per;
+    const bool few = take_run<PICKS, kThreads>(p, rs, start, per);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
-    const int run = s_run, item0 = s_item, off0 = s_off;
+    const int run = rs.run, item0 = rs.item, off0 = rs.off;
 
     if (run == 0) {
         // nothing to do
@@ -407,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (t < run) {
                 const bool first = in_seg == 0;
                 if (first) {  // the next segment
-                    it = s_it;
+                    it = rs.it;
                     if (t > 0) {
                         it.tiles = 0;
                         while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
@@ -632,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             }
             if (!whole && begins && tid == 0) {
                 if (few)
-                    p.shared_items[item0] = make_int4(done.n, done.g, s_first, s_last);
+                    p.shared_items[item0] = make_int4(done.n, done.g, rs.first, rs.last);
                 else
                     p.shared_items[blockIdx.x] = make_int4(done.n, done.g, (int)blockIdx.x, (int)((done_begin + done.tiles - 1) / per));
             }
@@ -640,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
 
         int segs = 0, nitem = item0, off = off0;
         for (int left = run; left > 0;) {
-            it = s_it;
+            it = rs.it;
             if (t > 0) {
                 it.tiles = 0;
                 while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
@@ -812,70 +648,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 0) tc::dealloc(tmem, S::kCols);
-}
-
-// Joins the items that CTAs of the launch before shared: a block per (entry of shared_items, head),
-// its threads' groups of 128 dims taking every GROUPS-th state, eight of them asked for before the
-// weights are known (the states lie in L2; the join is latency, not bandwidth).  The sums run in an
-// order fixed by the CTAs.
-// Eight groups for few blocks, two for many (one row of 4,608 tokens: 9.3 us in all against 11.4 with
-// two; 16 rows of 512 picks: 23.7 against 28.8 with eight).
-template <class S, int GROUPS>
-__global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
-    __shared__ float sw[kPagedMaxCtas], sm[GROUPS * 4], so[GROUPS][128], sl[GROUPS];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int c = blockIdx.y, tid = threadIdx.x, d = tid & 127, grp = tid >> 7;
-    const int4 item = p.shared_items[blockIdx.x];
-    const int first = item.z, n = item.w - first + 1;
-    if (item.w < 0) return;
-    auto state = [&](int i) { return p.states + ((int64_t)2 * (first + i) + (i == 0 ? 1 : 0)) * S::kState; };
-    constexpr int kDeep = 8;
-    float v[kDeep];
-#pragma unroll
-    for (int x = 0; x < kDeep; ++x) v[x] = grp + x * GROUPS < n ? state(grp + x * GROUPS)[2 * S::H + c * 128 + d] : 0.0f;
-    // the states' weights 2^(m - M) l
-    float M = -INFINITY;
-    for (int i = tid; i < n; i += 128 * GROUPS)
-        if (state(i)[S::H + c] != 0.0f) M = fmaxf(M, state(i)[c]);
-#pragma unroll
-    for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-    if ((tid & 31) == 0) sm[tid >> 5] = M;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < GROUPS * 4; ++x) M = fmaxf(M, sm[x]);
-    for (int i = tid; i < n; i += 128 * GROUPS) {
-        const float l = state(i)[S::H + c];
-        sw[i] = l == 0.0f ? 0.0f : ex2(state(i)[c] - M) * l;
-    }
-    __syncthreads();
-    float o = 0.0f, w = 0.0f;
-#pragma unroll
-    for (int x = 0; x < kDeep; ++x)
-        if (grp + x * GROUPS < n) {
-            o = fmaf(sw[grp + x * GROUPS], v[x], o);
-            w += sw[grp + x * GROUPS];
-        }
-#pragma unroll 8
-    for (int i = grp + kDeep * GROUPS; i < n; i += GROUPS) {
-        o = fmaf(sw[i], state(i)[2 * S::H + c * 128 + d], o);
-        w += sw[i];
-    }
-    so[grp][d] = o;
-    if (d == 0) sl[grp] = w;
-    __syncthreads();
-    if (grp == 0) {
-        o = w = 0.0f;
-#pragma unroll
-        for (int x = 0; x < GROUPS; ++x) {
-            o += so[x][d];
-            w += sl[x];
-        }
-        const int64_t at = (int64_t)item.x * p.Hq + (int64_t)item.y * S::H + c;
-        o = w == 0.0f ? 0.0f : o / w;
-        if (p.gate != nullptr && w != 0.0f) o = gated(p, at, o);
-        p.out[at * 128 + d] = f32_to_bf16_bits(o);
-    }
 }
 
 template <class S>
