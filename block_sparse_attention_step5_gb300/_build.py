@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libstep5sa.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = ["step5_api.cu", "summarize.cu", "score_select.cu", "attention.cu", "noalloc.cu", "front.cu", "shard.cu", "attention_shard.cu", "attention_tc.cu", "score_tc.cu",
-           "kv_append.cu", "paged_attention.cu", "paged_chunk.cu", "paged_attention_bf16.cu", "paged_plan.cu", "paged_api.cu"]
+           "kv_append.cu", "paged_attention.cu", "paged_chunk.cu", "paged_attention_bf16.cu", "paged_chunk_bf16.cu", "paged_plan.cu", "paged_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

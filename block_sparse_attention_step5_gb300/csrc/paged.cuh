@@ -85,6 +85,10 @@ cudaError_t launch_paged_chunk(const PagedAttnParams& p, const CUtensorMap& kmap
 // The same over bf16 pools; kmap, vmap: the pools as [regions][2 halves][8 tokens][64 dims], boxes of box_regions, 128-byte swizzle.
 cudaError_t launch_paged_attention_bf16(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                                         int num_sms, cudaStream_t stream, bool pdl);
+// The same for launches whose sequences have several rows (no picks); qmap: q as [2 halves][N][Hq][64 dims], boxes of a
+// group's heads of 128 / heads rows.
+cudaError_t launch_paged_chunk_bf16(const PagedAttnParams& p, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                                    const CUtensorMap& vmap, int num_sms, cudaStream_t stream, bool pdl);
 
 struct PlanParams {
     const int32_t* lengths;      // [B] tokens that each sequence has in the cache

@@ -48,6 +48,19 @@ bool encode_bf16_map(CUtensorMap* map, const void* base, uint64_t regions, int b
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of q as [2 halves of the dims][rows][heads][64 dims], boxes of `rows` rows of a group's heads, 128-byte swizzle.
+bool encode_q_map(CUtensorMap* map, const PagedAttnParams& p, int rows) {
+    auto enc = get_encode();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {64, (cuuint64_t)p.Hq, (cuuint64_t)p.N, 2};
+    cuuint64_t strides[3] = {256, (cuuint64_t)p.q_stride * 2, 128};
+    cuuint32_t box[4] = {64, (cuuint32_t)(p.Hq / p.G), (cuuint32_t)rows, 2};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p.q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t rot_dims,
                          int32_t t_cap, const void* q_bf16_or_null, int64_t q_stride, const void* k_bf16,
                          int64_t k_stride, const void* v_bf16, int64_t v_stride, const int32_t* row_seq,
@@ -187,7 +200,15 @@ step5_status attend_bf16_impl(const step5_geometry* geom, const step5_pages* pag
     const uint64_t regions = (uint64_t)pages->num_pages * geom->num_kv_groups * (pages->page_tokens / 8);
     if (!encode_bf16_map(&kmap, k_pages, regions, p.box_regions) || !encode_bf16_map(&vmap, v_pages, regions, p.box_regions))
         return STEP5_ERR_CUDA;
-    const cudaError_t e = launch_paged_attention_bf16(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
+    const int64_t hq = geom->num_q_heads / geom->num_kv_groups, head_rows = N * hq;
+    cudaError_t e;
+    if (sel_ids == nullptr && head_rows >= 64 * (int64_t)B && head_rows >= 128) {
+        CUtensorMap qmap;
+        if (!encode_q_map(&qmap, p, (int)(128 / hq))) return STEP5_ERR_CUDA;
+        e = launch_paged_chunk_bf16(p, qmap, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
+    } else {
+        e = launch_paged_attention_bf16(p, kmap, vmap, num_sms(), (cudaStream_t)stream, true);
+    }
     return e == cudaSuccess ? STEP5_OK : STEP5_ERR_CUDA;
 }
 
