@@ -200,9 +200,14 @@ step5_status attend_bf16_impl(const step5_geometry* geom, const step5_pages* pag
     const uint64_t regions = (uint64_t)pages->num_pages * geom->num_kv_groups * (pages->page_tokens / 8);
     if (!encode_bf16_map(&kmap, k_pages, regions, p.box_regions) || !encode_bf16_map(&vmap, v_pages, regions, p.box_regions))
         return STEP5_ERR_CUDA;
+    // Rows of a sequence share its keys' tiles from 128 head rows a sequence on; below, up to four of them read its keys
+    // together.  With 8 heads a group, microseconds shared and not: one sequence's 16 rows behind 8,192 tokens 30 and 21, behind
+    // 32,768 40 and 43, its 32 rows 31 and 32, 42 and 82; 8 rows of each of 8 of 32,768 168 and 153, of each of 16 306 and 340.  With 16
+    // heads, 8 rows of each of 4 of 8,192 43 and 49, of 32,768 98 and 148, 4 rows of each of 8 62 and 53, 168 and 149; with 4
+    // heads, 32 rows of one 31 and 26, 41 and 72, 8 of each of 16 101 and 81.
     const int64_t hq = geom->num_q_heads / geom->num_kv_groups, head_rows = N * hq;
     cudaError_t e;
-    if (sel_ids == nullptr && head_rows >= 64 * (int64_t)B && head_rows >= 128) {
+    if (sel_ids == nullptr && head_rows >= 128 * (int64_t)B) {
         CUtensorMap qmap;
         if (!encode_q_map(&qmap, p, (int)(128 / hq))) return STEP5_ERR_CUDA;
         e = launch_paged_chunk_bf16(p, qmap, kmap, vmap, num_sms(), (cudaStream_t)stream, true);

@@ -60,7 +60,7 @@ constexpr float kPTop = 32.0f;       // weights are split from p * 2^(8 - slack)
 // 10.2 with three; 16 rows 23.7 against 23.4).
 template <int H_, bool PICKS_, bool MANY_>
 struct Shape {
-    static constexpr int H = H_;                       // query heads of a group
+    static constexpr int H = H_, C = H_;               // query heads of a group, columns of an item
     static constexpr bool PICKS = PICKS_;
     static constexpr int NS = 2 * H < 16 ? 16 : 2 * H;
     static constexpr int NO = (3 * H + 15) / 16 * 16;

@@ -1,19 +1,34 @@
-// paged_attention_bf16.cu -- attention over the bf16 paged cache, rows on their own: every token of a causal window,
+// paged_attention_bf16.cu -- attention over the bf16 paged cache for few rows a sequence: every token of a causal window,
 // or the picked regions plus the row's own.
 //
 //   s_t = softmax_scale (q . k_t),  p = softmax(s),  out = sum_t p_t v_t
 //
-// As over the e4m3 pages, 128 keys are the M side of both products and the H heads of a row the small one,
+// As over the e4m3 pages, 128 keys are the M side of both products, and the C columns of an item the small one: the H heads of R
+// rows (1, or 2 or 4 neighbouring rows of the call, which mostly are one sequence's drafts and read its keys once),
 //
-//   S^T [128 keys x H]    = K_tile [128 x 128 dims]        . q^T            (two TMEM buffers)
-//   O^T [128 dims x 2 H] += V_tile^T [128 dims x 128 keys] . (p parts)^T
+//   S^T [128 keys x C]    = K_tile [128 x 128 dims]        . q^T            (two TMEM buffers)
+//   O^T [128 dims x 2 C] += V_tile^T [128 dims x 128 keys] . (p parts)^T
 //
-// with bf16 operands as the cache has them.  A weight has 8 bits in bf16; its rounding error goes along as a second part, more columns of
+// with bf16 operands as the cache has them.  A weight has 8 bits in bf16; what its first part leaves goes along as a second part, more columns of
 // the small side, which cost nothing, so 16 bits of each weight meet V.  A region (8 tokens x 256 B) lands as two swizzle atoms,
 // [half of the dims][8 tokens][128 B], from one box of a 4-D view of the pool (64 dims x 8 tokens x 2 halves x regions): the K-major
 // operand of the first product and the MN-major one of the second.
 //
-// The split of the work, the roles of the warps and the join are those of the kernel over the e4m3 pages.
+// An item of several rows walks the keys of each of its sequences in turn, the other rows masked.  A weight of zero must meet a
+// finite value: a V row that no row sees is zeroed, and where some rows see it and others do not, what is not finite in it is
+// cleared and the token noted; the rows that see it take it up again from the page at their end.
+//
+// The split of the work, the roles of the warps and the join are those of the kernel over the e4m3 pages.  A tile is 64 KB, so one
+// CTA an SM with 5 or 6 of them half in flight keeps HBM busy; picks, whose copies are 2 KB each, want two CTAs (a CTA's copies of
+// that size come at 44 GB/s out of L2, two CTAs' at 87).
+//
+// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens, join included:
+//   one row of 4,608 tokens       10 us  latency: split, page and key loads, one tile, second product and states, join
+//   16 rows of 16K to 32K        129 us  805 MB, 6.2 TB/s: HBM
+//   8 x 4 rows behind 6K to 8K    35 us  116 MB in copies of 2 KB (pages of 24 tokens): their rate, start and join
+//   one row of 512 picks        11.3 us  latency, as the short row
+//   16 rows of 512 picks          31 us  134 MB in copies of 2 KB out of HBM, 4.3 TB/s
+//   2,048 rows of 512 picks    1,310 us  17.2 GB of copies of 2 KB out of L2, 13.1 TB/s of the 13.7 that L2 gives copies of any size
 #include "paged_items.cuh"
 
 namespace step5 {
@@ -27,30 +42,37 @@ constexpr int kRing = 8;             // tiles whose masks are in shared memory
 constexpr uint32_t kRegionBytes = 2048, kSlotBytes = kTile * kRegionBytes;
 constexpr float kSlack = 8.0f;       // log2 units a tile's maximum may pass the running one by
 
-template <int H_, bool PICKS_, int CTAS_>
+constexpr float kNone = 3.0e38f;     // less the running maximum of a head without keys so far (finite: scores may be -infinity)
+
+template <int H_, int R_, bool PICKS_, int CTAS_>
 struct Shape {
-    static constexpr int H = H_;                       // query heads of a group
+    static constexpr int H = H_, R = R_, C = H * R;    // query heads of a group, rows of an item, columns: heads of row after row
     static constexpr bool PICKS = PICKS_;
     static constexpr int kCtas = CTAS_;                // per SM
-    static constexpr int kSlots = CTAS_ == 1 ? 6 : 3;
+    static constexpr int kSlots = CTAS_ == 2 ? 3 : C == 32 ? 5 : 6;
     static_assert(kSlots <= 6, "the barriers of copies and the ring are reused after 4 and 8 tiles");
-    static constexpr int NS = 16;                      // columns of S: the heads
-    static constexpr int NO = 2 * H < 16 ? 16 : 2 * H; // columns of O: the weights' two parts
-    static constexpr uint32_t kCols = 64;
+    static constexpr int NS = C < 16 ? 16 : C;         // columns of S
+    static constexpr int NO = 2 * C < 16 ? 16 : 2 * C; // columns of O: the weights' two parts
+    static constexpr uint32_t kCols = 2 * NS + NO <= 64 ? 64 : 128;
     static constexpr uint32_t kQBytes = NS * 256, kPBytes = 128 * NO * 2;
     static constexpr uint32_t kPGroup = 16 * NO;       // bytes of 8 keys of P
     static constexpr uint32_t kSmem = 1024 + kSlots * kSlotBytes + kQBytes + 2 * kPBytes;
     static constexpr uint32_t kIdesc1 = tc::instr_desc(tc::kFmtBF16, false, false, 128, NS);
     static constexpr uint32_t kIdesc2 = tc::instr_desc(tc::kFmtBF16, true, true, 128, NO);
-    static constexpr int kState = H * 130;             // floats of a partial state: m[H], l[H], o[H][128]
+    static constexpr int kState = C * 130;             // floats of a partial state: m[C], l[C], o[C][128]
     static_assert(2 * NS + NO <= (int)kCols, "tensor memory");
+    static_assert((size_t)kPagedMaxCtas * 2 * kState <= kPagedStateFloats, "workspace");
+    static_assert(C <= 32 && (R == 1 || !PICKS), "columns; picks are a row's own");
 };
+
+// What a tile's softmax and second product need to know of it: product steps, and ...
+enum : int { kFirst = 256, kRowsShift = 16 };  // the segment's first tile; the item's rows that its sequence is of
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, S::kCtas)
     paged_attn_bf16_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       PagedAttnParams p) {
-    constexpr int H = S::H;
+    constexpr int H = S::H, R = S::R, C = S::C;
     constexpr bool PICKS = S::PICKS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align_smem(smem_raw, 1024);
@@ -61,12 +83,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __shared__ uint32_t ring[kRing][kTile];  // of a region: its tokens that the row sees | 256 if a copy brings it
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
-    __shared__ int s_note[kRing];  // of a tile: MMA steps | first tile of a segment << 8
-    __shared__ float red[3][4][H];
+    __shared__ int s_note[kRing], s_t0[kRing];  // of a tile: product steps | kFirst | rows; (several rows) first token
+    __shared__ float red[3][4][C];
+    __shared__ int2 s_cleared[2];  // of segment i % 2 (several rows): first and last token whose values were cleared
     __shared__ RunSmem<kThreads> rs;
 
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int items = p.N * p.G;
+    const int items = (p.N + R - 1) / R * p.G;
 
     if (tid == 0) {
         prefetch_tmap(&kmap);
@@ -89,17 +112,18 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         s_fail = 0;
     }
     if (warp == 0) tc::alloc(&s_tmem, S::kCols);
-    if (H < S::NS)  // q rows that no head fills (softmax threads, which fence them below)
-        for (int i = tid; i < (S::NS - H) * 16; i += kSoft)
+    if (C < S::NS)  // q rows that no head fills (softmax threads, which fence them below)
+        for (int i = tid; i < (S::NS - C) * 16; i += kSoft)
             if (tid < kSoft) {
-                const int half = i / ((S::NS - H) * 8), r = i % ((S::NS - H) * 8);
-                reinterpret_cast<uint4*>(qt + half * S::NS * 128 + H * 128)[r] = make_uint4(0, 0, 0, 0);
+                constexpr int n = C < S::NS ? (S::NS - C) * 8 : 1;
+                const int half = i / n, r = i % n;
+                reinterpret_cast<uint4*>(qt + half * S::NS * 128 + C * 128)[r] = make_uint4(0, 0, 0, 0);
             }
     pdl_wait();
     pdl_launch_dependents();
 
     int64_t start, per;
-    const bool few = take_run<PICKS, kThreads>(p, rs, start, per);
+    const bool few = take_run<PICKS, kThreads, R>(p, rs, start, per);
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -125,12 +149,20 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // next four while these go by.
         int b_r = 0, b_row = -1, n_r = 0, n_row = -1, batch = -1, done = 0;
         const int32_t* ids = nullptr;
+        RowSet<R> set{};                 // (several rows) the item's, its sequences not yet walked, and this one
+        uint32_t todo = 0, rows = 1;
         auto look = [&](int of, int steps) {
             const int e = (of * 4 + (lane >> 3)) * kTile + q;
             if (steps & 1) {
                 n_r = -1;
                 if (PICKS) {
                     if (e < it.entries) n_r = e == it.entries - 1 ? it.hi >> 3 : ids[e];
+                } else if constexpr (R > 1) {  // with its box, of which some region is a row's (windows may leave gaps)
+                    const int z = it.r0 + e, t0 = (z & ~(k - 1)) * 8;
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (it.b >= 0 && (rows >> r & 1u) && t0 <= set.pos[r] && (p.window == 0 || t0 + 8 * k > set.pos[r] - p.window + 1))
+                            n_r = z;
                 } else if (it.b >= 0 && e < (it.entries + k - 1) / k * k && ((it.r0 + e) | (k - 1)) >= (it.lo >> 3)) {
                     n_r = it.r0 + e;  // (with its box, of which some region is the row's)
                 }
@@ -174,12 +206,16 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             if (!isv) {
                 // (this slot was free, so the softmax is past tile t - 5 and the ring's entry is free too)
                 if (lane >> 3 == (at & 3)) {
+                    // (several rows: which tokens a row sees is the softmax's business)
                     const int t0 = b_r * 8;
                     const int a = min(max(it.lo - t0, 0), 8), z = min(max(it.hi - t0 + 1, 0), 8);
                     const uint32_t mask = b_row >= 0 && z > a ? ((1u << z) - 1u) & ~((1u << a) - 1u) : 0u;
                     ring[t & (kRing - 1)][q] = mask | (b_row >= 0 ? 256u : 0u);
                 }
-                if (lw == 0 && lane == 0) s_note[t & (kRing - 1)] = note;
+                if (lw == 0 && lane == 0) {
+                    s_note[t & (kRing - 1)] = note;
+                    if (R > 1) s_t0[t & (kRing - 1)] = (it.r0 + at * kTile) * 8;
+                }
                 __syncwarp();
             }
             if (lane == 0) arrive(full);
@@ -196,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     it = rs.it;
                     if (t > 0) {
                         it.tiles = 0;
-                        while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+                        while (nitem < items && (it = item_of<PICKS, R>(p, nitem)).tiles <= off) ++nitem;
                     }
                     if (nitem >= items) {  // (the rows have changed under the kernel)
                         ok = false;
@@ -209,9 +245,22 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     left -= in_seg;
                     off = 0;
                     batch = -1, done = 0;
+                    if constexpr (R > 1) {
+                        set = rows_at<R>(p, it.n);
+                        todo = rows_with_keys(set);
+                        it.tiles = 0;  // (from here on those of the sequence)
+                    }
                 } else {
                     ++at;
                 }
+                if constexpr (R > 1)
+                    while (at >= it.tiles && todo) {  // the item's next sequence
+                        at -= it.tiles;
+                        const Pass a = next_pass<R>(p, set, todo);
+                        it.b = a.b, it.lo = a.lo, it.hi = a.hi, it.r0 = a.r0, it.entries = a.entries, it.tiles = a.tiles;
+                        rows = a.rows;
+                        batch = -1, done = 0;
+                    }
                 --in_seg;
                 if (batch != at >> 2) {
                     if (done != 3) look(at >> 2, 3 & ~done);
@@ -228,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 const int steps = it.b < 0 ? 0 : min(8, (it.entries - at * kTile + 1) >> 1);
                 // a box of several regions is copied whole or not at all; every entry of it has its row
                 nzero = (~got << (lw * 8)) & (0xffu << (lw * 8)) & ((1u << (2 * steps)) - 1u);
-                nnote = steps | (first ? 256 : 0);
+                nnote = steps | (first ? kFirst : 0) | (int)rows << kRowsShift;
                 put(false, nrow, nnote, 0, t);
             }
             if (t > 0 && ok) put(true, row, 0, zero, t - 1);
@@ -263,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             // of tile t overwrites); q of a segment's first tile is there.  Second: P_t is there.
             if (qk) {
                 if (t >= 2 && !wait(&obar[t & 1], (uint32_t)(((t - 2) >> 1) & 1))) ok = false;
-                if ((note & 256) && !wait(&qbar, (uint32_t)(seg++ & 1))) ok = false;
+                if ((note & kFirst) && !wait(&qbar, (uint32_t)(seg++ & 1))) ok = false;
             } else {
                 if (!wait(&pbar[t & 1], (uint32_t)((t >> 1) & 1))) ok = false;
             }
@@ -289,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                     for (int i = 0; i < 8; ++i)  // 16 keys (two regions) each
                         if (i < (note & 255))
                             tc::mma_f16(tmem + 2u * S::NS, da + (2u * kRegionBytes >> 4) * i, db + (S::kPGroup >> 3) * i, S::kIdesc2,
-                                        !(note & 256) || i > 0);
+                                        !(note & kFirst) || i > 0);
                     tc::commit(&obar[t & 1]);
                     tc::commit(&empty[slot]);
                 }
@@ -310,9 +359,11 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // ---------------- softmax warps: one key per thread (its TMEM lane)
         const int key = tid, q = key >> 3;
         const uint32_t lanes = tc::taddr(tmem, warp * 32, 0);
-        float2 neg_m[H / 2], l_part[H / 2];  // less the running maxima, the row sums of this thread's keys
+        float2 neg_m[C / 2], l_part[C / 2];  // less the running maxima, the row sums of this thread's keys
         Item it{}, done{};  // the segment's item; that of the segment before, for its epilogue
         int64_t done_begin = 0;
+        RowSet<R> set{}, done_set{};     // (several rows) theirs
+        int segs = 0;
         bool whole = true, begins = true;  // it has the whole item, its first tile
         bool failed = false;
         int t = 0;  // tile of the run
@@ -322,15 +373,17 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             atomicExch(&s_fail, 1);
         };
 
-        // The item's heads, 16 lanes to each.
+        // The item's columns, 16 lanes to each.
         auto build_q = [&] {
 #pragma unroll
-            for (int u0 = 0; u0 < H; u0 += 8) {
+            for (int u0 = 0; u0 < C; u0 += 8) {
                 const int u = u0 + (tid >> 4), d8 = tid & 15;
-                if (H < 8 && u >= H) break;  // (whole warps)
+                if (C < 8 && u >= C) break;  // (whole warps)
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (it.b >= 0)
-                    x = *reinterpret_cast<const uint4*>(p.q + (int64_t)it.n * p.q_stride + ((int64_t)it.g * H + u) * 128 + d8 * 8);
+                bool there = it.b >= 0;
+                if constexpr (R > 1) there = (rows_with_keys(set) >> (u / H) & 1u) != 0;
+                if (there)
+                    x = *reinterpret_cast<const uint4*>(p.q + (int64_t)(it.n + u / H) * p.q_stride + ((int64_t)it.g * H + u % H) * 128 + d8 * 8);
                 *reinterpret_cast<uint4*>(qt + (d8 >> 3) * S::NS * 128 + u * 128 + (((d8 & 7) ^ (u & 7)) << 4)) = x;
             }
             fence_proxy_async();
@@ -341,13 +394,13 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         // O of the segment that ended with tile t - 1, and its output or partial state.
         auto epilogue = [&] {
             const int tl = t - 1;
-            float(&rd)[4][H] = red[2];
-            int hidx = 0;
-            float l[H];
+            float(&rd)[4][C] = red[2];
+            int cidx = 0;
+            float l[C];
 #pragma unroll
-            for (int h = 0; h < H; ++h) l[h] = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
-            const float sum = fold<H, 16>(l, lane, &hidx, Add{});
-            if ((lane & (32 / H - 1)) == 0) rd[warp][hidx] = sum;
+            for (int c = 0; c < C; ++c) l[c] = c & 1 ? l_part[c / 2].y : l_part[c / 2].x;
+            const float sum = fold<C, 16>(l, lane, &cidx, Add{});
+            if ((lane & (32 / C - 1)) == 0) rd[warp][cidx] = sum;
             const bool w_ok = wait(&obar[tl & 1], (uint32_t)((tl >> 1) & 1));
             tc::fence_after_sync();
             if (!w_ok) give_up();
@@ -355,41 +408,57 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 failed = true;
                 return;
             }
-            float o[H], a[16];
-            const uint32_t ob = lanes + 2 * S::NS;
-            tc::ld16(ob, a);
-            if constexpr (H == 16) {
-                float b[16];
-                tc::ld16(ob + 16, b);
+            float o[C], L[C];
+            {
+                constexpr int n = C < 16 ? 16 : C;  // (fewer than 16 columns: both parts in one load)
+                float a[n], b[n];
+                const uint32_t ob = lanes + 2 * S::NS;
 #pragma unroll
-                for (int h = 0; h < H; ++h) o[h] = a[h] + b[h];
-            } else {
+                for (int c = 0; c < n; c += 16) {
+                    tc::ld16(ob + c, *reinterpret_cast<float(*)[16]>(a + c));
+                    if (C >= 16) tc::ld16(ob + C + c, *reinterpret_cast<float(*)[16]>(b + c));
+                }
 #pragma unroll
-                for (int h = 0; h < H; ++h) o[h] = a[h] + a[H + h];
+                for (int c = 0; c < C; ++c) o[c] = a[c] + (C >= 16 ? b[c] : a[(C + c) % n]);
             }
-            float L[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                L[h] = (rd[0][h] + rd[1][h]) + (rd[2][h] + rd[3][h]);
-                o[h] = L[h] == 0.0f ? 0.0f : o[h] / L[h];
+            for (int c = 0; c < C; ++c) {
+                L[c] = (rd[0][c] + rd[1][c]) + (rd[2][c] + rd[3][c]);
+                o[c] = L[c] == 0.0f ? 0.0f : o[c] / L[c];
+            }
+            if constexpr (R > 1) {  // values that were cleared, in the rows that see them
+                const int2 cl = s_cleared[(segs - 1) & 1];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int z = done_set.b[r] >= 0 ? min(cl.y, done_set.pos[r]) : -1;
+                    for (int tok = max(cl.x, p.window > 0 ? max(0, done_set.pos[r] - p.window + 1) : 0); tok <= z; ++tok) {
+                        const int64_t row = page_row(p.pages, p.G, done_set.b[r], done.g, tok);
+                        if (row < 0) continue;
+                        const float v = bf16_to_f32(reinterpret_cast<const uint16_t*>(p.v_pages)[row * 128 + key]);
+                        if (!(fabsf(v) < INFINITY))
+#pragma unroll
+                            for (int h = 0; h < H; ++h)
+                                if (L[r * H + h] != 0.0f) o[r * H + h] += v;
+                    }
+                }
             }
             if (whole) {
-                const int64_t at = (int64_t)done.n * p.Hq + (int64_t)done.g * H;
-                if (p.gate != nullptr)
 #pragma unroll
-                    for (int h = 0; h < H; ++h)
-                        if (L[h] != 0.0f) o[h] = gated(p, at + h, o[h]);  // (zero stays zero)
-#pragma unroll
-                for (int h = 0; h < H; ++h) p.out[(at + h) * 128 + key] = f32_to_bf16_bits(o[h]);
+                for (int c = 0; c < C; ++c) {
+                    const int64_t at = (int64_t)(done.n + c / H) * p.Hq + (int64_t)done.g * H + c % H;
+                    if (R > 1 && done_set.b[c / H] == -1) continue;
+                    if (p.gate != nullptr && L[c] != 0.0f) o[c] = gated(p, at, o[c]);  // (zero stays zero)
+                    p.out[at * 128 + key] = f32_to_bf16_bits(o[c]);
+                }
             } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
                 float* st = p.states + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState;
 #pragma unroll
-                for (int h = 0; h < H; ++h) st[2 * H + h * 128 + key] = o[h];
+                for (int c = 0; c < C; ++c) st[2 * C + c * 128 + key] = o[c];
                 if (key == 0)
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        st[h] = -(h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x);
-                        st[H + h] = L[h];
+                    for (int c = 0; c < C; ++c) {
+                        st[c] = -(c & 1 ? neg_m[c / 2].y : neg_m[c / 2].x);
+                        st[C + c] = L[c];
                     }
             }
             if (!whole && begins && tid == 0) {
@@ -405,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             it = rs.it;
             if (t > 0) {
                 it.tiles = 0;
-                while (nitem < items && (it = item_at<PICKS>(p, nitem)).tiles <= off) ++nitem;
+                while (nitem < items && (it = item_of<PICKS, R>(p, nitem)).tiles <= off) ++nitem;
             }
             if (nitem >= items) {
                 give_up();
@@ -413,11 +482,18 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 break;
             }
             ++nitem;
+            if constexpr (R > 1) set = rows_at<R>(p, it.n);
             build_q();
             if (t > 0) epilogue();
             if (failed) break;
             if (tid == 0) {
-                if (it.b == -2) raise_status(p.status, kDevRange);
+                if (R == 1 && it.b == -2) raise_status(p.status, kDevRange);
+                if constexpr (R > 1) {
+                    s_cleared[segs & 1] = make_int2(INT32_MAX, -1);  // (taken by segment segs - 2, which is through)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (set.b[r] == -2) raise_status(p.status, kDevRange);
+                }
                 if (PICKS && it.b >= 0) {
                     const int n = p.sel_count[(int64_t)it.n * p.G + it.g];
                     if (n < 0 || n > p.top_k) raise_status(p.status, kDevRange);
@@ -425,65 +501,77 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             }
             const int seg = min(it.tiles - off, left);
             done = it;
+            done_set = set;
+            ++segs;
             done_begin = start + (run - left) - off;
             whole = seg == it.tiles;
             begins = off == 0;
             left -= seg;
             off = 0;
 #pragma unroll
-            for (int h = 0; h < H / 2; ++h) {
-                neg_m[h] = both(INFINITY);
-                l_part[h] = both(0.0f);
+            for (int c = 0; c < C / 2; ++c) {
+                neg_m[c] = both(kNone);
+                l_part[c] = both(0.0f);
             }
             for (int i = 0; i < seg; ++i, ++t) {
                 // (tile t - 2's second product is done too: the first product of this one waited for it)
                 bool w_ok = wait(&sbar[t & 1], (uint32_t)((t >> 1) & 1));
                 tc::fence_after_sync();
                 const uint32_t me = ring[t & (kRing - 1)][q];
-                const bool sees = (me >> (key & 7) & 1u) != 0;
-                // s[h] = q . k in log2 units, y[h] that less the running maximum
-                float2 s[H / 2], y[H / 2];
-                {
-                    float x[16];
-                    tc::ld16(lanes + (uint32_t)(S::NS * (t & 1)), x);
+                uint32_t seen = me >> (key & 7) & 1u;  // the item's rows that see the key
+                if constexpr (R > 1) {
+                    const int tok = s_t0[t & (kRing - 1)] + key;
+                    const uint32_t rows = (uint32_t)s_note[t & (kRing - 1)] >> kRowsShift;
+                    seen = 0;
 #pragma unroll
-                    for (int h = 0; h < H; h += 2) s[h / 2] = mul2(make_float2(x[h], x[h + 1]), both(p.scale_log2));
+                    for (int r = 0; r < R; ++r)
+                        if ((me & 256u) && (rows >> r & 1u) && tok <= set.pos[r] && (p.window == 0 || tok > set.pos[r] - p.window)) seen |= 1u << r;
+                }
+                auto sees = [&](int c) { return (seen >> (c / H) & 1u) != 0; };
+                // s[c] = q . k in log2 units, y[c] that less the running maximum
+                float2 s[C / 2], y[C / 2];
+#pragma unroll
+                for (int c0 = 0; c0 < C; c0 += 16) {
+                    float x[16];
+                    tc::ld16(lanes + (uint32_t)(S::NS * (t & 1) + c0), x);
+#pragma unroll
+                    for (int c = 0; c < 16 && c < C; c += 2) s[(c0 + c) / 2] = mul2(make_float2(x[c], x[c + 1]), both(p.scale_log2));
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int h = 0; h < H; h += 2) {
-                    y[h / 2] = add2(s[h / 2], neg_m[h / 2]);
-                    top = fmaxf(top, fmaxf(y[h / 2].x, y[h / 2].y));
+                for (int c = 0; c < C; c += 2) {
+                    y[c / 2] = add2(s[c / 2], neg_m[c / 2]);
+                    if (sees(c)) top = fmaxf(top, fmaxf(y[c / 2].x, y[c / 2].y));
                 }
                 // The running maxima move when a key passes one by more than the slack; l and O are rescaled
                 // then.  Every softmax thread takes the same steps.
                 if (!w_ok) give_up();
-                if (__builtin_expect(group_or(1, kSoft, (sees && top > kSlack) || !w_ok), 0)) {
+                if (__builtin_expect(group_or(1, kSoft, top > kSlack || !w_ok), 0)) {
                     if (*reinterpret_cast<volatile int*>(&s_fail) != 0) failed = true;
-                    float alpha[H];
-                    int hidx = 0;
+                    float alpha[C];
+                    int cidx = 0;
 #pragma unroll
-                    for (int h = 0; h < H; ++h) alpha[h] = sees ? (h & 1 ? s[h / 2].y : s[h / 2].x) : -INFINITY;
-                    const float wmax = fold<H, 16>(alpha, lane, &hidx, Max{});
-                    float(&rd)[4][H] = red[t & 1];
-                    if ((lane & (32 / H - 1)) == 0) rd[warp][hidx] = wmax;
+                    for (int c = 0; c < C; ++c) alpha[c] = sees(c) ? (c & 1 ? s[c / 2].y : s[c / 2].x) : -INFINITY;
+                    const float wmax = fold<C, 16>(alpha, lane, &cidx, Max{});
+                    float(&rd)[4][C] = red[t & 1];
+                    if ((lane & (32 / C - 1)) == 0) rd[warp][cidx] = wmax;
                     if (group_or(1, kSoft, failed)) {
                         failed = true;
                         break;
                     }
 #pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        const float tmax = fmaxf(fmaxf(rd[0][h], rd[1][h]), fmaxf(rd[2][h], rd[3][h]));
-                        float& neg = h & 1 ? neg_m[h / 2].y : neg_m[h / 2].x;
-                        float& l = h & 1 ? l_part[h / 2].y : l_part[h / 2].x;
-                        const bool moves = tmax > kSlack - neg || (neg == INFINITY && tmax > -INFINITY);
+                    for (int c = 0; c < C; ++c) {
+                        const float tmax = fmaxf(fmaxf(rd[0][c], rd[1][c]), fmaxf(rd[2][c], rd[3][c]));
+                        float& neg = c & 1 ? neg_m[c / 2].y : neg_m[c / 2].x;
+                        float& l = c & 1 ? l_part[c / 2].y : l_part[c / 2].x;
+                        const bool moves = tmax > kSlack - neg || (neg == kNone && tmax > -INFINITY);
                         const float a = ex2(-neg - tmax);
-                        alpha[h] = moves ? a : 1.0f;
+                        alpha[c] = moves ? a : 1.0f;
                         neg = moves ? -tmax : neg;
-                        l *= alpha[h];
+                        l *= alpha[c];
                     }
 #pragma unroll
-                    for (int h = 0; h < H; h += 2) y[h / 2] = add2(s[h / 2], neg_m[h / 2]);
+                    for (int c = 0; c < C; c += 2) y[c / 2] = add2(s[c / 2], neg_m[c / 2]);
                     if (i > 0) {
                         w_ok = wait(&obar[(t - 1) & 1], (uint32_t)(((t - 1) >> 1) & 1));
                         tc::fence_after_sync();
@@ -492,46 +580,73 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                             float o[16];
                             tc::ld16(lanes + 2 * S::NS + c, o);
 #pragma unroll
-                            for (int x = 0; x < 16; ++x) o[x] *= alpha[(c + x) % H];
+                            for (int x = 0; x < 16; ++x) o[x] *= alpha[(c + x) % C];
                             tc::st16(lanes + 2 * S::NS + c, o);
                         }
                     }
                 }
-                if (__any_sync(0xffffffffu, !sees)) {  // (a key that is not seen may have anything for a score)
+                if (__any_sync(0xffffffffu, seen != (1u << R) - 1u)) {  // (what is not seen may have anything for a score)
 #pragma unroll
-                    for (int h = 0; h < H / 2; ++h) y[h] = sees ? y[h] : both(-INFINITY);
+                    for (int c = 0; c < C; c += 2) y[c / 2] = sees(c) ? y[c / 2] : both(-INFINITY);
                 }
                 // A weight in two bf16 parts: its first 8 bits, and the next 8.  The second is above zero where the weight
                 // is (its last bit is set), so that an infinite value meets two positive numbers.
-                uint32_t hi[H / 2], lo[H / 2];
+                uint32_t hi[C / 2], lo[C / 2];
 #pragma unroll
-                for (int h = 0; h < H; h += 2) {
-                    const float2 w = make_float2(ex2(y[h / 2].x), ex2(y[h / 2].y));
-                    l_part[h / 2] = add2(l_part[h / 2], w);
+                for (int c = 0; c < C; c += 2) {
+                    const float2 w = make_float2(ex2(y[c / 2].x), ex2(y[c / 2].y));
+                    l_part[c / 2] = add2(l_part[c / 2], w);
                     const uint32_t a = __float_as_uint(w.x), b = __float_as_uint(w.y);
-                    hi[h / 2] = __byte_perm(a, b, 0x7632);
-                    lo[h / 2] = pack_bf16x2(__uint_as_float(a | 1u) - __uint_as_float(a & 0xffff0000u),
+                    hi[c / 2] = __byte_perm(a, b, 0x7632);
+                    lo[c / 2] = pack_bf16x2(__uint_as_float(a | 1u) - __uint_as_float(a & 0xffff0000u),
                                             __uint_as_float(b | 1u) - __uint_as_float(b & 0xffff0000u));
                 }
                 uint8_t* pb = pt + (t & 1) * S::kPBytes + q * S::kPGroup + (key & 7) * 16;
-                if constexpr (H == 4) {
+                if constexpr (C == 4) {
                     *reinterpret_cast<uint4*>(pb) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < H / 8; ++x) {
+                    for (int x = 0; x < C / 8; ++x) {
                         *reinterpret_cast<uint4*>(pb + x * 128) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-                        *reinterpret_cast<uint4*>(pb + (H / 8 + x) * 128) =
+                        *reinterpret_cast<uint4*>(pb + (C / 8 + x) * 128) =
                             make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
                     }
                 }
-                // a copied V row that the row does not see is zeroed: the cache may hold anything
-                // there, and a zero weight must meet a finite value
-                if (__builtin_expect((me & 256u) && !sees, 0)) {
+                // A copied V row that no row of the item sees is zeroed: the cache may hold anything there, and a zero
+                // weight must meet a finite value.  Where some rows see it and others do not, what is not finite is, and the
+                // token noted for the rows that see it.
+                const uint32_t with = R == 1 ? 1u : rows_with_keys(set);
+                if (__builtin_expect((me & 256u) && (seen & with) != with, 0)) {
                     const int slot = (t + 1 < run ? 2 * t + 2 : 2 * t + 1) % S::kSlots;
                     w_ok &= wait(&vfull[t & 3], (uint32_t)((t >> 2) & 1));
                     uint4* vr = reinterpret_cast<uint4*>(slots + slot * kSlotBytes + q * kRegionBytes + (key & 7) * 128);
+                    if (R == 1 || seen == 0) {
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) vr[x] = vr[64 + x] = make_uint4(0, 0, 0, 0);
+                        for (int x = 0; x < 8; ++x) vr[x] = vr[64 + x] = make_uint4(0, 0, 0, 0);
+                    } else {
+                        bool any = false;
+#pragma unroll 1
+                        for (int i16 = 0; i16 < 16; ++i16) {  // (lanes of a region on different banks)
+                            uint4& at = vr[(i16 >> 3) * 64 + ((i16 ^ key) & 7)];
+                            const uint4 x = at;
+                            uint32_t xs[4] = {x.x, x.y, x.z, x.w}, bad = 0;
+#pragma unroll
+                            for (int z = 0; z < 4; ++z) {
+                                const uint32_t b = ((xs[z] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // an exponent of all ones
+                                xs[z] &= ~((b >> 15) * 0xffffu);
+                                bad |= b;
+                            }
+                            if (bad) {
+                                at = make_uint4(xs[0], xs[1], xs[2], xs[3]);
+                                any = true;
+                            }
+                        }
+                        if (any) {
+                            const int tok = s_t0[t & (kRing - 1)] + key;
+                            atomicMin(&s_cleared[(segs - 1) & 1].x, tok);
+                            atomicMax(&s_cleared[(segs - 1) & 1].y, tok);
+                        }
+                    }
                 }
                 fence_proxy_async();
                 tc::fence_before_sync();
@@ -571,8 +686,9 @@ cudaError_t launch_shape(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     cfg.numAttrs = pdl ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, paged_attn_bf16_kernel<S>, kmap, vmap, p);
     if (e != cudaSuccess) return e;
-    if (2 * p.N * p.G <= (int)cfg.gridDim.x) cfg.gridDim.x = (unsigned)(p.N * p.G);  // (the entries are by item then)
-    cfg.gridDim.y = S::H;
+    const int items = (p.N + S::R - 1) / S::R * p.G;
+    if (2 * items <= (int)cfg.gridDim.x) cfg.gridDim.x = (unsigned)items;  // (the entries are by item then)
+    cfg.gridDim.y = S::C;
     cfg.dynamicSmemBytes = 0;
     if ((int)(cfg.gridDim.x * cfg.gridDim.y) <= 2 * num_sms) {
         cfg.blockDim = dim3(128 * 8);
@@ -585,9 +701,19 @@ cudaError_t launch_shape(const PagedAttnParams& p, const CUtensorMap& kmap, cons
 template <int H>
 cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, int num_sms,
                          cudaStream_t stream, bool pdl) {
-    if (p.sel_ids == nullptr) return launch_shape<Shape<H, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
-    // (16 heads' weights leave room for one CTA an SM)
-    return launch_shape<Shape<H, true, H == 16 ? 1 : 2>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (p.sel_ids != nullptr)  // (16 heads' weights leave room for one CTA an SM)
+        return launch_shape<Shape<H, 1, true, H == 16 ? 1 : 2>>(p, kmap, vmap, num_sms, stream, pdl);
+    // Two or four rows of a sequence read its keys together where it has that many.  With 8 heads a group, microseconds alone and
+    // together: 2 rows of each of 4 sequences of 8,192 tokens 24 and 19, of 32,768 tokens 68 and 52; 4 rows of each of 8 of
+    // 8,192 61 and 41, of 32,768 314 and 98; 4 rows of one of 32,768 34 and 21.  The longer chain of a tile shows where all rows'
+    // keys are few: 4 rows of one sequence of 8,192 15 and 17, of each of 4 of 1,000 11.6 and 16.3, of each of 8 of 1,000
+    // 17.8 and 18.6.  (The host knows what the table can hold, not the lengths.)
+    if ((int64_t)p.N * p.G * p.pages.table_len * p.pages.page_tokens <= 1 << 17)
+        return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    if constexpr (H <= 8)
+        if (p.N >= 3 * p.B) return launch_shape<Shape<H, 4, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (p.N >= 2 * p.B) return launch_shape<Shape<H, 2, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
 }
 
 }  // namespace

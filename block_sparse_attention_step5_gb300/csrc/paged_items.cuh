@@ -72,6 +72,79 @@ __device__ __forceinline__ Item item_at(const PagedAttnParams& p, int i) {
     return it;
 }
 
+// Items of R rows: the keys of rows n .. n + R - 1 in group g, those of each of their sequences in turn.
+template <int R>
+struct RowSet {
+    int b[R], pos[R];  // as the call has them; b = -1: padding or past N, -2: out of range
+};
+template <int R>
+__device__ __forceinline__ RowSet<R> rows_at(const PagedAttnParams& p, int n) {
+    RowSet<R> s;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        s.b[r] = n + r < p.N ? p.row_seq[n + r] : -1;
+        s.pos[r] = n + r < p.N ? p.row_pos[n + r] : -1;
+        if (s.b[r] != -1 && (s.b[r] < 0 || s.b[r] >= p.B || s.pos[r] < 0 || s.pos[r] >= p.pages.page_tokens * p.pages.table_len))
+            s.b[r] = -2;
+    }
+    return s;
+}
+// One of an item's sequences: its rows (a mask) and their first and last token.
+struct Pass {
+    int b, lo, hi, r0, entries, tiles;
+    uint32_t rows;
+};
+// The sequence of the first of the rows `todo`, which loses its rows.
+template <int R>
+__device__ __forceinline__ Pass next_pass(const PagedAttnParams& p, const RowSet<R>& s, uint32_t& todo) {
+    Pass a{-1, INT32_MAX, -1, 0, 0, 0, 0u};
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r)
+        if (todo >> r & 1u) a.b = s.b[r];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+        if ((todo >> r & 1u) && s.b[r] == a.b) {
+            a.rows |= 1u << r;
+            a.lo = min(a.lo, p.window > 0 ? max(0, s.pos[r] - p.window + 1) : 0);
+            a.hi = max(a.hi, s.pos[r]);
+        }
+    todo &= ~a.rows;
+    a.r0 = (a.lo >> 3) & ~(p.box_regions - 1);
+    a.entries = (a.hi >> 3) - a.r0 + 1;
+    a.tiles = (a.entries + kTile - 1) / kTile;
+    return a;
+}
+template <int R>
+__device__ __forceinline__ uint32_t rows_with_keys(const RowSet<R>& s) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < R; ++r) m |= s.b[r] >= 0 ? 1u << r : 0u;
+    return m;
+}
+
+// Item i of R rows (of one: as above).  b: -1 without tiles, -2 with one empty tile (rows out of range alone), else 0.
+template <bool PICKS, int R>
+__device__ __forceinline__ Item item_of(const PagedAttnParams& p, int i) {
+    if constexpr (R == 1) {
+        return item_at<PICKS>(p, i);
+    } else {
+        const int blocks = (p.N + R - 1) / R;
+        Item it{};
+        it.g = i / blocks;
+        it.n = (i - it.g * blocks) * R;
+        const RowSet<R> s = rows_at<R>(p, it.n);
+        uint32_t todo = rows_with_keys(s);
+        while (todo) it.tiles += next_pass<R>(p, s, todo).tiles;
+        if (it.tiles == 0) {
+            it.b = -1;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (s.b[r] == -2) it.b = -2, it.tiles = 1;
+        }
+        return it;
+    }
+}
+
 // The output v of a (row, head), number `at` of them, through its gate.
 __device__ __forceinline__ float gated(const PagedAttnParams& p, int64_t at, float v) {
     return v * (1.0f / (1.0f + expf(-bf16_to_f32(p.gate[at]))));
@@ -88,9 +161,9 @@ struct RunSmem {
 
 // Splits the items' tiles over the CTAs (every thread calls it, and the block meets at a barrier behind it).  Returns
 // whether there are few; of many, start is the run's first tile among all and per the tiles of a run.
-template <bool PICKS, int THREADS>
+template <bool PICKS, int THREADS, int R = 1>
 __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREADS>& s, int64_t& start, int64_t& per) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, items = p.N * p.G;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, items = (p.N + R - 1) / R * p.G;
     start = 0, per = 1;
     const bool few = 2 * items <= (int)gridDim.x;
     if (few) {
@@ -98,7 +171,7 @@ __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREA
         // smallest L of 32 tried that needs no more CTAs than there are (2 L0 always does).  No CTA
         // then has parts of two items. (fewer than 2^8 items of at most 2^24 tiles)
         Item own{};
-        if (tid < items) own = item_at<PICKS>(p, tid);
+        if (tid < items) own = item_of<PICKS, R>(p, tid);
         const uint32_t mine = (uint32_t)own.tiles;
         s.tiles[tid] = own.tiles;
         const uint32_t sum = __reduce_add_sync(0xffffffffu, mine);
@@ -152,7 +225,7 @@ __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREA
         const int chunk = (items + THREADS - 1) / THREADS;
         const int i0 = min(items, tid * chunk), i1 = min(items, i0 + chunk);
         int64_t sum = 0;
-        for (int i = i0; i < i1; ++i) sum += item_at<PICKS>(p, i).tiles;
+        for (int i = i0; i < i1; ++i) sum += item_of<PICKS, R>(p, i).tiles;
         int64_t inc = sum;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -172,7 +245,7 @@ __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREA
         if (start >= before && start < before + sum) {
             int64_t at = before;
             for (int i = i0; i < i1; ++i) {
-                const Item it = item_at<PICKS>(p, i);
+                const Item it = item_of<PICKS, R>(p, i);
                 const int t = it.tiles;
                 if (start < at + t) {
                     s.item = i;
@@ -203,15 +276,17 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
     const int4 item = p.shared_items[blockIdx.x];
     const int first = item.z, n = item.w - first + 1;
     if (item.w < 0) return;
+    // (column c: head c % H of the item's row c / H)
+    if (S::C > S::H && (item.x + c / S::H >= p.N || p.row_seq[item.x + c / S::H] == -1)) return;
     auto state = [&](int i) { return p.states + ((int64_t)2 * (first + i) + (i == 0 ? 1 : 0)) * S::kState; };
     constexpr int kDeep = 8;
     float v[kDeep];
 #pragma unroll
-    for (int x = 0; x < kDeep; ++x) v[x] = grp + x * GROUPS < n ? state(grp + x * GROUPS)[2 * S::H + c * 128 + d] : 0.0f;
+    for (int x = 0; x < kDeep; ++x) v[x] = grp + x * GROUPS < n ? state(grp + x * GROUPS)[2 * S::C + c * 128 + d] : 0.0f;
     // the states' weights 2^(m - M) l
     float M = -INFINITY;
     for (int i = tid; i < n; i += 128 * GROUPS)
-        if (state(i)[S::H + c] != 0.0f) M = fmaxf(M, state(i)[c]);
+        if (state(i)[S::C + c] != 0.0f) M = fmaxf(M, state(i)[c]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
     if ((tid & 31) == 0) sm[tid >> 5] = M;
@@ -219,7 +294,7 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
 #pragma unroll
     for (int x = 0; x < GROUPS * 4; ++x) M = fmaxf(M, sm[x]);
     for (int i = tid; i < n; i += 128 * GROUPS) {
-        const float l = state(i)[S::H + c];
+        const float l = state(i)[S::C + c];
         sw[i] = l == 0.0f ? 0.0f : ex2(state(i)[c] - M) * l;
     }
     __syncthreads();
@@ -232,7 +307,7 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
         }
 #pragma unroll 8
     for (int i = grp + kDeep * GROUPS; i < n; i += GROUPS) {
-        o = fmaf(sw[i], state(i)[2 * S::H + c * 128 + d], o);
+        o = fmaf(sw[i], state(i)[2 * S::C + c * 128 + d], o);
         w += sw[i];
     }
     so[grp][d] = o;
@@ -245,7 +320,7 @@ __global__ void __launch_bounds__(128 * GROUPS) join_kernel(PagedAttnParams p) {
             o += so[x][d];
             w += sl[x];
         }
-        const int64_t at = (int64_t)item.x * p.Hq + (int64_t)item.y * S::H + c;
+        const int64_t at = (int64_t)(item.x + c / S::H) * p.Hq + (int64_t)item.y * S::H + c % S::H;
         o = w == 0.0f ? 0.0f : o / w;
         if (p.gate != nullptr && w != 0.0f) o = gated(p, at, o);
         p.out[at * 128 + d] = f32_to_bf16_bits(o);

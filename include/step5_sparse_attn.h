@@ -481,7 +481,9 @@ step5_status step5_sparse_attn_e4m3(const step5_geometry* geom, const step5_page
  * never reach its result, whatever the pages hold there (infinities and NaN too).  A region of the keys whose table
  * entry is bad is left out and sets STEP5_DEV_RANGE; a row without keys, or out of range, gets zeros, as does one whose
  * every score is -infinity; a padding row's output is left as it was.  N <= 65535.  Any order of rows.
- * When rows share tiles, and the workspace: as step5_paged_attn_e4m3. */
+ * From N * num_q_heads / G >= 128 B on, neighbouring rows of a sequence share its keys' tiles; below, up to four of them
+ * read its keys together.  So for a prompt chunk of few sequences out of a large table pass those sequences' rows of the
+ * table, B of them.  The workspace: as step5_paged_attn_e4m3. */
 step5_status step5_paged_attn(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B, int32_t window,
                               const void* q_bf16, int64_t q_stride, const void* k_pages_bf16, const void* v_pages_bf16,
                               const int32_t* block_table_or_null, const int32_t* row_seq, const int32_t* row_pos,

@@ -46,7 +46,7 @@ def attend(q, k, v, table, row_seq, row_pos, scale, window=0, ids=None, counts=N
 
 def shares(N, hq, B):
     """Whether rows of a sequence share its keys' tiles (the rule of the header)."""
-    return N * hq >= max(128, 64 * B)
+    return N * hq >= 128 * B
 
 
 def tolerance(out, mass, shared):

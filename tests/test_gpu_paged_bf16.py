@@ -130,6 +130,92 @@ def test_lengths(s5, tokens, rows):  # noqa: F811
     Case(s5, [(0, max(0, tokens - rows), rows)], G=2, seed=tokens).check()
 
 
+DRAFTS = {
+    "two": [(b, 90 + 61 * b, 2) for b in range(6)], "three": [(b, 300 + 7 * b, 3) for b in range(5)],
+    "four": [(b, 1000 - 37 * b, 4) for b in range(4)], "seven": [(0, 2040, 7), (1, 3, 7)],
+    "mixed": [(0, 500, 1), (1, 33, 4), (-1, 0, 2), (2, 900, 2), (3, 0, 3), (-1, 0, 1), (4, 127, 3)],
+    "woven": [(0, 500, 1), (1, 433, 1), (0, 501, 1), (1, 434, 1), (2, 60, 1), (0, 20, 1), (2, 61, 1), (2, 700, 2)],
+}
+
+
+@pytest.mark.parametrize("rows", list(DRAFTS))
+@pytest.mark.parametrize("G, hq, pt, window", [(4, 8, 64, 0), (2, 16, 24, 0), (3, 4, 16, 0), (2, 8, 8, 45), (1, 16, 128, 130), (4, 4, 40, 9)])
+def test_drafts(s5, rows, G, hq, pt, window):  # noqa: F811
+    """A few rows of each sequence, which read its keys together where the table holds enough of them."""
+    Case(s5, DRAFTS[rows], G, hq, pt, seed=len(rows) + window, apart=True, extra=24000 // (G * len(DRAFTS[rows]))).gated().check(window)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+@pytest.mark.parametrize("window", [0, 70])
+def test_values_of_a_later_draft_stay_with_it(s5, window, bad):  # noqa: F811
+    """Four drafts of each of three sequences: a value that is not finite, at one draft's token, reaches that draft
+    and those behind it, and no row before it or of another sequence."""
+    c = Case(s5, [(0, 300, 4), (1, 77, 4), (2, 1500, 4)], G=4, pt=16, seed=4, extra=20000)
+    clean = c.want(window)
+    page, slot = R.place(c.table, 1, 78, c.pt)
+    c.v[page, 2, slot, 100], c.k[R.place(c.table, 0, 302, c.pt)[0], 1, 302 % 16, 9] = bad, NAN
+    got = c.run(window).cpu().float()
+    assert status(s5) == 0
+    hit = got[5:8, 16:24, 100]
+    assert bool(torch.isnan(hit).all() if bad != bad else (hit == bad).all())
+    got[5:8, 16:24, 100] = clean[0][5:8, 16:24, 100].float()
+    assert bool(torch.isnan(got[2:4, 8:16]).all())
+    got[2:4, 8:16] = clean[0][2:4, 8:16].float()
+    c.near(got.bfloat16(), *clean)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_drafts_of_windows_that_lie_apart(s5, bad):  # noqa: F811
+    """What lies between the windows of rows of one item is not touched, whatever its pages and table entries hold."""
+    c = Case(s5, [(0, 5000, 2), (0, 40, 2), (1, 900, 3), (1, 8, 1)], G=4, pt=16, seed=8, extra=9000)
+    want = c.want(30)
+    mask = c.unseen(30)[:, None, :, None]
+    c.k.masked_fill_(mask, bad)
+    c.v.masked_fill_(mask, bad)
+    c.table[0, 4:300], c.table[1, 3:50] = -1, 10 ** 7
+    got = c.run(30).cpu()
+    assert status(s5) == 0
+    c.near(got, *want)
+
+
+def test_drafts_on_bad_pages_and_out_of_range(s5):  # noqa: F811
+    c = Case(s5, [(0, 500, 4), (1, 90, 4), (2, 33, 4)], G=4, pt=32, seed=6, extra=20000)
+    c.table[0, 3], c.table[2, 0], c.table[2, 1] = -1, 10 ** 6, -9
+    c.seq[5], c.pos[6], c.seq[7] = 77, c.table.shape[1] * 32, -1
+    got = c.run().cpu()
+    assert status(s5) == 1
+    assert bool((got[5:7] == 0).all()) and bool((got[7] == 5.0).all()) and bool((got[8:12] == 0).all())
+    c.seq[5:7] = -1
+    want = c.want(bad_pages=(-1, 10 ** 6, -9))
+    ok = [0, 1, 2, 3, 4, 8, 9, 10, 11]
+    assert B16.off(got[ok], want[0][ok], want[1][ok], c.shared) <= 1.0
+
+
+def test_scores_of_minus_infinity(s5):  # noqa: F811
+    """Keys whose scores overflow to -infinity weigh nothing, wherever they stand; a row with no others gets zeros."""
+    for runs in ([(0, 600, 1)], [(0, 600, 4), (1, 5000, 1)], [(0, 600, 40)]):
+        c = Case(s5, runs, G=1, hq=16, pt=64, seed=2)
+        c.q = c.q.contiguous()
+        c.q[0, :, 0], c.q[0, 3, 1] = 3.0e38, 0
+        lows = torch.rand(601, generator=c.gen) < 0.5
+        lows[:200] = True
+        for t in range(601):
+            page, slot = R.place(c.table, 0, t, c.pt)
+            c.k[page, :, slot, 0] = -3.0e38 if lows[t] else 0.0
+        got = c.run().cpu()[:1]
+        assert status(s5) == 0
+        out, mass = torch.zeros((1, 16, 128), dtype=torch.float64), torch.zeros((1, 16, 128), dtype=torch.float64)
+        tok = torch.nonzero(~lows)[:, 0]
+        page, slot = (torch.tensor(x) for x in zip(*[R.place(c.table, 0, int(t), c.pt) for t in tok]))
+        w = torch.softmax(c.q[0].double() @ c.k[page, 0, slot].double().T * c.geom.softmax_scale, -1)
+        out[0], mass[0] = w @ c.v[page, 0, slot].double(), w @ c.v[page, 0, slot].double().abs()
+        assert B16.off(got, out, mass, c.shared) <= 1.0
+        for t in range(601):
+            page, slot = R.place(c.table, 0, t, c.pt)
+            c.k[page, :, slot, 0] = -3.0e38
+        assert bool((c.run().cpu()[0] == 0).all()) and status(s5) == 0
+
+
 @pytest.mark.parametrize("runs", [[(b, 97 * b, 1) for b in range(40)], [(0, 900, 1), (1, 9000, 1), (2, 17, 1)],
                                   [(0, 30, 200), (1, 4000, 200)]])
 def test_ragged_batches(s5, runs):  # noqa: F811
