@@ -755,16 +755,51 @@ def step5_sparse_attn_paged(geom, q, cache: PagedCache, row_seq, row_pos, sel_id
                   sel_ids=sel_ids, sel_count=sel_count)
 
 
-@dataclass
-class PagedTable:
+class _Int32s:
+    """A handle of int32 GPU tensors, checked and laid out for the C call once, and again when one is assigned."""
+
+    def __setattr__(self, name, value):
+        if name in self._TENSORS:
+            self._lay_out(*(value if n == name else getattr(self, n) for n in self._TENSORS))
+        elif name in self._FOLLOWS:
+            raise AttributeError(f"{name} of a {type(self).__name__} follows from its tensors")
+        else:
+            super().__setattr__(name, value)
+
+    def _keep(self, tensors, shapes, **follows):
+        for name, t, shape in zip(self._TENSORS, tensors, shapes):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor {shape}")
+            if t.device != tensors[0].device:
+                raise ValueError(f"the tensors are on {tensors[0].device} and {t.device}")
+        d = tensors[0].device
+        self.__dict__.update(zip(self._TENSORS, tensors))
+        self.__dict__.update(follows, device=d, _index=d.index if d.type == "cuda" else -1,
+                             _args=tuple(t.data_ptr() for t in tensors))
+
+
+def _length(t, dims: int) -> tuple:
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError(f"a tensor of {dims} dimension{'s' if dims > 1 else ''} is needed")
+    return tuple(t.shape)
+
+
+class PagedTable(_Int32s):
     """The pages of a cache's sequences, all int32 on the GPU: the block table [B][table_len] (the tensor
     that the PagedCache has), the pages that each sequence holds [B], and the stack of free pages: free_pages
     [num_pages], of which the first free_count [1] are free, the last of them its top."""
-    block_table: torch.Tensor
-    held: torch.Tensor
-    free_pages: torch.Tensor
-    free_count: torch.Tensor
-    page_tokens: int
+
+    _TENSORS = ("block_table", "held", "free_pages", "free_count")
+    _FOLLOWS = ("B", "page_tokens", "device", "_index", "_args", "_shape")
+
+    def __init__(self, block_table, held, free_pages, free_count, page_tokens: int):
+        self.__dict__["page_tokens"] = int(page_tokens)
+        self._lay_out(block_table, held, free_pages, free_count)
+
+    def _lay_out(self, *tensors):
+        (B, table_len), (num_pages,) = _length(tensors[0], 2), _length(tensors[2], 1)
+        self._keep(tensors, ((B, table_len), (B,), (num_pages,), (1,)), B=B,
+                   _shape=Pages(num_pages, self.page_tokens, table_len))
 
     @classmethod
     def create(cls, num_pages: int, page_tokens: int, table_len: int, B: int, device="cuda") -> "PagedTable":
@@ -774,18 +809,20 @@ class PagedTable:
                    zeros(1) + num_pages, page_tokens)
 
 
-@dataclass
-class PagedRows:
+class PagedRows(_Int32s):
     """What step5_paged_plan writes of a step, all int32: of each row its sequence and position [N] (-1:
     padding), of each sequence its first row [B + 1], its tokens after the step, those granted, and the regions
     [region_begin, region_end) that the step completes [B]."""
-    row_seq: torch.Tensor
-    row_pos: torch.Tensor
-    row_start: torch.Tensor
-    ends: torch.Tensor
-    granted: torch.Tensor
-    region_begin: torch.Tensor
-    region_end: torch.Tensor
+
+    _TENSORS = ("row_seq", "row_pos", "row_start", "ends", "granted", "region_begin", "region_end")
+    _FOLLOWS = ("B", "N", "device", "_index", "_args")
+
+    def __init__(self, row_seq, row_pos, row_start, ends, granted, region_begin, region_end):
+        self._lay_out(row_seq, row_pos, row_start, ends, granted, region_begin, region_end)
+
+    def _lay_out(self, *tensors):
+        (N,), (B,) = _length(tensors[0], 1), _length(tensors[3], 1)
+        self._keep(tensors, ((N,), (N,), (B + 1,), (B,), (B,), (B,), (B,)), N=N, B=B)
 
     @classmethod
     def create(cls, B: int, N: int, device="cuda") -> "PagedRows":
@@ -797,22 +834,18 @@ def step5_paged_plan(table: PagedTable, rows: PagedRows, lengths, new_tokens, st
     """Plans a step of sequences that have ``lengths`` [B] tokens in the cache and get ``new_tokens`` [B] (int32):
     pages move between the table and its free ones, and ``rows`` is filled in (see the header).  lengths may be
     rows.ends, so that a captured step goes on from the one before."""
-    bt = table.block_table
-    B, table_len = bt.shape
-    dev = torch.cuda.current_device()
-    if table.free_pages.dim() != 1 or rows.row_seq.dim() != 1:
-        raise ValueError("free_pages and row_seq must be one-dimensional")
-    pages = Pages(table.free_pages.shape[0], int(table.page_tokens), table_len)
-    N = rows.row_seq.shape[0]
-    i32 = lambda what, t, *shape: _arg(what, t, torch.int32, shape, dev)
-    st = load().step5_paged_plan(
-        Geometry.of(geom), pages, N, B, i32("lengths", lengths, B), i32("new_tokens", new_tokens, B),
-        i32("block_table", bt, B, table_len), i32("held", table.held, B),
-        i32("free_pages", table.free_pages, pages.num_pages), i32("free_count", table.free_count, 1),
-        i32("row_seq", rows.row_seq, N), i32("row_pos", rows.row_pos, N), i32("row_start", rows.row_start, B + 1),
-        i32("ends", rows.ends, B), i32("granted", rows.granted, B), i32("region_begin", rows.region_begin, B),
-        i32("region_end", rows.region_end, B),
-        stream.cuda_stream if stream is not None else torch.cuda.current_stream(dev).cuda_stream)
+    dev = _current_device() if table._index >= 0 else torch.cuda.current_device()
+    if table._index != dev or rows._index != dev:
+        raise ValueError(f"the table is on {table.device}, the rows on {rows.device}, the current device is cuda:{dev}")
+    B = table.B
+    if rows.B != B:
+        raise ValueError(f"the table has {B} sequences, the rows {rows.B}")
+    if stream is not None:
+        st = stream.cuda_stream
+    else:
+        st = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    st = load().step5_paged_plan(Geometry.of(geom), table._shape, rows.N, B, _arg("lengths", lengths, torch.int32, (B,), dev),
+                                 _arg("new_tokens", new_tokens, torch.int32, (B,), dev), *table._args, *rows._args, st)
     if st:
         raise Step5Error("step5_paged_plan", st)
 

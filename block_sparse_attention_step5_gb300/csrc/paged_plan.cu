@@ -15,7 +15,6 @@ namespace step5 {
 
 namespace {
 
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
 constexpr int64_t kFar = 1 << 30;  // past every count of rows or pages; the stored sums stop here
 enum : uint8_t { kFits = 1, kNeeds = 2 };
 
@@ -34,83 +33,87 @@ __device__ __forceinline__ int owner(const int32_t* sums, int B, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanParams p) {
+// The sum of x over the block's threads before this one, and (in all) over all of them.  s: a number a warp.
+template <int THREADS>
+__device__ __forceinline__ int64_t before(int64_t x, int64_t* s, int64_t& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t inc = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+    }
+    if (lane == 31) s[warp] = inc;
+    __syncthreads();
+    int64_t w = lane < THREADS / 32 ? s[lane] : 0, sum = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += o;
+    }
+    all = __shfl_sync(0xffffffffu, sum, 31);
+    return inc - x + __shfl_sync(0xffffffffu, sum - w, warp);
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) paged_plan_kernel(PlanParams p) {
     extern __shared__ int32_t smem[];
     int32_t* s_start = smem;                  // [B + 1] first row, at most N
     int32_t* s_less = s_start + p.B + 1;      // [B + 1] pages given back before the sequence
     int32_t* s_need = s_less + p.B + 1;       // [B + 1] pages needed before it
     int32_t* s_len = s_need + p.B + 1;        // [B]
     uint8_t* s_flag = reinterpret_cast<uint8_t*>(s_len + p.B);
-    __shared__ int64_t s_sum[3][kPlanWarps];
+    __shared__ int64_t s_sum[3][THREADS / 32];
     __shared__ int s_taken;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int at = blockIdx.x * kPlanThreads + tid, all = gridDim.x * kPlanThreads;
-    const bool first = blockIdx.x == 0;
+    const int tid = threadIdx.x;
+    const int at = blockIdx.x * THREADS + tid, all = gridDim.x * THREADS;
     if (tid == 0) s_taken = 0;
     pdl_wait();
     pdl_launch_dependents();
 
-    // the sums, a block of sequences at a time
+    // the sequences' numbers (for now new tokens and held pages where the sums will be), then a run of sequences a thread
     int count = *p.free_count;
+    for (int b = tid; b < p.B; b += THREADS) {
+        s_len[b] = p.lengths[b];
+        s_start[b] = p.new_tokens[b];
+        s_need[b] = p.held[b];
+    }
     bool bad = count < 0 || count > p.num_pages;
     count = min(max(count, 0), p.num_pages);
+    __syncthreads();
+    const int each = (p.B + THREADS - 1) / THREADS, b0 = min(p.B, tid * each), b1 = min(p.B, b0 + each);
     const int64_t cap = (int64_t)p.page_tokens * p.table_len;
-    int64_t rows = 0, less = 0, need = 0;  // of the blocks before
-    for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
-        const int b = b0 + tid;
-        int64_t v[3] = {0, 0, 0};
-        bool good = false;
-        int want = 0, held = 0, len = 0;
-        if (b < p.B) {
-            len = p.lengths[b];
-            const int more = p.new_tokens[b];
-            held = p.held[b];
-            good = len >= 0 && more >= 0 && (int64_t)len + more <= cap && held >= 0 && held <= p.table_len;
-            bad |= !good;
-            v[0] = max(more, 0);
-            if (good) want = (int)(((int64_t)len + more + p.page_tokens - 1) / p.page_tokens);
-        }
-        // rows first: a sequence whose rows lie past N takes part in nothing else
-        auto scan = [&](int64_t x, int which) {  // the sum before this thread's, in the block
-            int64_t inc = x;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += o;
-            }
-            if (lane == 31) s_sum[which][warp] = inc;
-            return inc - x;
-        };
-        auto total = [&](int which, int64_t& before) {
-            int64_t sum = 0;
-#pragma unroll
-            for (int w = 0; w < kPlanWarps; ++w) {
-                if (w < warp) before += s_sum[which][w];
-                sum += s_sum[which][w];
-            }
-            return sum;
-        };
-        int64_t start = scan(v[0], 0) + rows;
-        __syncthreads();
-        const int64_t more_rows = total(0, start);
-        const bool fits = good && start + v[0] <= p.N;
-        if (b < p.B && good && !fits) bad = true;
-        if (fits) {
-            v[1] = max(held - want, 0);
-            v[2] = max(want - held, 0);
-        }
-        int64_t l = scan(v[1], 1) + less, n = scan(v[2], 2) + need;
-        __syncthreads();
-        const int64_t more_less = total(1, l), more_need = total(2, n);
-        if (b < p.B) {
-            s_start[b] = (int)min(start, (int64_t)p.N);
-            s_less[b] = (int)min(l, kFar);
-            s_need[b] = (int)min(n, kFar);
-            s_len[b] = len;
-            s_flag[b] = (fits ? kFits : 0) | (v[2] > 0 ? kNeeds : 0);
-        }
-        rows += more_rows, less += more_less, need += more_need;
-        __syncthreads();  // (s_sum is free again)
+    int64_t mine = 0, rows, less, need;
+    for (int b = b0; b < b1; ++b) mine += max(s_start[b], 0);
+    const int64_t start0 = before<THREADS>(mine, s_sum[0], rows);
+    // pages wanted and held: a sequence out of range, or whose rows lie past N, takes part in nothing else
+    auto pages_of = [&](int b, int64_t& start, int& l, int& n) {
+        const int len = s_len[b], more = s_start[b], held = s_need[b];
+        const bool good = len >= 0 && more >= 0 && (int64_t)len + more <= cap && held >= 0 && held <= p.table_len && start + more <= p.N;
+        start += max(more, 0);
+        const int want = good ? (int)(((uint32_t)len + (uint32_t)more + (uint32_t)p.page_tokens - 1u) / (uint32_t)p.page_tokens) : held;
+        l = max(held - want, 0);
+        n = max(want - held, 0);
+        return good;
+    };
+    int64_t start = start0, less0 = 0, need0 = 0;
+    for (int b = b0; b < b1; ++b) {
+        int l, n;
+        if (!pages_of(b, start, l, n)) bad = true;
+        less0 += l, need0 += n;
+    }
+    less0 = before<THREADS>(less0, s_sum[1], less);
+    need0 = before<THREADS>(need0, s_sum[2], need);
+    start = start0;
+    for (int b = b0; b < b1; ++b) {
+        const int64_t first = start;
+        int l, n;
+        const bool good = pages_of(b, start, l, n);
+        s_start[b] = (int)min(first, (int64_t)p.N);
+        s_less[b] = (int)min(less0, kFar);
+        s_need[b] = (int)min(need0, kFar);
+        s_flag[b] = (good ? kFits : 0) | (n > 0 ? kNeeds : 0);
+        less0 += l, need0 += n;
     }
     if (tid == 0) {
         s_start[p.B] = (int)min(rows, (int64_t)p.N);
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanParams p) 
         return (f & kFits) && (!(f & kNeeds) || s_need[b + 1] <= have);
     };
     int taken = 0;
-    for (int b = tid; b < p.B; b += kPlanThreads)
+    for (int b = tid; b < p.B; b += THREADS)
         if ((s_flag[b] & kNeeds) && granted(b)) taken = max(taken, s_need[b + 1]);
     if (taken) atomicMax(&s_taken, taken);
     cluster_sync();  // (also the block's barrier) everything that is changed below has been read
@@ -151,11 +154,18 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanParams p) 
         p.region_end[b] = len >= 0 ? end >> 3 : 0;
         if (ok) p.held[b] = want_of(b);
     }
-    for (int n = at; n < p.N; n += all) {
-        const int b = owner(s_start, p.B, n);
-        const bool real = b < p.B && granted(b);
-        p.row_seq[n] = real ? b : -1;
-        p.row_pos[n] = real ? s_len[b] + (n - s_start[b]) : -1;
+    // (a warp takes 128 rows at a time, four a lane: the next is found from the one before)
+    for (int n0 = (at >> 5) * 128 + (at & 31); n0 < p.N; n0 += 4 * all) {
+        int b = owner(s_start, p.B, n0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 32 * i;
+            if (n >= p.N) break;
+            while (b < p.B && s_start[b + 1] <= n) ++b;
+            const bool real = b < p.B && granted(b);
+            p.row_seq[n] = real ? b : -1;
+            p.row_pos[n] = real ? s_len[b] + (n - s_start[b]) : -1;
+        }
     }
     if (back > 0 && taken > 0) cluster_sync();  // (the same for every block)
     for (int x = at; x < taken; x += all) {
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanParams p) 
         if (page < 0 || page >= p.num_pages) bad = true;
         p.block_table[(int64_t)b * p.table_len + want_of(b) - (s_need[b + 1] - s_need[b]) + (x - s_need[b])] = page;
     }
-    if (first && tid == 0) {
+    if (blockIdx.x == 0 && tid == 0) {
         p.row_start[p.B] = s_start[p.B];
         *p.free_count = have - taken;
     }
@@ -172,27 +182,34 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanParams p) 
 
 }  // namespace
 
-cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream, bool pdl) {
+namespace {
+template <int THREADS>
+cudaError_t launch(const PlanParams& p, unsigned ctas, cudaStream_t stream, bool pdl) {
     static std::atomic<uint64_t> attr_set{0};
     cudaError_t e = once_per_device(attr_set, [] {
-        return cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kPlanMaxSeqs));
+        return cudaFuncSetAttribute(paged_plan_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)plan_smem(kPlanMaxSeqs));
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((int64_t)p.N + p.B <= 4 * kPlanThreads ? 1u : 8u);
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = plan_smem(p.B);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cfg.gridDim.x;
+    attr[0].val.clusterDim.x = ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, paged_plan_kernel, p);
+    return cudaLaunchKernelEx(&cfg, paged_plan_kernel<THREADS>, p);
+}
+}  // namespace
+
+cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream, bool pdl) {
+    return (int64_t)p.N + p.B <= 1024 ? launch<256>(p, 1, stream, pdl) : launch<1024>(p, 8, stream, pdl);
 }
 
 }  // namespace step5

@@ -75,3 +75,27 @@ def test_the_binding_checks_kinds_and_devices(s5):  # noqa: F811
         s5.step5_paged_plan(table, rows, row, row)
     assert table.free_pages.tolist() == [3, 2, 1, 0] and table.free_count.tolist() == [4]
     assert rows.row_start.shape == (2,) and rows.row_seq.shape == (4,)
+
+
+def test_handles_check_what_is_assigned(s5):  # noqa: F811
+    i32 = lambda *shape: torch.zeros(shape, dtype=torch.int32)
+    table = s5.PagedTable(i32(3, 4), i32(3), i32(20), i32(1), 16)
+    assert table.B == 3 and table.page_tokens == 16
+    for name, bad in (("held", i32(4)), ("held", torch.zeros(3)), ("free_count", i32(2)), ("block_table", i32(2, 4)),
+                      ("block_table", i32(3, 8)[:, ::2]), ("free_pages", i32(2, 2)), ("held", None)):
+        with pytest.raises(ValueError):
+            setattr(table, name, bad)
+    for name in ("B", "page_tokens", "device"):
+        with pytest.raises(AttributeError):
+            setattr(table, name, 1)
+    longer = i32(40)
+    table.free_pages = longer
+    assert table.free_pages is longer and table._shape.num_pages == 40 and table._args[2] == longer.data_ptr()
+    rows = s5.PagedRows.create(3, 10, device="cpu")
+    with pytest.raises(ValueError):
+        rows.ends = i32(4)
+    with pytest.raises(ValueError):
+        rows.row_pos = i32(11)
+    lengths = i32(3)
+    rows.ends = lengths
+    assert rows.ends is lengths and rows.B == 3 and rows.N == 10
