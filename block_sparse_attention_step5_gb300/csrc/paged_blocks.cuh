@@ -141,6 +141,7 @@ struct Walk {
 // A CTA's run of tiles: those from `start` on, of the tiles of all items (blocks of rows, group after group).
 struct BlockRun {
     int64_t of_group, total, per, start;  // tiles of a group, of all, of a run
+    int run, g0;                          // the run's tiles and first group
 };
 template <int THREADS>
 struct BlockRunSmem {
@@ -150,7 +151,9 @@ struct BlockRunSmem {
 
 // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups
 // (every thread calls it, and the block meets at a barrier behind it).  tiles: room for a number a block.
-template <class S, int THREADS>
+// WHOLE > 0: whole items go to a CTA instead where that takes the busiest one at most WHOLE tiles more than an equal
+// share (an item's share goes by its middle tile); tiles then has room for kChunkMaxCtas numbers more.
+template <class S, int THREADS, int WHOLE = 0>
 __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunSmem<THREADS>& s, int* tiles) {
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int blocks = (p.N + S::NB - 1) / S::NB;
@@ -185,6 +188,39 @@ __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunS
     r.total = r.of_group * p.G;
     r.per = (r.total + gridDim.x - 1) / gridDim.x;
     r.start = blockIdx.x * r.per;
+    if constexpr (WHOLE > 0) {
+        if (blocks * p.G <= 8 * kChunkMaxCtas && r.total < (1 << 24)) {  // (many items: the joins weigh little)
+            int* load = tiles + blocks;
+            for (int i = tid; i < (int)gridDim.x; i += THREADS) load[i] = 0;
+            if (tid == 0) s.blk = INT32_MAX;
+            __syncthreads();
+            const int per = (int)r.per, of_group = (int)r.of_group;
+            for (int g = 0; g < p.G; ++g) {
+                int at = g * of_group + (int)before;
+                for (int i = i0; i < i1; at += tiles[i], ++i)
+                    if (tiles[i] > 0) {
+                        const int cta = (2 * at + tiles[i]) / (2 * per);
+                        atomicAdd(&load[cta], tiles[i]);
+                        if (cta == (int)blockIdx.x) atomicMin(&s.blk, g * blocks + i);
+                    }
+            }
+            __syncthreads();
+            int most = 0;
+            for (int i = lane; i < (int)gridDim.x; i += 32) most = max(most, load[i]);
+            most = __reduce_max_sync(0xffffffffu, most);
+            const int first = s.blk;
+            if (most <= per + WHOLE) {
+                r.run = load[blockIdx.x];
+                r.g0 = r.run ? first / blocks : 0;
+                __syncthreads();  // (first is read)
+                if (tid == 0) s.blk = first % blocks, s.off = 0;
+                return r;
+            }
+            __syncthreads();
+        }
+    }
+    r.run = (int)(r.start < r.total ? min(r.per, r.total - r.start) : 0);
+    r.g0 = r.run ? (int)(r.start / r.of_group) : 0;
     if (r.start < r.total) {
         const int64_t in = r.start % r.of_group;
         if (in >= before && in < before + sum) {

@@ -120,13 +120,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
 
     const BlockRun of = take_run<S, kThreads>(p, rs, reinterpret_cast<int*>(smem));  // (nothing is copied yet)
-    const int64_t of_group = of.of_group, total = of.total, per = of.per, start = of.start;
+    const int64_t per = of.per, start = of.start;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s_tmem;
-    const int run = (int)(start < total ? min(per, total - start) : 0);
-    const int blk0 = rs.blk, off0 = rs.off, g0 = run ? (int)(start / of_group) : 0;
+    const int run = of.run, blk0 = rs.blk, off0 = rs.off, g0 = of.g0;
 
     // Every role walks the run's segments alike: item (group, block), tiles off .. off + n - 1 of it.
     // next() returns false when there is none (the rows have changed under the kernel).

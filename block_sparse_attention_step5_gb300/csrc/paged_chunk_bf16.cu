@@ -40,6 +40,10 @@ constexpr uint32_t kIdescQk = tc::instr_desc(tc::kFmtBF16, false, false, 128, 12
 constexpr uint32_t kIdescPv = tc::instr_desc(tc::kFmtBF16, false, true, 128, 128);
 constexpr float kSlack = 8.0f;                  // log2 units a weight may lie above the running maximum
 
+// Tiles that the busiest CTA may have over an equal share before items are cut: what a cut costs, a partial state and its join
+// for most CTAs (window of 512: ZZ us cut, ZZ whole; three prompts of 701 rows ZZ and ZZ).
+constexpr int kWholeTiles = 5;
+
 // A tile as the copying warp leaves it for the others.
 struct Tile {
     uint64_t rows;       // the block's rows that the tile's sequence is of
@@ -48,6 +52,7 @@ struct Tile {
     uint32_t note;       // kFirst ...
     int g, n0;           // group, first row of the block
     int last;            // the CTA that has the item's last tile
+    int all_lo, all_hi;  // tokens that every row of the block but padding sees
 };
 // A segment: the tiles of an item (group, block of rows) that a CTA has.
 enum : uint32_t {
@@ -79,25 +84,23 @@ struct Control {
 template <class S>
 constexpr uint32_t kSmem = kTilesBytes + (uint32_t)sizeof(Control<S>);
 
-// What dims c .. c + 31 hold among tokens lo .. hi of sequence b: masks of infinities of either sign (a NaN is both).
-__device__ __noinline__ uint2 not_finite(const PagedAttnParams& p, int b, int g, int c, int lo, int hi) {
-    uint32_t pos = 0, neg = 0;
+// Adds to 64 values of a head row (bf16 at out, or fp32 in groups of 8 at state) what is not finite in their dims, from dim d0 on,
+// among tokens lo .. hi of sequence b.  Rarely run, and apart from the code that is.
+__device__ __noinline__ void add_not_finite(const PagedAttnParams& p, int b, int g, int d0, int lo, int hi, uint16_t* out, float* state) {
     for (int t = lo; t <= hi; ++t) {
         const int64_t row = page_row(p.pages, p.G, b, g, t);
         if (row < 0) continue;
-        const uint4* v = reinterpret_cast<const uint4*>(p.v_pages + row * 256 + c * 2);
-        for (int i = 0; i < 4; ++i) {
-            const uint4 x = v[i];
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            for (int y = 0; y < 8; ++y) {
-                const uint32_t u = xs[y >> 1] >> (16 * (y & 1)) & 0xffffu;
-                if ((u & 0x7f80u) != 0x7f80u) continue;
-                if ((u & 0x7fu) || !(u & 0x8000u)) pos |= 1u << (8 * i + y);
-                if ((u & 0x7fu) || (u & 0x8000u)) neg |= 1u << (8 * i + y);
-            }
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v_pages) + row * 128 + d0;
+#pragma unroll 1
+        for (int d = 0; d < 64; ++d) {
+            const float x = bf16_to_f32(v[d]);
+            if (fabsf(x) < INFINITY) continue;
+            if (state != nullptr)
+                state[(d >> 3) * 2048 + (d & 7)] += x;
+            else
+                out[d] = f32_to_bf16_bits(bf16_to_f32(out[d]) + x);
         }
     }
-    return make_uint2(pos, neg);
 }
 
 template <class S>
@@ -142,15 +145,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
-    const BlockRun of = take_run<S, kThreads>(p, sm.rs, reinterpret_cast<int*>(smem));  // (nothing is copied yet)
-    const int64_t of_group = of.of_group, total = of.total, per = of.per, start = of.start;
+    const BlockRun of = take_run<S, kThreads, kWholeTiles>(p, sm.rs, reinterpret_cast<int*>(smem));  // (nothing is copied yet)
+    const int64_t per = of.per, start = of.start;
     fence_proxy_async();  // (the copies write where the tiles' numbers were)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sm.tmem;
-    const int run = (int)(start < total ? min(per, total - start) : 0);
-    const int blk0 = sm.rs.blk, off0 = sm.rs.off, g0 = run ? (int)(start / of_group) : 0;
+    const int run = of.run, blk0 = sm.rs.blk, off0 = sm.rs.off, g0 = of.g0;
 
     // Every role walks the run's segments alike: item (group, block), tiles off .. off + n - 1 of it.
     // next() returns false when there is none (the rows have changed under the kernel).
@@ -255,6 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tl.g = s.g;
                     tl.n0 = s.blk * NB;
                     tl.last = last;
+                    const bool one = w.rows == w.valid && w.bad == 0;
+                    tl.all_lo = one ? w.max_lo : INT32_MAX;
+                    tl.all_hi = one ? w.min_hi : -1;
                 }
                 if (first)  // (the softmax is past tile t - 4, and with it past the first tile of segment i - 4)
 #pragma unroll
@@ -328,59 +333,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kst = 0, vst = 0, vpar = 0, segs = 0, note = 0;
             bool ok = wait(&sm.kfull[0], 0) && wait(&sm.qbar, 0);
             uint32_t begun = 0;  // row tiles that have had a product of the segment
-            auto qk = [&](uint32_t w) {
-                const uint64_t da = dq + w * (kQBytes >> 4), db = dk + kst * (kTileBytes >> 4);
-                if (!(note & kIdle << w))
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)  // 16 dims each
-                        tc::mma_f16(tmem + 128u * w, da + (i < 4 ? 2 * i : (kQBytes >> 5) + 2 * (i - 4)),
-                                    db + (i < 4 ? 2 * i : 64 + 2 * (i - 4)), kIdescQk, i > 0);
-                arrive(&sm.sbar[w]);  // (hands the tile's ring entry on, which came with its K)
-                tc::commit(&sm.sbar[w]);
-                if (w == 1) tc::commit(&sm.kempty[kst]);
-            };
-            if (ok) {
-                tc::fence_after_sync();
-                note = sm.ring[0].note;
-                qk(0);
-                qk(1);
-            }
-            for (int t = 0; t < run && ok; ++t) {
+            // Step t: P V of tile t, Q K of tile t + 1 (from t = -1 on), of the row tiles in turn.
+            for (int t = -1; t < run && ok; ++t) {
                 const uint32_t of = note;
-                const bool more = t + 1 < run, turn = (of & kLast) != 0;
+                const bool more = t + 1 < run, turn = t < 0 || (of & kLast) != 0;
                 if (of & kFirst) begun = 0;
-                ok = wait(&sm.go[vst], vpar);  // V of this tile and K of the next are there
-                tc::fence_after_sync();
-                if (more) {
-                    if (++kst == kStagesK) kst = 0;
-                    note = sm.ring[(t + 1) & (kRing - 1)].note;
+                if (t >= 0) {
+                    if (!(ok = wait(&sm.go[vst], vpar))) break;  // V of this tile and K of the next are there
+                    if (more && ++kst == kStagesK) kst = 0;
                 }
+                tc::fence_after_sync();
+                if (more) note = sm.ring[(t + 1) & (kRing - 1)].note;
                 const uint64_t db = dv + vst * (kTileBytes >> 4);
 #pragma unroll
-                for (uint32_t w = 0; w < 2; ++w) {
-                    if (!(ok = ok && wait(&sm.pbar[w], (uint32_t)(t & 1)))) break;
-                    tc::fence_after_sync();
-                    if (!(of & kIdle << w)) {
+                for (uint32_t i = 0; i < 4; ++i) {  // P V 0, Q K 0, P V 1, Q K 1; at a turn both P V first
+                    if (t < 0 && i < 2) continue;
+                    const uint32_t w = turn ? i & 1 : i >> 1;
+                    if (turn ? i < 2 : !(i & 1)) {
+                        if (!(ok = wait(&sm.pbar[w], (uint32_t)(t & 1)))) break;
+                        tc::fence_after_sync();
+                        if (!(of & kIdle << w)) {
+                            const uint32_t d = tmem + 256u + 128u * w, a = tmem + 128u * w;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)  // 16 keys each
-                            tc::mma_f16_ts(tmem + 256u + 128u * w, tmem + 128u * w + 8u * i, db + (2 * kRegionBytes >> 4) * i, kIdescPv,
-                                           (begun >> w & 1u) || i > 0);
-                        begun |= 1u << w;
+                            for (int k = 0; k < 8; ++k)  // 16 keys each
+                                tc::mma_f16_ts(d, a + 8u * k, db + (2 * kRegionBytes >> 4) * k, kIdescPv, (begun >> w & 1u) || k > 0);
+                            begun |= 1u << w;
+                        }
+                        if (turn) {
+                            arrive(&sm.obar[w]);  // (hands the checking warps' notes on)
+                            tc::commit(&sm.obar[w]);
+                        }
+                        if (w == 1) tc::commit(&sm.vempty[vst]);
+                    } else if (more) {
+                        if (turn && w == 0 && t >= 0) {
+                            if (!(ok = wait(&sm.qbar, ++segs & 1u))) break;
+                            tc::fence_after_sync();
+                        }
+                        const uint64_t da = dq + w * (kQBytes >> 4), dk1 = dk + kst * (kTileBytes >> 4);
+                        if (!(note & kIdle << w)) {
+                            const uint32_t d = tmem + 128u * w;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)  // 16 dims each
+                                tc::mma_f16(d, da + (k < 4 ? 2 * k : (kQBytes >> 5) + 2 * (k - 4)), dk1 + (k < 4 ? 2 * k : 64 + 2 * (k - 4)),
+                                            kIdescQk, k > 0);
+                        }
+                        arrive(&sm.sbar[w]);  // (hands the tile's ring entry on, which came with its K)
+                        tc::commit(&sm.sbar[w]);
+                        if (w == 1) tc::commit(&sm.kempty[kst]);
                     }
-                    if (turn) {
-                        arrive(&sm.obar[w]);  // (hands the checking warps' notes on)
-                        tc::commit(&sm.obar[w]);
-                    }
-                    if (w == 1) tc::commit(&sm.vempty[vst]);
-                    if (more && !turn) qk(w);
                 }
-                if (++vst == kStagesV) vst = 0, vpar ^= 1u;
-                if (more && turn) {
-                    if (!(ok = ok && wait(&sm.qbar, ++segs & 1u))) break;
-                    tc::fence_after_sync();
-                    qk(0);
-                    qk(1);
-                }
+                if (t >= 0 && ++vst == kStagesV) vst = 0, vpar ^= 1u;
             }
             if (!ok) {  // the products issued end before their memory goes away
                 give_up();
@@ -406,21 +408,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!(note & kAll)) {
                 Cleared& to = sm.cleared[(segs - 1) & 7];
-                uint4* v = reinterpret_cast<uint4*>(vs + st * kTileBytes + half * 8 * kRegionBytes);
-#pragma unroll 4
-                for (int i = 0; i < 32; ++i) {  // a quarter of a region each
-                    const uint4 x = v[i * 32 + lane];
-                    uint32_t xs[4] = {x.x, x.y, x.z, x.w}, bad[4];
+#pragma unroll 1
+                for (int r = half * 8; r < half * 8 + 8; ++r) {
+                    const int tok = tl.t0 + r * 8;
+                    if (tok >= tl.all_lo && tok + 7 <= tl.all_hi) continue;
+                    uint4* v = reinterpret_cast<uint4*>(vs + st * kTileBytes + r * kRegionBytes);
+                    uint4 x[4];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) bad[y] = ((xs[y] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // an exponent of all ones
-                    if (__builtin_expect((bad[0] | bad[1] | bad[2] | bad[3]) != 0, 0)) {
+                    for (int i = 0; i < 4; ++i) x[i] = v[i * 32 + lane];
+                    auto top = [](uint32_t u) { return (u & 0x7fff7fffu) + 0x00800080u; };  // bits 15 and 31: an exponent of all ones
+                    uint32_t any = 0;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) xs[y] &= ~((bad[y] >> 15) * 0xffffu);
-                        v[i * 32 + lane] = make_uint4(xs[0], xs[1], xs[2], xs[3]);
-                        const int r = half * 8 + (i >> 2), tok = tl.t0 + r * 8 + (((i & 1) * 32 + lane) >> 3);
-                        if (tl.ok >> r & 1u) {
-                            atomicMin(&to.lo, tok);
-                            atomicMax(&to.hi, tok);
+                    for (int i = 0; i < 4; ++i) any |= top(x[i].x) | top(x[i].y) | top(x[i].z) | top(x[i].w);
+                    if (__builtin_expect(any & 0x80008000u, 0)) {
+#pragma unroll 1
+                        for (int i = 0; i < 16; ++i) {
+                            uint32_t* at = reinterpret_cast<uint32_t*>(v + (i >> 2) * 32 + lane) + (i & 3);
+                            const uint32_t bad = top(*at) & 0x80008000u;
+                            if (bad == 0) continue;
+                            *at &= ~((bad >> 15) * 0xffffu);
+                            if (tl.ok >> r & 1u) {
+                                const int token = tok + (((i >> 2 & 1) * 32 + lane) >> 3);
+                                atomicMin(&to.lo, token);
+                                atomicMax(&to.hi, token);
+                            }
                         }
                     }
                 }
@@ -478,14 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::ld32(lanes + 256u + 128u * w + c, o);
 #pragma unroll
                 for (int d = 0; d < 32; ++d) o[d] = l == 0.0f ? 0.0f : o[d] * f;
-                if (__builtin_expect(first <= last && l != 0.0f, 0)) {
-                    const uint2 m = not_finite(p, p.row_seq[e_n0 + j], e_g, c, first, last);
-#pragma unroll
-                    for (int d = 0; d < 32; ++d) {
-                        if (m.x >> d & 1u) o[d] += INFINITY;
-                        if (m.y >> d & 1u) o[d] -= INFINITY;
-                    }
-                }
                 if (whole && pos != -1) {
 #pragma unroll
                     for (int d = 0; d < 32; d += 16) {
@@ -504,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
+            if (__builtin_expect(first <= last && l != 0.0f, 0))
+                add_not_finite(p, p.row_seq[e_n0 + j], e_g, 64 * half, first, last, p.out + at * 128 + 64 * half,
+                               whole ? nullptr : st + 512 + 8 * half * 2048 + hr * 8);
             if (!whole && begins && hr == 0 && half == 0) p.shared_items[blockIdx.x] = make_int4(e_n0, e_g, (int)blockIdx.x, e_last);
             return true;
         };
@@ -528,80 +534,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::got32(x[1]);
             if (idle) {
                 if (group_or(pair, 64, bad)) break;
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) arrive(&sm.pbar[w]);
-                if ((note & kLast) && !epilogue(segs++)) break;
-                continue;
-            }
-            if (!(note & kAll)) {  // the columns that the row sees: from .. to - 1, of readable regions
-                int from = 0, to = 0;
-                if (pos >= 0 && (tl.rows >> j & 1u)) {
-                    from = min(max(lo - tl.t0 - 64 * half, 0), 64);
-                    to = min(max(pos - tl.t0 + 1 - 64 * half, 0), 64);
-                }
+            } else {
+                if (!(note & kAll)) {  // the columns that the row sees: from .. to - 1, of readable regions
+                    int from = 0, to = 0;
+                    if (pos >= 0 && (tl.rows >> j & 1u)) {
+                        from = min(max(lo - tl.t0 - 64 * half, 0), 64);
+                        to = min(max(pos - tl.t0 + 1 - 64 * half, 0), 64);
+                    }
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t okr = tl.ok >> (8 * half + 4 * c) & 15u;
-                    const uint32_t below = to - 32 * c >= 32 ? ~0u : (1u << max(to - 32 * c, 0)) - 1u;
-                    const uint32_t under = from - 32 * c >= 32 ? ~0u : (1u << max(from - 32 * c, 0)) - 1u;
-                    const uint32_t mask = below & ~under & ((okr * 0x00204081u & 0x01010101u) * 0xffu);
-                    if (__any_sync(0xffffffffu, mask != ~0u))
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t okr = tl.ok >> (8 * half + 4 * c) & 15u;
+                        const uint32_t below = to - 32 * c >= 32 ? ~0u : (1u << max(to - 32 * c, 0)) - 1u;
+                        const uint32_t under = from - 32 * c >= 32 ? ~0u : (1u << max(from - 32 * c, 0)) - 1u;
+                        const uint32_t mask = below & ~under & ((okr * 0x00204081u & 0x01010101u) * 0xffu);
+                        if (__any_sync(0xffffffffu, mask != ~0u))
 #pragma unroll
-                        for (int d = 0; d < 32; ++d) x[c][d] = mask >> d & 1u ? x[c][d] : 0xff800000u;
-                }
-            }
-            // the largest logit of the thread's keys (in log2 units); the running maximum follows the row's when it is
-            // passed by more than the slack, which rescales l and O
-            float m2[2] = {__uint_as_float(x[0][0]), __uint_as_float(x[0][1])};
-#pragma unroll
-            for (int d = 2; d < 62; d += 4) {
-                m2[0] = max3(m2[0], __uint_as_float(x[d / 32][d % 32]), __uint_as_float(x[(d + 1) / 32][(d + 1) % 32]));
-                m2[1] = max3(m2[1], __uint_as_float(x[(d + 2) / 32][(d + 2) % 32]), __uint_as_float(x[(d + 3) / 32][(d + 3) % 32]));
-            }
-            float mx = max3(m2[0], m2[1], fmaxf(__uint_as_float(x[1][30]), __uint_as_float(x[1][31]))) * p.scale_log2;
-            auto passed = [&](float m) { return m > kSlack - neg_m || (neg_m == INFINITY && m > -INFINITY); };
-            // (the pair's barrier also stands between the reads of S and P, which takes its place)
-            tc::fence_before_sync();
-            if (__builtin_expect(group_or(pair, 64, passed(mx) || bad), 0)) {
-                if (group_or(pair, 64, bad)) break;
-                mx = joined(mx, [](float a, float b) { return fmaxf(a, b); });
-                float f = 1.0f;
-                if (passed(mx)) {
-                    f = ex2(-neg_m - mx);
-                    l *= f;
-                    neg_m = -mx;
-                }
-                if (begun) {
-#pragma unroll 1
-                    for (int c = 0; c < 64; c += 16) {
-                        float o[16];
-                        tc::ld16(o_at + c, o);
-#pragma unroll
-                        for (int d = 0; d < 16; ++d) o[d] *= f;
-                        tc::st16(o_at + c, o);
+                            for (int d = 0; d < 32; ++d) x[c][d] = mask >> d & 1u ? x[c][d] : 0xff800000u;
                     }
                 }
-            }
-            tc::fence_after_sync();
-            // weights, 8 bits each in bf16 as V is
-            const float2 scale = both(p.scale_log2), nm = both(neg_m == INFINITY ? 0.0f : neg_m);
-            float2 sum[2] = {both(0.0f), both(0.0f)};
+                // the largest logit of the thread's keys (in log2 units); the running maximum follows the row's when it is
+                // passed by more than the slack, which rescales l and O
+                float m2[2] = {__uint_as_float(x[0][0]), __uint_as_float(x[0][1])};
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int d = 0; d < 32; d += 2) {
-                    const float2 y = fma2(make_float2(__uint_as_float(x[c][d]), __uint_as_float(x[c][d + 1])), scale, nm);
-                    const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
-                    sum[d / 2 & 1] = add2(sum[d / 2 & 1], e2);
-                    pk[d / 2] = pack_bf16x2(e2.x, e2.y);
+                for (int d = 2; d < 62; d += 4) {
+                    m2[0] = max3(m2[0], __uint_as_float(x[d / 32][d % 32]), __uint_as_float(x[(d + 1) / 32][(d + 1) % 32]));
+                    m2[1] = max3(m2[1], __uint_as_float(x[(d + 2) / 32][(d + 2) % 32]), __uint_as_float(x[(d + 3) / 32][(d + 3) % 32]));
                 }
-                tc::st16u(p_at + 16 * c, pk);
+                float mx = max3(m2[0], m2[1], fmaxf(__uint_as_float(x[1][30]), __uint_as_float(x[1][31]))) * p.scale_log2;
+                auto passed = [&](float m) { return m > kSlack - neg_m || (neg_m == INFINITY && m > -INFINITY); };
+                // (the pair's barrier also stands between the reads of S and P, which takes its place)
+                tc::fence_before_sync();
+                if (__builtin_expect(group_or(pair, 64, passed(mx) || bad), 0)) {
+                    if (group_or(pair, 64, bad)) break;
+                    mx = joined(mx, [](float a, float b) { return fmaxf(a, b); });
+                    float f = 1.0f;
+                    if (passed(mx)) {
+                        f = ex2(-neg_m - mx);
+                        l *= f;
+                        neg_m = -mx;
+                    }
+                    if (begun) {
+#pragma unroll 1
+                        for (int c = 0; c < 64; c += 16) {
+                            float o[16];
+                            tc::ld16(o_at + c, o);
+#pragma unroll
+                            for (int d = 0; d < 16; ++d) o[d] *= f;
+                            tc::st16(o_at + c, o);
+                        }
+                    }
+                }
+                tc::fence_after_sync();
+                // weights, 8 bits each in bf16 as V is
+                const float2 scale = both(p.scale_log2), nm = both(neg_m == INFINITY ? 0.0f : neg_m);
+                float2 sum[2] = {both(0.0f), both(0.0f)};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int d = 0; d < 32; d += 2) {
+                        const float2 y = fma2(make_float2(__uint_as_float(x[c][d]), __uint_as_float(x[c][d + 1])), scale, nm);
+                        const float2 e2 = make_float2(ex2(y.x), ex2(y.y));
+                        sum[d / 2 & 1] = add2(sum[d / 2 & 1], e2);
+                        pk[d / 2] = pack_bf16x2(e2.x, e2.y);
+                    }
+                    tc::st16u(p_at + 16 * c, pk);
+                }
+                begun = true;
+                sum[0] = add2(sum[0], sum[1]);
+                l += sum[0].x + sum[0].y;
             }
-            begun = true;
-            sum[0] = add2(sum[0], sum[1]);
-            l += sum[0].x + sum[0].y;
             tc::wait_st();
             tc::fence_before_sync();
             __syncwarp();

@@ -24,6 +24,7 @@ __device__ __forceinline__ bool group_or(int id, int threads, bool v) {
 // Waits for phase `parity` of the barrier; gives up after 2^22 polls (far beyond any copy or product).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) {
     const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
     for (uint32_t i = 0; i < (1u << 22); ++i) {
         uint32_t done;
         asm volatile(
