@@ -857,7 +857,8 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
     t["q"] rotated into q_rot by cos/sin), then summarise, score + select over the indexer
     tensors of ``t`` as decode_step does, and attend over the picked regions of the cache.  With ``plan``,
     (table, rows, lengths, new_tokens) as step5_paged_plan takes them, the step is planned first, and its
-    rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end."""
+    rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end.  (Rows that it pads have no
+    picks and no output, and the scoring, which knows no padding, sets DEV_RANGE for them.)"""
     rows = t
     if plan is not None:
         step5_paged_plan(*plan, stream=stream, geom=geom)

@@ -711,8 +711,8 @@ cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     if ((int64_t)p.N * p.G * p.pages.table_len * p.pages.page_tokens <= 1 << 17)
         return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
     if constexpr (H <= 8)
-        if (p.N >= 3 * p.B) return launch_shape<Shape<H, 4, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
-    if (p.N >= 2 * p.B) return launch_shape<Shape<H, 2, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+        if (p.N >= (int64_t)3 * p.B) return launch_shape<Shape<H, 4, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (p.N >= (int64_t)2 * p.B) return launch_shape<Shape<H, 2, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
     return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
 }
 

@@ -26,7 +26,7 @@ struct Row {
 __device__ __forceinline__ Row row_of(const PagedAttnParams& p, int b, int pos) {
     Row r{b, pos, 0};
     if (r.b == -1) return r;
-    if (r.b < 0 || r.b >= p.B || r.pos < 0 || r.pos / p.pages.page_tokens >= p.pages.table_len) {
+    if (r.b < 0 || r.b >= p.B || r.pos < 0 || r.pos >= p.pages.page_tokens * p.pages.table_len) {  // (fits int32)
         r.b = -2;
         return r;
     }

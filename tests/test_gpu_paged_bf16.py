@@ -450,6 +450,44 @@ def test_contiguous_caches_as_pages(s5):  # noqa: F811
     assert float(((got.double() - other.double()).cpu().abs() / (2 * B16.tolerance(out, mass, True))).max()) <= 1.0
 
 
+@pytest.mark.parametrize("n", [1, 5, 200])
+def test_padding_alone(s5, n):  # noqa: F811
+    """Calls whose every row is padding write nothing."""
+    for picks in (False, True):
+        c = Case(s5, [(-1, 0, n)], G=2, B=1, top_k=8)
+        c = c.pick() if picks else c
+        assert bool((c.run() == 5.0).all()) and status(s5) == 0
+
+
+@pytest.mark.parametrize("runs", [[(0, 900, 1), (1, 77, 1)], [(0, 700, 3), (1, 9, 4)], [(0, 650, 60), (1, 0, 60)]])
+def test_dense_over_contiguous_caches(s5, runs):  # noqa: F811
+    c = Case(s5, runs, G=2, pt=2048, seed=5)
+    c.k, c.v, c.table = c.k[:2].contiguous(), c.v[:2].contiguous(), None
+    got = c.run(100, cache=s5.PagedCache(*dev(c.k, c.v)))
+    assert status(s5) == 0
+    c.near(got.cpu(), *c.want(100))
+
+
+def test_most_rows_of_a_call(s5):  # noqa: F811
+    """65,535 rows, on their own and sharing tiles, against a few of them alone."""
+    for B, runs in ((65535, [(b, b % 40, 1) for b in range(65535)]), (1, [(0, 0, 65535)])):
+        c = Case(s5, [(0, 0, 1)], G=1, hq=4, pt=64, B=1, seed=3)
+        seq, pos = rows_of(*runs)
+        length = -(-(int(pos.max()) + 1) // 64)
+        k, v = (torch.randn((2 * length, 1, 64, 128), generator=torch.Generator("cuda").manual_seed(i), device="cuda").bfloat16() for i in (1, 2))
+        table = torch.arange(2 * length, device="cuda").int()[:length].expand(B, length).contiguous()
+        cache = s5.PagedCache(k, v, table)
+        q = torch.randn((65535, 4, 128), generator=torch.Generator("cuda").manual_seed(3), device="cuda").bfloat16()
+        out = torch.full_like(q, 5.0)
+        s5.step5_paged_attn(c.geom, q, cache, *dev(seq, pos), out, c.ws, window=300)
+        assert status(s5) == 0
+        some = torch.tensor([0, 1, 17, 31, 32, 33, 40000, 65533, 65534])
+        want = B16.attend(q[some].cpu(), k.cpu(), v.cpu(), table[:1].cpu(), torch.zeros(9, dtype=torch.int32), pos[some],
+                          c.geom.softmax_scale, 300)
+        assert B16.off(out[some], *want, B == 1) <= 1.0
+        assert not bool((out == 5.0).all(-1).any())
+
+
 def test_run_together(s5):  # noqa: F811
     """Prompts planned, appended and attended in chunks, then decode steps of the whole path with their plan, drafts
     rolled back, over bf16 pages: every output is the attention over what the cache holds."""
