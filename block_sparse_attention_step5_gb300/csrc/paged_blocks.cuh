@@ -142,7 +142,17 @@ struct Walk {
 struct BlockRun {
     int64_t of_group, total, per, start;  // tiles of a group, of all, of a run
     int run, g0;                          // the run's tiles and first group
+    bool dealt;                           // back to front: item dealt_item(round) of each round instead
 };
+// The item (block, group) of a CTA in a round of items dealt out back to front; false past the last.
+template <class S>
+__device__ __forceinline__ bool dealt_item(const PagedAttnParams& p, int round, int& blk, int& g) {
+    const int blocks = (p.N + S::NB - 1) / S::NB, c = (int)blockIdx.x, n = (int)gridDim.x;
+    const int k = round * n + (round & 1 ? n - 1 - c : c);
+    blk = blocks - 1 - k / p.G;
+    g = k % p.G;
+    return k < blocks * p.G;
+}
 template <int THREADS>
 struct BlockRunSmem {
     int64_t scan[THREADS / 32];
@@ -152,7 +162,9 @@ struct BlockRunSmem {
 // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups
 // (every thread calls it, and the block meets at a barrier behind it).  tiles: room for a number a block.
 // WHOLE > 0: whole items go to a CTA instead where that takes the busiest one at most WHOLE tiles more than an equal
-// share (an item's share goes by its middle tile); tiles then has room for kChunkMaxCtas numbers more.
+// share, dealt out in the items' order (an item goes by its middle tile) or from the last block back to the first, every other
+// round in the CTAs' reverse order (a chunk's last blocks have the most keys, so that large ones meet small ones),
+// whichever is better; tiles then has room for 2 kChunkMaxCtas numbers more.
 template <class S, int THREADS, int WHOLE = 0>
 __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunSmem<THREADS>& s, int* tiles) {
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -188,30 +200,34 @@ __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunS
     r.total = r.of_group * p.G;
     r.per = (r.total + gridDim.x - 1) / gridDim.x;
     r.start = blockIdx.x * r.per;
+    r.dealt = false;
     if constexpr (WHOLE > 0) {
         if (blocks * p.G <= 8 * kChunkMaxCtas && r.total < (1 << 24)) {  // (many items: the joins weigh little)
-            int* load = tiles + blocks;
-            for (int i = tid; i < (int)gridDim.x; i += THREADS) load[i] = 0;
+            int *load = tiles + blocks, *deal = load + kChunkMaxCtas;
+            for (int i = tid; i < (int)gridDim.x; i += THREADS) load[i] = deal[i] = 0;
             if (tid == 0) s.blk = INT32_MAX;
             __syncthreads();
-            const int per = (int)r.per, of_group = (int)r.of_group;
+            const int per = (int)r.per, of_group = (int)r.of_group, n = (int)gridDim.x;
             for (int g = 0; g < p.G; ++g) {
                 int at = g * of_group + (int)before;
                 for (int i = i0; i < i1; at += tiles[i], ++i)
                     if (tiles[i] > 0) {
-                        const int cta = (2 * at + tiles[i]) / (2 * per);
+                        const int cta = (2 * at + tiles[i]) / (2 * per), k = (blocks - 1 - i) * p.G + g, in = k % n;
                         atomicAdd(&load[cta], tiles[i]);
+                        atomicAdd(&deal[k / n & 1 ? n - 1 - in : in], tiles[i]);
                         if (cta == (int)blockIdx.x) atomicMin(&s.blk, g * blocks + i);
                     }
             }
             __syncthreads();
-            int most = 0;
-            for (int i = lane; i < (int)gridDim.x; i += 32) most = max(most, load[i]);
+            int most = 0, dealt = 0;
+            for (int i = lane; i < n; i += 32) most = max(most, load[i]), dealt = max(dealt, deal[i]);
             most = __reduce_max_sync(0xffffffffu, most);
-            const int first = s.blk;
-            if (most <= per + WHOLE) {
-                r.run = load[blockIdx.x];
-                r.g0 = r.run ? first / blocks : 0;
+            dealt = __reduce_max_sync(0xffffffffu, dealt);
+            if (min(most, dealt) <= per + WHOLE) {
+                const int first = s.blk;
+                r.dealt = dealt < most;
+                r.run = r.dealt ? deal[blockIdx.x] : load[blockIdx.x];
+                r.g0 = r.run && !r.dealt ? first / blocks : 0;
                 __syncthreads();  // (first is read)
                 if (tid == 0) s.blk = first % blocks, s.off = 0;
                 return r;

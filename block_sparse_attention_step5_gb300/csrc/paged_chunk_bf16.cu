@@ -42,7 +42,7 @@ constexpr float kSlack = 8.0f;                  // log2 units a weight may lie a
 
 // Tiles that the busiest CTA may have over an equal share before items are cut: what a cut costs, a partial state and its join
 // for most CTAs (window of 512: 53 us cut, 44 whole; three prompts of 701 rows 56.7 and 52.1).
-constexpr int kWholeTiles = 5;
+constexpr int kWholeTiles = 8;
 
 // A tile as the copying warp leaves it for the others.
 struct Tile {
@@ -154,14 +154,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sm.tmem;
     const int run = of.run, blk0 = sm.rs.blk, off0 = sm.rs.off, g0 = of.g0;
 
-    // Every role walks the run's segments alike: item (group, block), tiles off .. off + n - 1 of it.
+    // The copying warp walks the run's segments: item (group, block), tiles off .. off + n - 1 of it.
     // next() returns false when there is none (the rows have changed under the kernel).
     struct Segment {
         int g, blk, off, n, nt;
     };
+    int round = 0;
     auto next = [&](Segment& s, Walk<S>& w, int left) -> bool {
         for (;;) {
-            if (s.blk >= blocks) {
+            if (of.dealt) {
+                if (!dealt_item<S>(p, round++, s.blk, s.g)) return false;
+            } else if (s.blk >= blocks) {
                 s.blk = 0;
                 if (++s.g >= p.G) return false;
             }
