@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
     __shared__ uint32_t s_tmem;
     __shared__ int s_fail;
     __shared__ int s_note[kRing], s_t0[kRing];  // of a tile: product steps | kFirst | rows; (several rows) first token
-    __shared__ float red[3][4][C];
+    __shared__ float red[3][4][C], s_factor[C];  // s_factor: a column's gate over its sum, 0 without keys
     __shared__ int2 s_cleared[2];  // of segment i % 2 (several rows): first and last token whose values were cleared
     __shared__ RunSmem<kThreads> rs;
 
@@ -408,7 +408,17 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 failed = true;
                 return;
             }
-            float o[C], L[C];
+            const bool last = whole;
+            if (tid < C) {  // (a thread a column: the same in every thread is many instructions)
+                const float L = (rd[0][tid] + rd[1][tid]) + (rd[2][tid] + rd[3][tid]);
+                const int n = done.n + tid / H;
+                float f = L == 0.0f ? 0.0f : 1.0f / L;
+                if (last && p.gate != nullptr && L != 0.0f && n < p.N) f = gated(p, (int64_t)n * p.Hq + (int64_t)done.g * H + tid % H, f);
+                s_factor[tid] = f;
+                if (!last) p.states[((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState + C + tid] = L;
+            }
+            group_or(1, kSoft, false);
+            float o[C];
             {
                 constexpr int n = C < 16 ? 16 : C;  // (fewer than 16 columns: both parts in one load)
                 float a[n], b[n];
@@ -423,8 +433,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                L[c] = (rd[0][c] + rd[1][c]) + (rd[2][c] + rd[3][c]);
-                o[c] = L[c] == 0.0f ? 0.0f : o[c] / L[c];
+                const float f = s_factor[c];
+                o[c] = f == 0.0f ? 0.0f : o[c] * f;
             }
             if constexpr (R > 1) {  // values that were cleared, in the rows that see them
                 const int2 cl = s_cleared[(segs - 1) & 1];
@@ -438,17 +448,16 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                         if (!(fabsf(v) < INFINITY))
 #pragma unroll
                             for (int h = 0; h < H; ++h)
-                                if (L[r * H + h] != 0.0f) o[r * H + h] += v;
+                                if (s_factor[r * H + h] != 0.0f) o[r * H + h] += v;
                     }
                 }
             }
-            if (whole) {
+            if (last) {
+                uint16_t* to = p.out + ((int64_t)done.n * p.Hq + (int64_t)done.g * H) * 128 + key;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const int64_t at = (int64_t)(done.n + c / H) * p.Hq + (int64_t)done.g * H + c % H;
                     if (R > 1 && done_set.b[c / H] == -1) continue;
-                    if (p.gate != nullptr && L[c] != 0.0f) o[c] = gated(p, at, o[c]);  // (zero stays zero)
-                    p.out[at * 128 + key] = f32_to_bf16_bits(o[c]);
+                    to[((int64_t)(c / H) * p.Hq + c % H) * 128] = f32_to_bf16_bits(o[c]);
                 }
             } else {  // CTAs first .. last share the item; each leaves its state, which the join kernel reads
                 float* st = p.states + ((int64_t)2 * blockIdx.x + (begins ? 1 : 0)) * S::kState;
@@ -456,10 +465,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
                 for (int c = 0; c < C; ++c) st[2 * C + c * 128 + key] = o[c];
                 if (key == 0)
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        st[c] = -(c & 1 ? neg_m[c / 2].y : neg_m[c / 2].x);
-                        st[C + c] = L[c];
-                    }
+                    for (int c = 0; c < C; ++c) st[c] = -(c & 1 ? neg_m[c / 2].y : neg_m[c / 2].x);
             }
             if (!whole && begins && tid == 0) {
                 if (few)
@@ -470,22 +476,23 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
         };
 
         int nitem = item0, off = off0;
-        for (int left = run; left > 0;) {
-            it = rs.it;
-            if (t > 0) {
-                it.tiles = 0;
-                while (nitem < items && (it = item_of<PICKS, R>(p, nitem)).tiles <= off) ++nitem;
+        for (int left = run;;) {
+            if (left > 0) {
+                it = rs.it;
+                if (t > 0) {
+                    it.tiles = 0;
+                    while (nitem < items && (it = item_of<PICKS, R>(p, nitem)).tiles <= off) ++nitem;
+                }
+                if (nitem >= items) {
+                    give_up();
+                    break;
+                }
+                ++nitem;
+                if constexpr (R > 1) set = rows_at<R>(p, it.n);
+                build_q();
             }
-            if (nitem >= items) {
-                give_up();
-                failed = true;
-                break;
-            }
-            ++nitem;
-            if constexpr (R > 1) set = rows_at<R>(p, it.n);
-            build_q();
             if (t > 0) epilogue();
-            if (failed) break;
+            if (failed || left <= 0) break;
             if (tid == 0) {
                 if (R == 1 && it.b == -2) raise_status(p.status, kDevRange);
                 if constexpr (R > 1) {
@@ -656,7 +663,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas)
             }
             if (failed) break;
         }
-        if (!failed) epilogue();
     }
     tc::fence_before_sync();
     __syncthreads();
