@@ -713,12 +713,18 @@ cudaError_t launch_heads(const PagedAttnParams& p, const CUtensorMap& kmap, cons
     // together: 2 rows of each of 4 sequences of 8,192 tokens 24 and 19, of 32,768 tokens 68 and 52; 4 rows of each of 8 of
     // 8,192 61 and 41, of 32,768 314 and 98; 4 rows of one of 32,768 34 and 21.  The longer chain of a tile shows where all rows'
     // keys are few: 4 rows of one sequence of 8,192 15 and 17, of each of 4 of 1,000 11.6 and 16.3, of each of 8 of 1,000
-    // 17.8 and 18.6.  (The host knows what the table can hold, not the lengths.)
-    if ((int64_t)p.N * p.G * p.pages.table_len * p.pages.page_tokens <= 1 << 17)
-        return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    // 17.8 and 18.6, 2 rows of each of 16 in a window of 512 12.1 and 15.5.  (The host knows what the table can hold, not the
+    // lengths.)
+    const int64_t cap = (int64_t)p.pages.table_len * p.pages.page_tokens;
+    const int64_t keys = (p.window > 0 && p.window < cap ? p.window : cap) * p.N * p.G;  // at most, of all rows and groups
+    const bool few_keys = keys <= 1 << 17;
     if constexpr (H <= 8)
-        if (p.N >= (int64_t)3 * p.B) return launch_shape<Shape<H, 4, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
-    if (p.N >= (int64_t)2 * p.B) return launch_shape<Shape<H, 2, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+        if (!few_keys && p.N >= (int64_t)3 * p.B) return launch_shape<Shape<H, 4, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    if (!few_keys && p.N >= (int64_t)2 * p.B) return launch_shape<Shape<H, 2, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
+    // Many tiles are shared out finer by two CTAs an SM: 16 rows of 16K to 32K tokens 124 us against 134 with one, one of
+    // 524,288 159 against 161, 16 of 4K to 8K with 4 heads 40 against 41; 32 rows of 512 in a window 13.7 against 11.3.
+    if constexpr (H <= 8)
+        if (keys >= 1 << 19) return launch_shape<Shape<H, 1, false, 2>>(p, kmap, vmap, num_sms, stream, pdl);
     return launch_shape<Shape<H, 1, false, 1>>(p, kmap, vmap, num_sms, stream, pdl);
 }
 

@@ -178,6 +178,26 @@ def test_drafts_of_windows_that_lie_apart(s5, bad):  # noqa: F811
     c.near(got, *want)
 
 
+@pytest.mark.parametrize("G, hq, pt", [(8, 4, 16), (8, 8, 64), (8, 16, 40)])
+def test_drafts_in_long_windows(s5, G, hq, pt):  # noqa: F811
+    """Windows long enough for rows to read their keys together, their first tokens inside tiles."""
+    Case(s5, [(b, 3000 + 137 * b, 4) for b in range(3)] + [(3, 500, 2), (-1, 0, 1), (4, 2222, 3)], G, hq, pt, seed=hq).check(1100)
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+def test_long_windows_of_one_item_that_lie_apart(s5, bad):  # noqa: F811
+    """As above, and with a gap between the windows of an item's rows: what lies there is not touched."""
+    c = Case(s5, [(0, 9000, 2), (0, 1300, 2), (1, 7000, 3), (1, 40, 1), (2, 5000, 8)], G=8, hq=8, pt=16, seed=8)
+    want = c.want(1100)
+    mask = c.unseen(1100)[:, None, :, None]
+    c.k.masked_fill_(mask, bad)
+    c.v.masked_fill_(mask, bad)
+    c.table[0, 100:480], c.table[1, 10:350] = -1, 10 ** 7
+    got = c.run(1100).cpu()
+    assert status(s5) == 0
+    c.near(got, *want)
+
+
 def test_drafts_on_bad_pages_and_out_of_range(s5):  # noqa: F811
     c = Case(s5, [(0, 500, 4), (1, 90, 4), (2, 33, 4)], G=4, pt=32, seed=6, extra=20000)
     c.table[0, 3], c.table[2, 0], c.table[2, 1] = -1, 10 ** 6, -9
