@@ -162,10 +162,10 @@ struct BlockRunSmem {
 // The blocks' tiles (the same for every group), a warp to a block, then this CTA's run of the tiles of all groups
 // (every thread calls it, and the block meets at a barrier behind it).  tiles: room for a number a block.
 // WHOLE > 0: whole items go to a CTA instead where that takes the busiest one at most WHOLE tiles more than an equal
-// share, dealt out in the items' order (an item goes by its middle tile) or from the last block back to the first, every other
+// share (an item counting its tiles and ITEM more), dealt out in the items' order (an item goes by its middle tile) or from the last block back to the first, every other
 // round in the CTAs' reverse order (a chunk's last blocks have the most keys, so that large ones meet small ones),
-// whichever is better; tiles then has room for 2 kChunkMaxCtas numbers more.
-template <class S, int THREADS, int WHOLE = 0>
+// whichever is better; tiles then has room for 4 kChunkMaxCtas numbers more.
+template <class S, int THREADS, int WHOLE = 0, int ITEM = 0>
 __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunSmem<THREADS>& s, int* tiles) {
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int blocks = (p.N + S::NB - 1) / S::NB;
@@ -203,30 +203,34 @@ __device__ __forceinline__ BlockRun take_run(const PagedAttnParams& p, BlockRunS
     r.dealt = false;
     if constexpr (WHOLE > 0) {
         if (blocks * p.G <= 8 * kChunkMaxCtas && r.total < (1 << 24)) {  // (many items: the joins weigh little)
-            int *load = tiles + blocks, *deal = load + kChunkMaxCtas;
-            for (int i = tid; i < (int)gridDim.x; i += THREADS) load[i] = deal[i] = 0;
+            // [0], [1]: tiles and costs in order; [2], [3]: dealt out.  An item costs its tiles and ITEM more.
+            int(*load)[kChunkMaxCtas] = reinterpret_cast<int(*)[kChunkMaxCtas]>(tiles + blocks);
+            for (int i = tid; i < 4 * kChunkMaxCtas; i += THREADS) load[0][i] = 0;
             if (tid == 0) s.blk = INT32_MAX;
             __syncthreads();
-            const int per = (int)r.per, of_group = (int)r.of_group, n = (int)gridDim.x;
+            const int n = (int)gridDim.x, of_group = (int)r.of_group + ITEM * blocks, per = (of_group * p.G + n - 1) / n;
             for (int g = 0; g < p.G; ++g) {
-                int at = g * of_group + (int)before;
-                for (int i = i0; i < i1; at += tiles[i], ++i)
+                int at = g * of_group + (int)before + ITEM * i0;
+                for (int i = i0; i < i1; at += tiles[i] + ITEM, ++i)
                     if (tiles[i] > 0) {
-                        const int cta = (2 * at + tiles[i]) / (2 * per), k = (blocks - 1 - i) * p.G + g, in = k % n;
-                        atomicAdd(&load[cta], tiles[i]);
-                        atomicAdd(&deal[k / n & 1 ? n - 1 - in : in], tiles[i]);
+                        const int cost = tiles[i] + ITEM, cta = (2 * at + cost) / (2 * per);
+                        const int k = (blocks - 1 - i) * p.G + g, in = k % n, to = k / n & 1 ? n - 1 - in : in;
+                        atomicAdd(&load[0][cta], tiles[i]);
+                        atomicAdd(&load[1][cta], cost);
+                        atomicAdd(&load[2][to], tiles[i]);
+                        atomicAdd(&load[3][to], cost);
                         if (cta == (int)blockIdx.x) atomicMin(&s.blk, g * blocks + i);
                     }
             }
             __syncthreads();
             int most = 0, dealt = 0;
-            for (int i = lane; i < n; i += 32) most = max(most, load[i]), dealt = max(dealt, deal[i]);
+            for (int i = lane; i < n; i += 32) most = max(most, load[1][i]), dealt = max(dealt, load[3][i]);
             most = __reduce_max_sync(0xffffffffu, most);
             dealt = __reduce_max_sync(0xffffffffu, dealt);
             if (min(most, dealt) <= per + WHOLE) {
                 const int first = s.blk;
                 r.dealt = dealt < most;
-                r.run = r.dealt ? deal[blockIdx.x] : load[blockIdx.x];
+                r.run = load[r.dealt ? 2 : 0][blockIdx.x];
                 r.g0 = r.run && !r.dealt ? first / blocks : 0;
                 __syncthreads();  // (first is read)
                 if (tid == 0) s.blk = first % blocks, s.off = 0;

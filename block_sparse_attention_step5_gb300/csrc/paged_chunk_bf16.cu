@@ -43,6 +43,7 @@ constexpr float kSlack = 8.0f;                  // log2 units a weight may lie a
 // Tiles that the busiest CTA may have over an equal share before items are cut: what a cut costs, a partial state and its join
 // for most CTAs (window of 512: 53 us cut, 44 whole; three prompts of 701 rows 56.7 and 52.1).
 constexpr int kWholeTiles = 8;
+constexpr int kItemTiles = 2;  // what an item takes beside its tiles: q, the turn of the products, the epilogue
 
 // A tile as the copying warp leaves it for the others.
 struct Tile {
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     if (tid == 0) p.shared_items[blockIdx.x].w = -1;
-    const BlockRun of = take_run<S, kThreads, kWholeTiles>(p, sm.rs, reinterpret_cast<int*>(smem));  // (nothing is copied yet)
+    const BlockRun of = take_run<S, kThreads, kWholeTiles, kItemTiles>(p, sm.rs, reinterpret_cast<int*>(smem));  // (nothing is copied yet)
     const int64_t per = of.per, start = of.start;
     fence_proxy_async();  // (the copies write where the tiles' numbers were)
     tc::fence_before_sync();
