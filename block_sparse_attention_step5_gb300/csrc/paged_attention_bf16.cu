@@ -19,16 +19,16 @@
 // cleared and the token noted; the rows that see it take it up again from the page at their end.
 //
 // The split of the work, the roles of the warps and the join are those of the kernel over the e4m3 pages.  A tile is 64 KB, so one
-// CTA an SM with 5 or 6 of them half in flight keeps HBM busy; picks, whose copies are 2 KB each, want two CTAs (a CTA's copies of
-// that size come at 44 GB/s out of L2, two CTAs' at 87).
+// CTA an SM with 5 or 6 half tiles in shared memory, or two with 3, keep HBM busy; picks, whose copies are 2 KB each, want two CTAs
+// (a CTA's copies of that size come at 44 GB/s out of L2, two CTAs' at 87).
 //
-// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens, join included:
-//   one row of 4,608 tokens       10 us  latency: split, page and key loads, one tile, second product and states, join
-//   16 rows of 16K to 32K        129 us  805 MB, 6.2 TB/s: HBM
-//   8 x 4 rows behind 6K to 8K    35 us  116 MB in copies of 2 KB (pages of 24 tokens): their rate, start and join
-//   one row of 512 picks        11.3 us  latency, as the short row
-//   16 rows of 512 picks          31 us  134 MB in copies of 2 KB out of HBM, 4.3 TB/s
-//   2,048 rows of 512 picks    1,310 us  17.2 GB of copies of 2 KB out of L2, 13.1 TB/s of the 13.7 that L2 gives copies of any size
+// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens (by graph replay, join included):
+//   one row of 4,608 tokens      9.2 us  latency: split, page and key loads, one tile, second product and states, join
+//   16 rows of 16K to 32K        120 to 124 us  805 MB, 6.5 to 6.7 TB/s: HBM
+//   8 x 4 rows behind 6K to 8K    31 us  117 MB in copies of 2 KB (pages of 24 tokens), 1.5 us a tile at their rate, start and join
+//   one row of 512 picks         9.6 us  latency, as the short row
+//   16 rows of 512 picks          29 us  135 MB in copies of 2 KB out of HBM, 4.6 TB/s
+//   2,048 rows of 512 picks    1,298 us  17.2 GB of copies of 2 KB out of L2, 13.2 TB/s of the 13.7 that L2 gives copies of any size
 #include "paged_items.cuh"
 
 namespace step5 {

@@ -18,8 +18,20 @@
 // is not finite, and note the tokens it was found at; the rows that see one of those tokens take it up again at
 // their end, from the page itself.
 //
-// Work.  As over the e4m3 pages: the tiles of all (block of rows, group) items are laid end to end, each CTA takes an equal
-// run, and a second kernel joins the items that CTAs share.
+// Work.  An item is a (block of rows, group).  Where whole items share out evenly enough they go to a CTA whole; otherwise, as over
+// the e4m3 pages, the tiles of all items are laid end to end, each CTA takes an equal run, and a second kernel joins the items
+// that CTAs share.
+//
+// What it takes, with 4 KV groups of 8 heads and pages of 64 tokens (by graph replay, join included):
+//   2,048 rows behind 2,048 tokens        94 us  1.03e11 flop, 1.09 PFLOP/s (57 % of measured cuBLAS)
+//   2,048 rows behind 65,536 tokens    1,471 us  2.23e12 flop, 1.52 PFLOP/s (79 %); called on end 1,650 us, 1.35 PFLOP/s: the clock
+//   2,048 rows, window of 512 tokens      38 us  1.7e10 flop (9 us)
+//   3 prompts of 701, 2 groups of 16      41 us  1.2e10 flop (6 us)
+// A tile of keys takes its two row tiles 3,600 cycles, of which the tensor core works 2,056: each row tile's chain is 2,000 of softmax
+// (300 to fetch S, 250 maximum, 320 the pair's barrier, 850 weights at 4 cycles an exponential and scheduler, 250 to hand P over)
+// and 1,600 of its two products with the hand-overs, and two chains are all that tensor memory holds.  Around the tiles: start
+// 8 us (sharing out 4.5, first rows, pages, q and K 3.5); about two tiles' time for each item (its first maximum, the check of its
+// edges, the turn of the products, the epilogue).
 #include <type_traits>
 
 #include "paged_blocks.cuh"

@@ -4,11 +4,14 @@
 //   want_b = ceil((length_b + new_b) / page_tokens);  pages held_b -> want_b;  rows start_b .. start_b + new_b - 1
 //
 // All of it follows from three running sums over the sequences (new tokens, pages given back, pages needed), which
-// each block takes for itself; what is then written (rows, pages onto the stack, pages off it) is laid out flat over
-// all threads, an item finding its sequence by bisection of the sums in shared memory, so that one long sequence
-// and thousands of short ones spread alike.  One thread-block cluster: its barrier stands between the reads of
-// what is changed in place (held, the stack, the lengths where `ends` is the same buffer) and the writes, and again
-// between the pages put onto the stack and those taken off it.
+// each block takes for itself, a run of sequences a thread; what is then written (rows, pages onto the stack, pages off
+// it) is laid out flat over all threads, an item finding its sequence by bisection of the sums in shared memory, so that
+// one long sequence and thousands of short ones spread alike.  One thread-block cluster (of one block where there is
+// little): its barrier stands between the reads of what is changed in place (held, the stack, the lengths where `ends` is
+// the same buffer) and the writes, and again between the pages put onto the stack and those taken off it.
+//
+// What it takes: 64 sequences of a token each 5.1 us, 1,024 sequences and 65,536 rows 8.9 us (by graph replay; 0.6 MB: all of it
+// latency, five block barriers and two of the cluster, where a kernel that does nothing takes 2).
 #include "paged.cuh"
 
 namespace step5 {
