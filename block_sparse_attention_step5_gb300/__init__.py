@@ -861,8 +861,13 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
     picks and no output, and the scoring, which knows no padding, sets DEV_RANGE for them.)"""
     rows = t
     if plan is not None:
+        table, p = plan[:2]
+        # (refused before any page moves)
+        if p.N != t["q"].shape[0]:
+            raise ValueError(f"the plan has {p.N} rows, q {t['q'].shape[0]}")
+        if cache.block_table is None or table._args[0] != cache.block_table.data_ptr() or bytes(table._shape) != bytes(cache._shape):
+            raise ValueError("the plan's table must be the cache's")
         step5_paged_plan(*plan, stream=stream, geom=geom)
-        p = plan[1]
         rows = {"row_seq": p.row_seq, "row_pos": p.row_pos, "sum_begin": p.region_begin, "sum_end": p.region_end}
     append = step5_kv_append_e4m3 if cache.e4m3 else step5_kv_append
     append(geom, k, v, cache, rows["row_seq"], rows["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)

@@ -99,3 +99,26 @@ def test_handles_check_what_is_assigned(s5):  # noqa: F811
     lengths = i32(3)
     rows.ends = lengths
     assert rows.ends is lengths and rows.B == 3 and rows.N == 10
+
+
+def test_a_step_whose_plan_does_not_fit_moves_nothing(s5, monkeypatch):  # noqa: F811
+    """Other rows than q's, another table than the cache's, or other pages: refused before the plan runs."""
+    ran = []
+    monkeypatch.setattr(s5, "step5_paged_plan", lambda *a, **kw: ran.append(1))
+    geom = s5.STEP5_GEOMETRY
+    table = s5.PagedTable.create(6, 64, 2, 1, device="cpu")
+    row = torch.zeros(1, dtype=torch.int32)
+
+    def step(N, cache):
+        t = {"q": torch.zeros((2, 32, 128), dtype=torch.bfloat16)}
+        rows = s5.PagedRows.create(1, N, device="cpu")
+        s5.decode_step_paged(geom, t, cache, *[None] * 8, max_regions_per_seq=16, plan=(table, rows, row, row))
+
+    create = lambda pages, tokens, of: s5.PagedCache.create(geom, pages, tokens, of, e4m3=False, device="cpu")
+    with pytest.raises(ValueError, match="rows"):
+        step(3, create(6, 64, table.block_table))
+    own = s5.PagedCache(*(torch.zeros((6, 4, 64, 128), dtype=torch.bfloat16) for _ in range(2)))
+    for cache in (create(6, 64, table.block_table.clone()), create(7, 64, table.block_table), create(6, 32, table.block_table), own):
+        with pytest.raises(ValueError, match="table"):
+            step(2, cache)
+    assert not ran
