@@ -2,6 +2,8 @@
 // a group, in tiles), their split over the CTAs, and the join of the items that CTAs share.
 #pragma once
 
+#include <type_traits>
+
 #include "paged_device.cuh"
 
 namespace step5 {
@@ -169,7 +171,7 @@ __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREA
     if (few) {
         // Few items: each is cut into equal parts, one CTA a part, of at most L tiles for the
         // smallest L of 32 tried that needs no more CTAs than there are (2 L0 always does).  No CTA
-        // then has parts of two items. (fewer than 2^8 items of at most 2^24 tiles)
+        // then has parts of two items. (fewer than 2^8 items of at most 2^24 tiles a row)
         Item own{};
         if (tid < items) own = item_of<PICKS, R>(p, tid);
         const uint32_t mine = (uint32_t)own.tiles;
@@ -178,10 +180,10 @@ __device__ __forceinline__ bool take_run(const PagedAttnParams& p, RunSmem<THREA
         if (lane == 0) s.scan[warp] = sum;
         if (tid == 0) s.run = 0;
         __syncthreads();
-        uint32_t total = 0;
+        std::conditional_t<R == 1, uint32_t, uint64_t> total = 0;
 #pragma unroll
         for (int w = 0; w < THREADS / 32; ++w) total += (uint32_t)s.scan[w];
-        const uint32_t least = max(1u, total / gridDim.x + (total % gridDim.x ? 1u : 0u));
+        const uint32_t least = max(1u, (uint32_t)(total / gridDim.x) + (total % gridDim.x ? 1u : 0u));
         uint32_t most = least + (least * (uint32_t)lane + 30u) / 31u;  // this lane's L
         uint32_t ctas = 0;
         for (int i = warp; i < items; i += THREADS / 32) ctas += ((uint32_t)s.tiles[i] + most - 1u) / most;

@@ -457,6 +457,31 @@ def test_pools_past_32_bit_offsets(s5, runs, picks):  # noqa: F811
     c.near(got.cpu(), *want)
 
 
+@pytest.mark.parametrize("N, hq, window", [(1, 8, 0), (1, 4, 700), (2, 16, 5000), (4, 4, 0), (4, 8, 5000), (40, 4, 0), (40, 8, 700), (40, 16, 133)])
+def test_the_last_positions_of_all(s5, N, hq, window):  # noqa: F811
+    """Rows at the end of a table of 2^31 - 32 tokens.  All its entries but the last name one page, whose
+    keys' scores lie so far below the last page's that their weights are zero."""
+    gen = torch.Generator().manual_seed(N + hq)
+    pt, length = 65528, 32772
+    cap = pt * length
+    assert cap == 2 ** 31 - 32
+    geom = geometry(s5, 1, hq)
+    k, v = (normal(gen, 2, 1, pt, 128) for _ in "kv")
+    q = normal(gen, N, hq, 128)
+    q[..., 0] = 8.0
+    k[0, ..., 0], k[1, ..., 0] = -400.0, 0.0
+    table = torch.zeros((1, length), dtype=torch.int32)
+    table[0, -1] = 1
+    seq, pos = torch.zeros(N, dtype=torch.int32), torch.arange(cap - N, cap).int()
+    out = torch.full((N, hq, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    kg, vg, tg, qg, sg, pg = dev(k, v, table, q, seq, pos)
+    s5.step5_paged_attn(geom, qg, s5.PagedCache(kg, vg, tg), sg, pg, out, s5.PagedWorkspace.create(geom), window=window)
+    assert status(s5) == 0
+    first = cap - pt
+    want, mass = B16.attend(q, k[1:], v[1:], torch.zeros((1, 1), dtype=torch.int32), seq, (pos - first).int(), geom.softmax_scale, window)
+    assert B16.off(out, want, mass, B16.shares(N, hq, 1)) <= 1.0
+
+
 def test_contiguous_caches_as_pages(s5):  # noqa: F811
     """A cache without a table, a page a sequence, against step5_sparse_attn over the same picks."""
     c = Case(s5, [(0, 900, 1), (1, 77, 1)], G=4, pt=1024, seed=5, top_k=64).pick()
