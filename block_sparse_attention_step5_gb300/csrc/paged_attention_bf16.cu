@@ -22,9 +22,9 @@
 // CTA an SM with 5 or 6 half tiles in shared memory, or two with 3, keep HBM busy; picks, whose copies are 2 KB each, want two CTAs
 // (a CTA's copies of that size come at 44 GB/s out of L2, two CTAs' at 87).
 //
-// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens (by graph replay, join included):
+// What bounds it, with 4 KV groups of 8 heads and pages of 64 tokens (by graph replay or call after call, join included):
 //   one row of 4,608 tokens      9.2 us  latency: split, page and key loads, one tile, second product and states, join
-//   16 rows of 16K to 32K        120 to 124 us  805 MB, 6.5 to 6.7 TB/s: HBM
+//   16 rows of 16K to 32K        120 to 135 us (by lengths and GPU)  806 MB, 6.0 to 6.7 TB/s: HBM
 //   8 x 4 rows behind 6K to 8K    31 us  117 MB in copies of 2 KB (pages of 24 tokens), 1.5 us a tile at their rate, start and join
 //   one row of 512 picks         9.6 us  latency, as the short row
 //   16 rows of 512 picks          29 us  135 MB in copies of 2 KB out of HBM, 4.6 TB/s

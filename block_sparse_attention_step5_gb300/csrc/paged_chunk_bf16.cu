@@ -27,11 +27,11 @@
 //   2,048 rows behind 65,536 tokens    1,471 us  2.23e12 flop, 1.52 PFLOP/s (79 %); called on end 1,650 us, 1.35 PFLOP/s: the clock
 //   2,048 rows, window of 512 tokens      38 us  1.7e10 flop (9 us)
 //   3 prompts of 701, 2 groups of 16      41 us  1.2e10 flop (6 us)
-// A tile of keys takes its two row tiles 3,600 cycles, of which the tensor core works 2,056: each row tile's chain is 2,000 of softmax
-// (300 to fetch S, 250 maximum, 320 the pair's barrier, 850 weights at 4 cycles an exponential and scheduler, 250 to hand P over)
-// and 1,600 of its two products with the hand-overs, and two chains are all that tensor memory holds.  Around the tiles: start
-// 8 us (sharing out 4.5, first rows, pages, q and K 3.5); about two tiles' time for each item (its first maximum, the check of its
-// edges, the turn of the products, the epilogue).
+// A tile of keys takes its two row tiles at most 3,500 cycles (65,536 tokens: 875 tiles a CTA), of which the tensor core works 2,056.
+// By clock stamps in the kernel, which stretch a tile to 4,000, each row tile's chain is half softmax (330 to fetch S, 220 maximum,
+// 330 the pair's barrier, 850 weights, 240 to hand P over) and half its two products and their turn; two chains are all that tensor
+// memory holds.  Around the tiles: start 8 us (sharing out 4.5, first rows, pages, q, K and product 3.5); about two tiles' time for
+// each item (its first maximum, the check of its edges, the turn of the products, the epilogue).
 #include <type_traits>
 
 #include "paged_blocks.cuh"
@@ -53,7 +53,7 @@ constexpr uint32_t kIdescPv = tc::instr_desc(tc::kFmtBF16, false, true, 128, 128
 constexpr float kSlack = 8.0f;                  // log2 units a weight may lie above the running maximum
 
 // Tiles that the busiest CTA may have over an equal share before items are cut: what a cut costs, a partial state and its join
-// for most CTAs (window of 512: 53 us cut, 44 whole; three prompts of 701 rows 56.7 and 52.1).
+// for most CTAs (window of 512: 53 us cut, 44 whole; three prompts of 701 rows 56.7 and 52.1; 2,048 rows on 2K, dealt out, 112 and 97).
 constexpr int kWholeTiles = 8;
 constexpr int kItemTiles = 2;  // what an item takes beside its tiles: q, the turn of the products, the epilogue
 
