@@ -14,8 +14,8 @@
 // the tensor core has the other's two products (1,024 cycles for 128 rows against 128 keys).
 //
 // Unseen values.  A weight of zero must meet a finite value, but a page may hold anything where a row does not look.
-// Where some row of the block does not see some key of the tile (its edges), two warps look the tile of V over, clear what
-// is not finite, and note the tokens it was found at; the rows that see one of those tokens take it up again at
+// Where some row of the block does not see some key of the tile (its edges, bad pages), two warps look the tile of V over, clear
+// what is not finite, and note the tokens it was found at; the rows that see one of those tokens take it up again at
 // their end, from the page itself.
 //
 // Work.  An item is a (block of rows, group).  Where whole items share out evenly enough they go to a CTA whole; otherwise, as over
@@ -427,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int r = half * 8; r < half * 8 + 8; ++r) {
                     const int tok = tl.t0 + r * 8;
-                    if (tok >= tl.all_lo && tok + 7 <= tl.all_hi) continue;
+                    // (a region that was not copied, on a bad page, has what lay there before)
+                    if ((tl.ok >> r & 1u) && tok >= tl.all_lo && tok + 7 <= tl.all_hi) continue;
                     uint4* v = reinterpret_cast<uint4*>(vs + st * kTileBytes + r * kRegionBytes);
                     uint4 x[4];
 #pragma unroll

@@ -596,3 +596,23 @@ def test_run_together(s5):  # noqa: F811
     s5.step5_index_score_topk(geom, t["idx_q"], t["w"], t["row_seq"], t["row_pos"], t["cos"], t["sin"], t["summaries"], ids2,
                               cnt2, ws.tensor, t_cap=t["idx_k"].shape[2])
     assert torch.equal(ids, ids2) and torch.equal(cnt, cnt2)
+
+
+# ------------------------------------------------------------------------------ what one row's values leave behind
+
+def test_bad_pages_behind_values_that_are_not_finite(s5):  # noqa: F811
+    """Blocks of two sequences in turn, so that each CTA takes some of either: one's values are all NaN, the other's first
+    pages are bad.  What the first leaves in shared memory does not reach the second, whose rows all see those pages."""
+    for bad in (NAN, INF):
+        c = Case(s5, [(b, 255, 32) for _ in range(160) for b in range(2)], G=1, hq=8, pt=16, seed=11)
+        assert c.shared
+        c.v[c.table[0].long()] = bad
+        c.table[1, 1:3], c.table[1, 9] = -1, 10 ** 6
+        got = c.run().cpu()
+        assert status(s5) == 1
+        hit = got[c.seq == 0].float()
+        assert bool(torch.isnan(hit).all() if bad != bad else (hit == bad).all())
+        assert bool(torch.isfinite(got[c.seq == 1]).all())
+        some = torch.nonzero(c.seq == 1)[::97, 0]
+        want = B16.attend(c.q[some], c.k, c.v, c.table, c.seq[some], c.pos[some], c.geom.softmax_scale, bad_pages=(-1, 10 ** 6))
+        assert B16.off(got[some], *want, True) <= 1.0
