@@ -616,3 +616,75 @@ def test_bad_pages_behind_values_that_are_not_finite(s5):  # noqa: F811
         some = torch.nonzero(c.seq == 1)[::97, 0]
         want = B16.attend(c.q[some], c.k, c.v, c.table, c.seq[some], c.pos[some], c.geom.softmax_scale, bad_pages=(-1, 10 ** 6))
         assert B16.off(got[some], *want, True) <= 1.0
+
+
+def milliseconds(fn):
+    """The least of five calls."""
+    times = []
+    for _ in range(6):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        fn()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b))
+    return min(times[1:])
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("block, window", [([(0, 73, 12), (1, 16000, 4)], 0), ([(0, 16001, 16)], 8000)])
+def test_values_that_no_row_sees_take_no_time(s5, block, window, bad):  # noqa: F811
+    """Blocks with rows of two sequences, and windows, enough of them for whole items: what lies behind the last tokens and
+    before the windows is not finite.  It changes no bit and costs about nothing (the tiles that it is cleared from)."""
+    c = Case(s5, block * 304, G=1, hq=16, pt=64, seed=12)
+    assert c.shared
+    clean, cache, q = c.run(window), c.cache(), c.q_on_gpu()
+    out, (seq, pos) = torch.zeros_like(clean), dev(c.seq, c.pos)
+    call = lambda: s5.step5_paged_attn(c.geom, q, cache, seq, pos, out, c.ws, window=window)
+    before = milliseconds(call)
+    c.seq, c.pos = c.seq[:16], c.pos[:16]  # (the others see the same)
+    cache.v.masked_fill_(c.unseen(window)[:, None, :, None].cuda(), bad)
+    after = milliseconds(call)
+    assert torch.equal(out, clean) and status(s5) == 0
+    assert after <= 1.5 * before + 0.1, (before, after)
+
+
+def test_values_that_are_seen_far_apart(s5):  # noqa: F811
+    """As above, blocks with rows of two sequences: what is not finite at the first tokens and at the last reaches the rows that
+    see it, in its dimension, and nothing else changes a bit; the call takes no search of all that lies between."""
+    c = Case(s5, [(0, 73, 12), (1, 16000, 4)] * 304, G=1, hq=16, pt=64, seed=13)
+    clean, cache, q = c.run(), c.cache(), c.q_on_gpu()
+    out, (seq, pos) = torch.zeros_like(clean), dev(c.seq, c.pos)
+    call = lambda: s5.step5_paged_attn(c.geom, q, cache, seq, pos, out, c.ws)
+    before = milliseconds(call)
+    want = clean.clone()
+    for b, tok, d, x in ((0, 3, 5, NAN), (0, 80, 6, INF), (1, 2, 7, -INF), (1, 16000, 9, INF), (1, 16001, 20, -INF),
+                         (1, 16002, 30, INF), (1, 9000, 30, -INF)):
+        page, slot = R.place(c.table, b, tok, c.pt)
+        cache.v[page, 0, slot, d] = x
+        hit = ((seq == b) & (pos >= tok))[:, None] & (torch.arange(128, device="cuda") == d)
+        hit = hit[:, None, :].expand(want.shape)
+        want[hit] = x if d != 30 or tok == 16002 else torch.where(want[hit] == INF, NAN, x).bfloat16()
+    after = milliseconds(call)
+    assert status(s5) == 0
+    assert torch.equal(out.nan_to_num(-1e30, 2e30, -2e30), want.nan_to_num(-1e30, 2e30, -2e30))
+    assert after <= 4 * before + 0.1, (before, after)
+
+
+@pytest.mark.parametrize("bad", [NAN, -INF])
+@pytest.mark.parametrize("dims", [slice(0, 128), slice(70, 71)])
+def test_values_that_are_not_finite_throughout(s5, dims, bad):  # noqa: F811
+    """The same where a sequence has them at every token, in every dimension or in one."""
+    c = Case(s5, [(0, 73, 12), (1, 16000, 4)] * 304, G=1, hq=16, pt=64, seed=13)
+    clean, cache, q = c.run(), c.cache(), c.q_on_gpu()
+    out, (seq, pos) = torch.zeros_like(clean), dev(c.seq, c.pos)
+    call = lambda: s5.step5_paged_attn(c.geom, q, cache, seq, pos, out, c.ws)
+    before = milliseconds(call)
+    cache.v[c.table[1].long().cuda(), :, :, dims] = bad
+    after = milliseconds(call)
+    assert status(s5) == 0
+    hit = out[seq == 1][:, :, dims].float()
+    assert bool(torch.isnan(hit).all() if bad != bad else (hit == bad).all())
+    out[:, :, dims] = torch.where((seq == 1)[:, None, None], clean[:, :, dims], out[:, :, dims])
+    assert torch.equal(out, clean)
+    assert after <= 20 * before + 0.1, (before, after)
