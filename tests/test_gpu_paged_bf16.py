@@ -688,3 +688,25 @@ def test_values_that_are_not_finite_throughout(s5, dims, bad):  # noqa: F811
     out[:, :, dims] = torch.where((seq == 1)[:, None, None], clean[:, :, dims], out[:, :, dims])
     assert torch.equal(out, clean)
     assert after <= 20 * before + 0.1, (before, after)
+
+
+def test_values_that_two_drafts_see_far_apart(s5):  # noqa: F811
+    """Rows of two sequences that read their keys together, 304 such items: values that are not finite at the first tokens and at
+    the last reach the rows that see them, and the call takes no search of all that lies between."""
+    c = Case(s5, [(0, 16000, 1), (1, 15998, 1)], G=1, hq=8, pt=64, seed=14)
+    c.table = c.table.repeat(304, 1)
+    c.B, c.N, c.seq, c.pos = 608, 1216, torch.arange(608).int().repeat_interleave(2).view(304, 2, 2).transpose(1, 2).reshape(-1).contiguous(), c.pos.repeat(608)
+    c.q = normal(c.gen, c.N, 8, 128)
+    clean, cache, q = c.run(), c.cache(), c.q_on_gpu()
+    out, (seq, pos) = torch.zeros_like(clean), dev(c.seq, c.pos)
+    call = lambda: s5.step5_paged_attn(c.geom, q, cache, seq, pos, out, c.ws)
+    before = milliseconds(call)
+    want = clean.clone()
+    for b, tok, d, x in ((0, 3, 5, NAN), (0, 15999, 6, INF), (1, 2, 7, -INF), (1, 15998, 9, INF)):
+        page, slot = R.place(c.table, b, tok, c.pt)
+        cache.v[page, 0, slot, d] = x
+        want[(seq % 2 == b), :, d] = x
+    after = milliseconds(call)
+    assert status(s5) == 0
+    assert torch.equal(out.nan_to_num(-1e30, 2e30, -2e30), want.nan_to_num(-1e30, 2e30, -2e30))
+    assert after <= 1.5 * before + 0.1, (before, after)
