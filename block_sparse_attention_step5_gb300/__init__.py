@@ -865,8 +865,9 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
         # (refused before any page moves)
         if p.N != t["q"].shape[0]:
             raise ValueError(f"the plan has {p.N} rows, q {t['q'].shape[0]}")
-        if cache.block_table is None or table._args[0] != cache.block_table.data_ptr() or bytes(table._shape) != bytes(cache._shape):
-            raise ValueError("the plan's table must be the cache's")
+        if (cache.block_table is None or table._args[0] != cache.block_table.data_ptr() or table.B != cache.B
+                or bytes(table._shape) != bytes(cache._shape)):
+            raise ValueError("the plan's table must be the cache's, all its sequences")
         step5_paged_plan(*plan, stream=stream, geom=geom)
         rows = {"row_seq": p.row_seq, "row_pos": p.row_pos, "sum_begin": p.region_begin, "sum_end": p.region_end}
     append = step5_kv_append_e4m3 if cache.e4m3 else step5_kv_append

@@ -122,3 +122,17 @@ def test_a_step_whose_plan_does_not_fit_moves_nothing(s5, monkeypatch):  # noqa:
         with pytest.raises(ValueError, match="table"):
             step(2, cache)
     assert not ran
+
+
+def test_a_plan_of_other_sequences_than_the_caches_moves_nothing(s5, monkeypatch):  # noqa: F811
+    """A cache over the first rows of the plan's table has its address and its length, and fewer sequences: refused."""
+    ran = []
+    monkeypatch.setattr(s5, "step5_paged_plan", lambda *a, **kw: ran.append(1))
+    geom = s5.STEP5_GEOMETRY
+    table = s5.PagedTable.create(6, 64, 2, 3, device="cpu")
+    rows = s5.PagedRows.create(3, 2, device="cpu")
+    cache = s5.PagedCache.create(geom, 6, 64, table.block_table[:2], e4m3=False, device="cpu")
+    t = {"q": torch.zeros((2, 32, 128), dtype=torch.bfloat16)}
+    with pytest.raises(ValueError, match="table"):
+        s5.decode_step_paged(geom, t, cache, *[None] * 8, max_regions_per_seq=16, plan=(table, rows, *[torch.zeros(3).int()] * 2))
+    assert not ran
