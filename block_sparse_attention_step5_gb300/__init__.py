@@ -850,6 +850,20 @@ def step5_paged_plan(table: PagedTable, rows: PagedRows, lengths, new_tokens, st
         raise Step5Error("step5_paged_plan", st)
 
 
+def _check_indexers(g, t: dict, rows: dict):
+    """That the indexer's tensors have the step's rows and sequences: the calls take these from different ones of them."""
+    N, B, G, D = t["q"].shape[0], rows["sum_begin"].shape[0], g.num_kv_groups, g.idx_dim
+    length = lambda name: t[name].shape[2] if isinstance(t[name], torch.Tensor) and t[name].dim() == 4 else -1
+    t_cap, r_cap = length("idx_k"), length("summaries")
+    bf16 = torch.bfloat16
+    for name, dtype, want in (("sum_end", torch.int32, (B,)), ("idx_k", bf16, (B, G, t_cap, D)), ("idx_z", bf16, (B, G, t_cap, D)),
+                              ("summaries", torch.uint8, (B, G, r_cap, D)), ("idx_q", bf16, (N, g.idx_heads, D)),
+                              ("w", torch.float32, (N, g.idx_heads))):
+        x = (rows if name == "sum_end" else t)[name]
+        if not isinstance(x, torch.Tensor) or x.dtype != dtype or tuple(x.shape) != want:
+            raise ValueError(f"{name} must be {dtype} {want}, of the step's {N} rows and {B} sequences")
+
+
 def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws: PagedWorkspace, k, v, sel_ids,
                       sel_count, q_rot, out, max_regions_per_seq, cos=None, sin=None, gate=None, stream=None,
                       plan=None):
@@ -868,8 +882,10 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
         if (cache.block_table is None or table._args[0] != cache.block_table.data_ptr() or table.B != cache.B
                 or bytes(table._shape) != bytes(cache._shape)):
             raise ValueError("the plan's table must be the cache's, all its sequences")
-        step5_paged_plan(*plan, stream=stream, geom=geom)
         rows = {"row_seq": p.row_seq, "row_pos": p.row_pos, "sum_begin": p.region_begin, "sum_end": p.region_end}
+    _check_indexers(Geometry.of(geom), t, rows)
+    if plan is not None:
+        step5_paged_plan(*plan, stream=stream, geom=geom)
     append = step5_kv_append_e4m3 if cache.e4m3 else step5_kv_append
     append(geom, k, v, cache, rows["row_seq"], rows["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)
     step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], rows["sum_begin"], rows["sum_end"],

@@ -136,3 +136,29 @@ def test_a_plan_of_other_sequences_than_the_caches_moves_nothing(s5, monkeypatch
     with pytest.raises(ValueError, match="table"):
         s5.decode_step_paged(geom, t, cache, *[None] * 8, max_regions_per_seq=16, plan=(table, rows, *[torch.zeros(3).int()] * 2))
     assert not ran
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("name, shape", [("idx_q", (3, 16, 64)), ("w", (1, 16)), ("idx_k", (3, 4, 128, 64)), ("idx_z", (2, 4, 64, 64)),
+                                         ("summaries", (1, 4, 16, 64)), ("summaries", (2, 4, 16)), ("idx_k", None), ("sum_end", (1,)), ("w", "bf16")])
+def test_a_step_of_other_rows_or_sequences_than_its_indexers_is_refused(s5, monkeypatch, planned, name, shape):  # noqa: F811
+    """The scoring takes its rows from idx_q, the summaries their sequences from idx_k: more of them than there are rows and
+    regions to summarise would be read past their ends."""
+    ran = []
+    monkeypatch.setattr(s5, "step5_paged_plan", lambda *a, **kw: ran.append("plan"))
+    monkeypatch.setattr(s5, "step5_kv_append", lambda *a, **kw: ran.append("append"))
+    geom = s5.STEP5_GEOMETRY
+    table = s5.PagedTable.create(6, 64, 2, 2, device="cpu")
+    cache = s5.PagedCache.create(geom, 6, 64, table.block_table, e4m3=False, device="cpu")
+    bf16 = lambda *of: torch.zeros(of, dtype=torch.bfloat16)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    t = {"q": bf16(2, 32, 128), "idx_q": bf16(2, 16, 64), "w": torch.zeros(2, 16), "idx_k": bf16(2, 4, 128, 64), "idx_z": bf16(2, 4, 128, 64),
+         "summaries": torch.zeros((2, 4, 16, 64), dtype=torch.uint8), "cos": bf16(128, 16), "sin": bf16(128, 16),
+         "row_seq": i32(2), "row_pos": i32(2), "sum_begin": i32(2), "sum_end": i32(2)}
+    t[name] = None if shape is None else t[name].bfloat16() if shape == "bf16" else torch.zeros(shape, dtype=t[name].dtype)
+    if planned and name == "sum_end":
+        return  # (the plan's own)
+    plan = (table, s5.PagedRows.create(2, 2, device="cpu"), i32(2), i32(2)) if planned else None
+    with pytest.raises(ValueError, match=name):
+        s5.decode_step_paged(geom, t, cache, None, None, bf16(2, 4, 128), bf16(2, 4, 128), *[None] * 4, max_regions_per_seq=16, plan=plan)
+    assert not ran
