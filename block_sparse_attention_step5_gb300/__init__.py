@@ -40,7 +40,7 @@ __all__ = [
     "step5_merge_attend_shard",
     "RowsLayout", "step5_rows_layout_for", "HostRows", "step5_decode_step_host", "step5_set_host_copies",
     "step5_workspace_bytes", "step5_workspace_init", "step5_device_status",
-    "step5_set_select_path", "step5_set_wait_polls", "step5_set_attention_path", "step5_select_path_for", "step5_set_prologue_overlap", "step5_decode_step", "step5_status_string", "step5_convert_bf16_to_e4m3",
+    "step5_set_select_path", "step5_set_wait_polls", "step5_set_attention_path", "step5_select_path_for", "step5_set_prologue_overlap", "step5_set_check_only", "step5_decode_step", "step5_status_string", "step5_convert_bf16_to_e4m3",
     "Workspace", "decode_step",
     "Pages", "PagedCache", "PagedWorkspace", "step5_kv_append", "step5_kv_append_e4m3", "step5_paged_attn_e4m3",
     "step5_sparse_attn_e4m3", "step5_paged_workspace_bytes", "decode_step_paged",
@@ -139,6 +139,7 @@ def load():
         "step5_set_attention_path": (i32, [i32]),
         "step5_set_prologue_overlap": (i32, [i32]),
         "step5_set_host_copies": (i32, [i32]),
+        "step5_set_check_only": (i32, [i32]),
         "step5_select_path_for": (i32, [G, i32, i32, i32]),
         "step5_status_string": (ctypes.c_char_p, [i32]),
         "step5_convert_bf16_to_e4m3": (i32, [P, P, i64, P]),
@@ -171,6 +172,10 @@ def _check(fn: str, status: int):
         raise Step5Error(fn, status)
 
 
+def _run(fn: str, *args):
+    _check(fn, getattr(load(), fn)(*args))
+
+
 def step5_status_string(status: int) -> str:
     return load().step5_status_string(status).decode()
 
@@ -197,6 +202,12 @@ def step5_set_prologue_overlap(enable: int) -> int:
     """1 = the scoring kernel reads its non-summary inputs before waiting for the launch
     before it (which must not write them); 0 = every read waits.  Returns the previous."""
     return load().step5_set_prologue_overlap(enable)
+
+
+def step5_set_check_only(enable: int) -> int:
+    """1: this thread's calls of a paged step (see the header) only check their arguments; 0 (default): they
+    run.  Returns the previous value."""
+    return load().step5_set_check_only(int(enable))
 
 
 def step5_set_host_copies(always: int) -> int:
@@ -239,28 +250,37 @@ def step5_region_summarize(geom, idx_k, idx_z, cos, sin, region_begin, region_en
                            summaries, summaries_f32=None, max_regions_per_seq=None, stream=None):
     """idx_k/idx_z [B][G][t_cap][64] bf16, cos/sin [t_cap][rope/2] bf16 (or None),
     region_begin/end [B] int32, summaries [B][G][r_cap][64] uint8 (written)."""
+    _run(*_summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summaries, summaries_f32,
+                          max_regions_per_seq, stream))
+
+
+def _summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summaries, summaries_f32, max_regions_per_seq,
+                    stream):
     B, G, t_cap, _ = idx_k.shape
     r_cap = summaries.shape[2]
     if max_regions_per_seq is None:
         max_regions_per_seq = r_cap
-    _check("step5_region_summarize", load().step5_region_summarize(
-        ctypes.byref(Geometry.of(geom)), B, t_cap, r_cap, int(max_regions_per_seq),
-        _ptr(idx_k), _ptr(idx_z), _ptr(cos), _ptr(sin), _ptr(region_begin), _ptr(region_end),
-        _ptr(summaries), _ptr(summaries_f32), _stream(stream)))
+    return ("step5_region_summarize", ctypes.byref(Geometry.of(geom)), B, t_cap, r_cap, int(max_regions_per_seq), _ptr(idx_k),
+            _ptr(idx_z), _ptr(cos), _ptr(sin), _ptr(region_begin), _ptr(region_end), _ptr(summaries), _ptr(summaries_f32),
+            _stream(stream))
 
 
 def step5_index_score_topk(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids,
                            sel_count, workspace, t_cap, scores=None, sel_scores=None, stream=None):
     """idx_q [N][idx_heads][64] bf16, w [N][idx_heads] fp32, row_seq/row_pos [N] int32,
     summaries [B][G][r_cap][64] uint8; writes sel_ids [N][G][top_k], sel_count [N][G]."""
+    _run(*_score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, sel_count, workspace, t_cap, scores,
+                      sel_scores, stream))
+
+
+def _score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, sel_count, workspace, t_cap, scores, sel_scores,
+                stream):
     N = idx_q.shape[0]
     B, _, r_cap, _ = summaries.shape
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check("step5_index_score_topk", load().step5_index_score_topk(
-        ctypes.byref(Geometry.of(geom)), N, B, int(t_cap), r_cap, _ptr(idx_q), _ptr(w),
-        _ptr(row_seq), _ptr(row_pos), _ptr(cos), _ptr(sin), _ptr(summaries), _ptr(sel_ids),
-        _ptr(sel_count), _ptr(scores), _ptr(sel_scores), _ptr(workspace), ws_bytes,
-        _stream(stream)))
+    return ("step5_index_score_topk", ctypes.byref(Geometry.of(geom)), N, B, int(t_cap), r_cap, _ptr(idx_q), _ptr(w),
+            _ptr(row_seq), _ptr(row_pos), _ptr(cos), _ptr(sin), _ptr(summaries), _ptr(sel_ids), _ptr(sel_count), _ptr(scores),
+            _ptr(sel_scores), _ptr(workspace), ws_bytes, _stream(stream))
 
 
 def step5_index_score_topk_noalloc(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids,
@@ -647,7 +667,7 @@ def _device_and_stream(cache: "PagedCache", geom, stream):
     return dev, (_raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _kv_append(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, row_pos, cos, sin, q, q_out, stream):
+def _append_call(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, row_pos, cos, sin, q, q_out, stream):
     g = Geometry.of(geom)
     dev, st = _device_and_stream(cache, g, stream)
     if cache.e4m3 != e4m3:
@@ -667,11 +687,9 @@ def _kv_append(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, row_
         sp = _arg("sin", sin, torch.bfloat16, table, dev)
         t_cap, half = table
     rows = (N,)
-    st = getattr(load(), fn)(g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
-                             _arg("row_seq", row_seq, torch.int32, rows, dev),
-                             _arg("row_pos", row_pos, torch.int32, rows, dev), cp, sp, qo, *cache._pools, st)
-    if st:
-        raise Step5Error(fn, st)
+    return (fn, g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
+            _arg("row_seq", row_seq, torch.int32, rows, dev), _arg("row_pos", row_pos, torch.int32, rows, dev), cp, sp, qo,
+            *cache._pools, st)
 
 
 def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
@@ -680,18 +698,18 @@ def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, s
     writes it and v into the bf16 cache at (row_seq, row_pos) [N] int32; with q
     [N][Hq][128], its rotation into q_out.  q, k and v may be slices of one [N][heads][128]
     tensor (rows apart, heads together)."""
-    _kv_append("step5_kv_append", False, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+    _run(*_append_call("step5_kv_append", False, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
 
 
 def step5_kv_append_e4m3(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
                          stream=None):
     """step5_kv_append into an e4m3 cache: codes and the power-of-two scale of each region
     and group.  A sequence's rows stand together at ascending positions (see the header)."""
-    _kv_append("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream)
+    _run(*_append_call("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
 
 
-def _attend_paged(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None,
-                  sel_ids=None, sel_count=None):
+def _attend_call(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None,
+                 sel_ids=None, sel_count=None):
     g = Geometry.of(geom)
     dev, st = _device_and_stream(cache, g, stream)
     if cache.e4m3 != e4m3:
@@ -708,14 +726,10 @@ def _attend_paged(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_
     else:
         before, after = (window,), ()
     rows = (_arg("q", q, torch.bfloat16, shape, dev),) if e4m3 else _rows("q", q, Hq, g.head_dim, dev, N)
-    st = getattr(load(), fn)(g, cache._pages, N, cache.B, *before, *rows, *cache._pools,
-                             _arg("row_seq", row_seq, torch.int32, (N,), dev),
-                             _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
-                             None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
-                             _arg("out", out, torch.bfloat16, shape, dev), None if w is None else w.data_ptr(),
-                             0 if w is None else w.nbytes, st)
-    if st:
-        raise Step5Error(fn, st)
+    return (fn, g, cache._pages, N, cache.B, *before, *rows, *cache._pools, _arg("row_seq", row_seq, torch.int32, (N,), dev),
+            _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
+            None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
+            _arg("out", out, torch.bfloat16, shape, dev), None if w is None else w.data_ptr(), 0 if w is None else w.nbytes, st)
 
 
 def _window(window) -> int:
@@ -727,32 +741,32 @@ def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, wor
     """Causal attention of rows q [N][Hq][128] bf16 at (row_seq, row_pos) over the e4m3
     cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
     sigmoid gate [N][Hq] when given."""
-    _attend_paged("step5_paged_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                  window=_window(window))
+    _run(*_attend_call("step5_paged_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                       window=_window(window)))
 
 
 def step5_paged_attn(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
                      stream=None):
     """step5_paged_attn_e4m3 over the bf16 cache.  q may be a slice of one [N][heads][128]
     tensor (rows apart, heads together)."""
-    _attend_paged("step5_paged_attn", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                  window=_window(window))
+    _run(*_attend_call("step5_paged_attn", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                       window=_window(window)))
 
 
 def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                            gate=None, stream=None):
     """step5_sparse_attn over the e4m3 cache: the picked regions sel_ids [N][G][top_k],
     sel_count [N][G] and the row's own region."""
-    _attend_paged("step5_sparse_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                  sel_ids=sel_ids, sel_count=sel_count)
+    _run(*_attend_call("step5_sparse_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                       sel_ids=sel_ids, sel_count=sel_count))
 
 
 def step5_sparse_attn_paged(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                             gate=None, stream=None):
     """step5_sparse_attn over the bf16 cache's pages, as step5_sparse_attn_e4m3 over the e4m3
     ones.  q as in step5_paged_attn."""
-    _attend_paged("step5_sparse_attn_paged", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                  sel_ids=sel_ids, sel_count=sel_count)
+    _run(*_attend_call("step5_sparse_attn_paged", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                       sel_ids=sel_ids, sel_count=sel_count))
 
 
 class _Int32s:
@@ -871,7 +885,8 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
     t["q"] rotated into q_rot by cos/sin), then summarise, score + select over the indexer
     tensors of ``t`` as decode_step does, and attend over the picked regions of the cache.  With ``plan``,
     (table, rows, lengths, new_tokens) as step5_paged_plan takes them, the step is planned first, and its
-    rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end.  (Rows that it pads have no
+    rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end; no page moves if the plan or a
+    call behind it refuses an argument.  (Rows that it pads have no
     picks and no output, and the scoring, which knows no padding, sets DEV_RANGE for them.)"""
     rows = t
     if plan is not None:
@@ -884,14 +899,23 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
             raise ValueError("the plan's table must be the cache's, all its sequences")
         rows = {"row_seq": p.row_seq, "row_pos": p.row_pos, "sum_begin": p.region_begin, "sum_end": p.region_end}
     _check_indexers(Geometry.of(geom), t, rows)
-    if plan is not None:
+    append, attend = (("step5_kv_append_e4m3", "step5_sparse_attn_e4m3") if cache.e4m3 else
+                      ("step5_kv_append", "step5_sparse_attn_paged"))
+    seq, pos = rows["row_seq"], rows["row_pos"]
+    calls = (_append_call(append, cache.e4m3, geom, k, v, cache, seq, pos, cos, sin, t["q"], q_rot, stream),
+             _summarize_call(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], rows["sum_begin"], rows["sum_end"], t["summaries"],
+                             None, max_regions_per_seq, stream),
+             _score_call(geom, t["idx_q"], t["w"], seq, pos, t["cos"], t["sin"], t["summaries"], sel_ids, sel_count, ws.tensor,
+                         t["idx_k"].shape[2], None, None, stream),
+             _attend_call(attend, cache.e4m3, geom, q_rot, cache, seq, pos, out, paged_ws, gate, stream, sel_ids=sel_ids,
+                          sel_count=sel_count))
+    if plan is not None:  # (the other calls' checks first: 16 us of the host, once a step)
+        prev = step5_set_check_only(1)
+        try:
+            for call in calls:
+                _run(*call)
+        finally:
+            step5_set_check_only(prev)
         step5_paged_plan(*plan, stream=stream, geom=geom)
-    append = step5_kv_append_e4m3 if cache.e4m3 else step5_kv_append
-    append(geom, k, v, cache, rows["row_seq"], rows["row_pos"], cos, sin, q=t["q"], q_out=q_rot, stream=stream)
-    step5_region_summarize(geom, t["idx_k"], t["idx_z"], t["cos"], t["sin"], rows["sum_begin"], rows["sum_end"],
-                           t["summaries"], max_regions_per_seq=max_regions_per_seq, stream=stream)
-    step5_index_score_topk(geom, t["idx_q"], t["w"], rows["row_seq"], rows["row_pos"], t["cos"], t["sin"],
-                           t["summaries"], sel_ids, sel_count, ws.tensor, t_cap=t["idx_k"].shape[2], stream=stream)
-    attend = step5_sparse_attn_e4m3 if cache.e4m3 else step5_sparse_attn_paged
-    attend(geom, q_rot, cache, rows["row_seq"], rows["row_pos"], sel_ids, sel_count, out, paged_ws, gate=gate,
-           stream=stream)
+    for call in calls:
+        _run(*call)

@@ -14,6 +14,7 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 step5_status check_geometry(const step5_geometry* g);
 uint32_t* status_ptr();  // the current device's status word, or null
 int num_sms();           // of the current device
+bool check_only();       // of the calling thread: step5_set_check_only
 PFN_cuTensorMapEncodeTiled_v12000 get_encode();
 
 }  // namespace step5

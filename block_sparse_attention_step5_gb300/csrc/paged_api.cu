@@ -81,6 +81,7 @@ step5_status append_impl(const step5_geometry* geom, const step5_pages* pages, i
     if (!aligned16(q_bf16_or_null) || !aligned16(q_out_bf16_or_null) || !aligned16(k_bf16) || !aligned16(v_bf16) ||
         !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(rope_cos_bf16) || !aligned16(rope_sin_bf16))
         return STEP5_ERR_INVALID_ARGUMENT;
+    if (check_only()) return STEP5_OK;
     uint32_t* st = status_ptr();
     if (!st) return STEP5_ERR_CUDA;
     AppendParams p;
@@ -128,6 +129,7 @@ step5_status attend_params(PagedAttnParams& p, const step5_geometry* geom, const
     if (!aligned16(q_bf16) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out_bf16) || !aligned16(workspace))
         return STEP5_ERR_INVALID_ARGUMENT;
     if (workspace == nullptr || workspace_bytes < step5_paged_workspace_bytes(geom)) return STEP5_ERR_WORKSPACE;
+    if (check_only()) return STEP5_OK;
     uint32_t* st = status_ptr();
     if (!st) return STEP5_ERR_CUDA;
     p.q = static_cast<const uint16_t*>(q_bf16);
@@ -169,7 +171,7 @@ step5_status attend_impl(const step5_geometry* geom, const step5_pages* pages, i
     const step5_status s = attend_params(p, geom, pages, N, B, window, q_bf16, geom ? (int64_t)geom->num_q_heads * 128 : 0,
                                          k_pages, v_pages, true, k_scales, v_scales, block_table, row_seq, row_pos,
                                          sel_ids, sel_count, gate, out_bf16, workspace, workspace_bytes);
-    if (s != STEP5_OK) return s;
+    if (s != STEP5_OK || check_only()) return s;
     CUtensorMap kmap, vmap;
     const uint64_t rows = (uint64_t)pages->num_pages * geom->num_kv_groups * pages->page_tokens;
     if (!encode_pool_map(&kmap, k_pages, rows, p.box_regions) || !encode_pool_map(&vmap, v_pages, rows, p.box_regions))
@@ -195,7 +197,7 @@ step5_status attend_bf16_impl(const step5_geometry* geom, const step5_pages* pag
     const step5_status s = attend_params(p, geom, pages, N, B, window, q_bf16, q_stride, k_pages, v_pages, false, nullptr,
                                          nullptr, block_table, row_seq, row_pos, sel_ids, sel_count, gate, out_bf16,
                                          workspace, workspace_bytes);
-    if (s != STEP5_OK) return s;
+    if (s != STEP5_OK || check_only()) return s;
     CUtensorMap kmap, vmap;
     const uint64_t regions = (uint64_t)pages->num_pages * geom->num_kv_groups * (pages->page_tokens / 8);
     if (!encode_bf16_map(&kmap, k_pages, regions, p.box_regions) || !encode_bf16_map(&vmap, v_pages, regions, p.box_regions))
@@ -304,6 +306,7 @@ step5_status step5_paged_plan(const step5_geometry* geom, const step5_pages* pag
         !row_start || !ends || !granted || !region_begin || !region_end)
         return STEP5_ERR_INVALID_ARGUMENT;
     if (N > 1 << 24 || B > kPlanMaxSeqs) return STEP5_ERR_UNSUPPORTED;
+    if (check_only()) return STEP5_OK;
     uint32_t* st = status_ptr();
     if (!st) return STEP5_ERR_CUDA;
     PlanParams p;

@@ -22,6 +22,7 @@ int32_t g_select_path = 0;  // 0 auto, 1 fused, 2 split
 int32_t g_overlap_prologue = 0;
 int32_t g_host_copies = 0;  // step5_decode_step_host: 1 = always through copies
 uint32_t g_wait_polls = 0;  // split path's waits on other blocks: 0 = kBarrierPolls
+thread_local int32_t t_check_only = 0;
 int32_t g_attn_path = 0;    // step (4): 0 auto (split: cluster; one block per pair: tensor cores), 1 warp MMA kernel, 2 tensor cores
 
 }  // namespace
@@ -45,6 +46,8 @@ step5_status check_geometry(const step5_geometry* g) {
     if (!(g->softmax_scale > 0.0f) || !isfinite(g->softmax_scale)) return STEP5_ERR_INVALID_ARGUMENT;
     return STEP5_OK;
 }
+
+bool check_only() { return t_check_only != 0; }
 
 uint32_t* status_ptr() {
     static uint32_t* ptr[64] = {};
@@ -305,6 +308,12 @@ const char* step5_status_string(step5_status s) {
 int32_t step5_set_host_copies(int32_t always) {
     const int32_t prev = g_host_copies;
     if (always == 0 || always == 1) g_host_copies = always;
+    return prev;
+}
+
+int32_t step5_set_check_only(int32_t enable) {
+    const int32_t prev = t_check_only;
+    if (enable == 0 || enable == 1) t_check_only = enable;
     return prev;
 }
 
@@ -595,7 +604,7 @@ step5_status step5_region_summarize(const step5_geometry* geom, int32_t B, int32
                                     uint8_t* summaries_e4m3, float* summaries_f32_or_null, step5_stream_t stream) {
     return summarize_impl(geom, B, t_cap, r_cap, max_regions_per_seq, idx_k_bf16, idx_z_bf16, rope_cos_bf16,
                           rope_sin_bf16, region_begin, region_end, summaries_e4m3, summaries_f32_or_null, stream,
-                          true);
+                          !check_only());
 }
 
 step5_status step5_index_score_topk(const step5_geometry* geom, int32_t N, int32_t B, int32_t t_cap, int32_t r_cap,
@@ -606,7 +615,7 @@ step5_status step5_index_score_topk(const step5_geometry* geom, int32_t N, int32
                                     size_t workspace_bytes, step5_stream_t stream) {
     return score_impl(geom, N, B, t_cap, r_cap, idx_q_bf16, w, row_seq, row_pos, rope_cos_bf16, rope_sin_bf16,
                       summaries_e4m3, sel_ids, sel_count, scores_or_null, sel_scores_or_null, workspace,
-                      workspace_bytes, stream, g_overlap_prologue, nullptr, nullptr, true);
+                      workspace_bytes, stream, g_overlap_prologue, nullptr, nullptr, !check_only());
 }
 
 step5_status step5_index_score_topk_shard(const step5_geometry* geom, int32_t N, int32_t B, int32_t t_cap,

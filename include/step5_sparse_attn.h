@@ -594,6 +594,14 @@ int32_t step5_set_select_path(int32_t mode);
  * ignored.  Returns the previous value. */
 int32_t step5_set_prologue_overlap(int32_t enable);
 
+/* 1: step5_paged_plan, step5_kv_append, step5_kv_append_e4m3, step5_region_summarize,
+ * step5_index_score_topk and the attention calls over pages only check their arguments:
+ * they return the status that the call would refuse them with, or STEP5_OK, and enqueue
+ * nothing, so that the calls of a step can be checked before its plan moves pages.  0
+ * (default): they run.  Of the calling thread; other values are ignored.  Returns the
+ * previous value. */
+int32_t step5_set_check_only(int32_t enable);
+
 /* step5_decode_step_host's host-buffer access: 0 (default) = in place when the host
  * buffers are device-addressable page-locked memory, else through copies; 1 = always
  * through copies.  Process-wide; other values are ignored.  Returns the previous value. */

@@ -1,0 +1,75 @@
+"""decode_step_paged with a plan on the GPU: what it refuses moves nothing, padded steps, either kind of pool, and a step
+captured in a graph and replayed."""
+import pytest
+import torch
+
+import paged_bf16_reference as B16
+import paged_reference as R
+from test_gpu_paged import dev, geometry, normal, s5, status  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+class Step:
+    """Three sequences in a table of six with a planned step of one or two tokens each: everything that decode_step_paged takes.
+    The indexer's tensors have random values (finite, as the front end writes them)."""
+
+    def __init__(self, s5, N=6, e4m3=False, lengths=(300, 0, 77, 0, 1001, 0), new=(1, 0, 2, 0, 1, 0), pt=64, seed=1, cap=2048):  # noqa: F811
+        gen = torch.Generator().manual_seed(seed)
+        self.s5, self.gen, self.N, self.pt, self.e4m3 = s5, gen, N, pt, e4m3
+        self.geom = g = geometry(s5, top_k=32)
+        B = self.B = len(lengths)
+        self.table = s5.PagedTable.create(B * cap // pt, pt, cap // pt, B)
+        self.rows = s5.PagedRows.create(B, N)
+        self.cache = s5.PagedCache.create(g, B * cap // pt, pt, self.table.block_table, e4m3=e4m3)
+        self.lengths, self.new = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (lengths, new))
+        # the tokens that are there
+        start = s5.PagedRows.create(B, sum(lengths))
+        s5.step5_paged_plan(self.table, start, torch.zeros_like(self.lengths), self.lengths)
+        k, v = (normal(gen, sum(lengths), 4, 128).cuda() for _ in "kv")
+        (s5.step5_kv_append_e4m3 if e4m3 else s5.step5_kv_append)(g, k, v, self.cache, start.row_seq, start.row_pos)
+        self.t = {"q": normal(gen, N, 32, 128, scale=1.5).cuda(), "idx_q": normal(gen, N, 16, 64).cuda(), "w": torch.rand(N, 16, generator=gen).cuda(),
+                  "idx_k": normal(gen, B, 4, cap, 64).cuda(), "idx_z": normal(gen, B, 4, cap, 64).cuda(), "cos": None, "sin": None,
+                  "summaries": torch.zeros((B, 4, cap // 8, 64), dtype=torch.uint8, device="cuda")}
+        s5.step5_region_summarize(g, self.t["idx_k"], self.t["idx_z"], None, None, torch.zeros_like(self.lengths), self.lengths // 8,
+                                  self.t["summaries"])
+        half = normal(gen, cap, 64).cuda()
+        i32 = lambda *shape: torch.full(shape, 55, dtype=torch.int32, device="cuda")
+        self.args = {"k": normal(gen, N, 4, 128).cuda(), "v": normal(gen, N, 4, 128).cuda(), "sel_ids": i32(N, 4, 32), "sel_count": i32(N, 4),
+                     "q_rot": torch.full_like(self.t["q"], 5.0), "out": torch.full_like(self.t["q"], 5.0),
+                     "ws": s5.Workspace.create(g, N, cap // 8), "paged_ws": s5.PagedWorkspace.create(g), "cos": half, "sin": half,
+                     "gate": normal(gen, N, 32).cuda(), "max_regions_per_seq": 1}
+        assert status(s5) == 0
+
+    def run(self, **over):
+        t = {**self.t, **{k[2:]: over.pop(k) for k in list(over) if k.startswith("t_")}}
+        a = {**self.args, **over}
+        self.s5.decode_step_paged(self.geom, t, self.cache, plan=(self.table, self.rows, self.lengths, self.new), **a)
+
+    def state(self):
+        names = ("block_table", "held", "free_pages", "free_count")
+        return [getattr(self.table, n).clone() for n in names] + [self.lengths.clone(), self.cache.k.clone()]
+
+
+def test_what_a_planned_step_refuses_moves_nothing(s5):  # noqa: F811
+    """Every argument of the calls behind the plan is checked before it runs: with lengths the plan's own ends, as a captured
+    step has them, a step that moved pages and then failed would grow the sequences twice when it is called again."""
+    c = Step(s5, N=4)
+    c.rows.ends = c.lengths
+    before = c.state()
+    a, t = c.args, c.t
+    off = lambda x: torch.zeros(x.numel() + 4, dtype=x.dtype, device="cuda")[4:].view(x.shape)  # (8 bytes past an alignment of 16)
+    for bad in (dict(k=a["k"][:3]), dict(k=a["k"].float()), dict(v=a["v"].cpu()), dict(v=a["v"][:, :2]), dict(k=off(a["k"])), dict(q_rot=a["q_rot"][:2]),
+                dict(q_rot=None), dict(cos=a["cos"][:, :20]), dict(cos=a["cos"], sin=None), dict(cos=a["cos"][:, :12].contiguous(), sin=a["sin"][:, :12].contiguous()),
+                dict(sel_ids=a["sel_ids"][..., :16]), dict(sel_ids=a["sel_ids"].long()), dict(sel_count=a["sel_count"][:3]), dict(sel_ids=None),
+                dict(out=a["out"][:3]), dict(out=off(a["out"])), dict(out=None), dict(gate=a["gate"].float()), dict(gate=a["gate"][:, :8]),
+                dict(paged_ws=None), dict(paged_ws=torch.zeros(64, dtype=torch.uint8, device="cuda")), dict(ws=None), dict(max_regions_per_seq=-1),
+                dict(t_idx_q=off(t["idx_q"])), dict(t_idx_k=off(t["idx_k"])), dict(t_summaries=t["summaries"][..., :32]),
+                dict(t_summaries=t["summaries"].cpu()), dict(t_q=off(t["q"])), dict(t_cos=a["cos"][:, :16].contiguous())):
+        with pytest.raises((ValueError, s5.Step5Error, AttributeError, TypeError)):
+            c.run(**bad)
+        assert all(torch.equal(x, y) for x, y in zip(before, c.state())), list(bad)
+        assert status(s5) == 0 and bool((a["out"] == 5.0).all())
+    c.run()  # (none of them left the checks on)
+    assert status(s5) == 0
+    assert c.lengths.tolist() == [301, 0, 79, 0, 1002, 0] and not bool((a["out"] == 5.0).all())

@@ -162,3 +162,49 @@ def test_a_step_of_other_rows_or_sequences_than_its_indexers_is_refused(s5, monk
     with pytest.raises(ValueError, match=name):
         s5.decode_step_paged(geom, t, cache, None, None, bf16(2, 4, 128), bf16(2, 4, 128), *[None] * 4, max_regions_per_seq=16, plan=plan)
     assert not ran
+
+
+def test_calls_that_only_check(s5):  # noqa: F811
+    """While a thread's checks alone are on, its calls of a paged step refuse what they refuse, and enqueue nothing (without a GPU
+    a call that went on would fail); another thread's are not touched."""
+    import threading
+
+    if torch.cuda.is_available():
+        pytest.skip("addresses that no GPU may see")
+
+    from test_paged_boundary import append
+    from test_paged_boundary import attend as attend_e4m3
+    lib, g = s5.load(), ctypes.byref(s5.STEP5_GEOMETRY)
+    summarize = lambda span=4, k=FAKE: lib.step5_region_summarize(g, 2, 64, 8, span, k, FAKE, None, None, FAKE, FAKE, FAKE, None, None)
+    score = lambda N=2, q=FAKE: lib.step5_index_score_topk(g, N, 2, 64, 8, q, FAKE, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, None, None, FAKE, 1 << 40, None)
+    assert s5.step5_set_check_only(1) == 0
+    try:
+        assert [plan(s5), append(s5), append(s5, e4m3=False), attend(s5, False), attend(s5, True), attend_e4m3(s5, False),
+                attend_e4m3(s5, True), summarize(), score()] == [0] * 9
+        assert [plan(s5, N=0), append(s5, k=ODD), append(s5, e4m3=False, rot=24), attend(s5, False, qs=4100), attend(s5, True, ws=None),
+                attend_e4m3(s5, False, out=None), attend_e4m3(s5, True, N=65536), summarize(k=ODD), summarize(-1), score(0), score(q=None)] \
+            == [1, 1, 2, 1, 3, 1, 2, 1, 1, 1, 1]
+        assert s5.step5_set_check_only(2) == 1 and s5.step5_set_check_only(1) == 1
+        seen = []
+        other = threading.Thread(target=lambda: seen.append(s5.step5_set_check_only(0)))
+        other.start()
+        other.join()
+        assert seen == [0]
+    finally:
+        assert s5.step5_set_check_only(0) == 1
+    assert plan(s5) == 4
+
+
+def test_what_the_other_calls_of_a_planned_step_refuse_is_refused_before_it(s5, monkeypatch):  # noqa: F811
+    """The plan runs behind the checks of every call: here the first of them finds its tensors on the CPU."""
+    ran, geom = [], s5.STEP5_GEOMETRY
+    monkeypatch.setattr(s5, "step5_paged_plan", lambda *a, **kw: ran.append(1))
+    table = s5.PagedTable.create(6, 64, 2, 2, device="cpu")
+    cache = s5.PagedCache.create(geom, 6, 64, table.block_table, e4m3=False, device="cpu")
+    bf16 = lambda *of: torch.zeros(of, dtype=torch.bfloat16)
+    t = {"q": bf16(2, 32, 128), "idx_q": bf16(2, 16, 64), "w": torch.zeros(2, 16), "idx_k": bf16(2, 4, 128, 64), "idx_z": bf16(2, 4, 128, 64),
+         "summaries": torch.zeros((2, 4, 16, 64), dtype=torch.uint8), "cos": None, "sin": None}
+    rows, of = s5.PagedRows.create(2, 2, device="cpu"), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises((ValueError, RuntimeError, AssertionError)):
+        s5.decode_step_paged(geom, t, cache, None, None, bf16(2, 4, 128), bf16(2, 4, 128), *[None] * 4, max_regions_per_seq=1, plan=(table, rows, of, of))
+    assert not ran and s5.step5_set_check_only(0) == 0
