@@ -886,8 +886,7 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
     tensors of ``t`` as decode_step does, and attend over the picked regions of the cache.  With ``plan``,
     (table, rows, lengths, new_tokens) as step5_paged_plan takes them, the step is planned first, and its
     rows and regions take the place of t's row_seq, row_pos, sum_begin and sum_end; no page moves if the plan or a
-    call behind it refuses an argument.  (Rows that it pads have no
-    picks and no output, and the scoring, which knows no padding, sets DEV_RANGE for them.)"""
+    call behind it refuses an argument.  Rows that it pads have no picks, and their q_rot and out are left as they are."""
     rows = t
     if plan is not None:
         table, p = plan[:2]

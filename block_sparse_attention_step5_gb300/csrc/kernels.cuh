@@ -150,7 +150,7 @@ struct ScoreParams {
     const int32_t* defer_begin;
     const int32_t* defer_end;
 };
-// Validated (sequence, R) of row n, or R = -1 when the row is out of range.
+// Validated (sequence, R) of row n, or R = -1 when the row is out of range (or padding: sequence -1, no error).
 // Candidate regions of row n in this call's summaries: region_lo + [0, R).  A whole-row
 // call needs a slot for every candidate; a shard takes those of its slots.
 __device__ __forceinline__ int row_regions(const ScoreParams& p, int n, int& b, int& pos) {

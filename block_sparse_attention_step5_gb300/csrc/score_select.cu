@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kFusedThreads) score_fused_kernel(ScoreParams 
     int b, pos;
     int R = row_regions(p, n, b, pos);
     if (R < 0 || R > key_cap) {
-        if (threadIdx.x == 0) raise_status(p.status, kDevRange);
+        if (threadIdx.x == 0 && b != -1) raise_status(p.status, kDevRange);
         R = 0;
         b = 0;
         pos = 0;
@@ -908,7 +908,7 @@ __device__ __forceinline__ Tile next_tile(const ScoreParams& p, Walk& k, int lim
         if (n != k.cn) {
             k.cn = n;
             k.cR = row_regions(p, n, k.cb, k.cpos);
-            if (k.cR < 0 && threadIdx.x == 0) raise_status(p.status, kDevRange);
+            if (k.cR < 0 && k.cb != -1 && threadIdx.x == 0) raise_status(p.status, kDevRange);
         }
         if (k.r >= k.cR) {  // the rest of this (row, group) holds no candidate
             k.left -= p.r_cap - k.r;

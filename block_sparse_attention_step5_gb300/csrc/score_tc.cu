@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kScThreads) score_tc_kernel(const __grid_const
         int b = -1, R = -1, pos = 0;
         if (n < p.N) {
             R = row_regions(p, n, b, pos);
-            if (R < 0) raise_status(p.status, kDevRange);
+            if (R < 0 && b != -1) raise_status(p.status, kDevRange);
         }
         s_b[j] = R < 0 ? -1 : b;
         s_R[j] = R;

@@ -135,6 +135,7 @@ step5_status step5_region_summarize(const step5_geometry* geom, int32_t B, int32
  * sel_ids: [N][G][top_k]; sel_count: [N][G].
  * scores_or_null: [N][G][r_cap] fp32, receives every score (entries past R(p) are not
  * written).  sel_scores_or_null: [N][G][top_k] fp32, the picked scores (-inf padding).
+ * A row of sequence -1 is padding: it has no picks (sel_count 0, ids -1) and raises no flag.
  * workspace: see step5_workspace_bytes / step5_workspace_init. */
 step5_status step5_index_score_topk(const step5_geometry* geom, int32_t N, int32_t B,
                                     int32_t t_cap, int32_t r_cap,

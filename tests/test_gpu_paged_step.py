@@ -73,3 +73,49 @@ def test_what_a_planned_step_refuses_moves_nothing(s5):  # noqa: F811
     c.run()  # (none of them left the checks on)
     assert status(s5) == 0
     assert c.lengths.tolist() == [301, 0, 79, 0, 1002, 0] and not bool((a["out"] == 5.0).all())
+
+
+@pytest.mark.parametrize("path", [0, 1, 2, 3])
+@pytest.mark.parametrize("noalloc", [False, True])
+def test_scoring_of_padding(s5, path, noalloc):  # noqa: F811
+    """Rows of sequence -1 have no picks and raise no flag, on every selection path; the other rows' picks are what they
+    are without them, and a row out of range is still told."""
+    g = geometry(s5, top_k=64)
+    gen = torch.Generator().manual_seed(path)
+    B, t_cap = 3, 4096
+    summ = torch.randint(0, 120, (B, 4, t_cap // 8, 64), generator=gen).to(torch.uint8).cuda()
+    N = 24
+    seq = torch.tensor([0, -1, 1, -1, -1, 2, 2, -1] * 3, dtype=torch.int32)
+    pos = torch.where(seq >= 0, torch.randint(0, t_cap, (N,), generator=gen), torch.tensor([-1, 7, 1 << 30] * 8)).int()
+    q, w = normal(gen, N, 16, 64).cuda(), torch.rand(N, 16, generator=gen).cuda()
+
+    def score(keep, seq=seq, pos=pos):
+        n = int(keep.sum())
+        out = [torch.full((n, 4, 64), 99, dtype=torch.int32, device="cuda"), torch.full((n, 4), 99, dtype=torch.int32, device="cuda"),
+               torch.full((n, 4, 64), 99.0, device="cuda")]
+        at = (g, q[keep].contiguous(), w[keep].contiguous(), *dev(seq[keep], pos[keep]), None, None, summ, *out[:2])
+        prev = s5.step5_set_select_path(path)
+        try:
+            if noalloc:
+                s5.step5_index_score_topk_noalloc(*at, t_cap=t_cap, sel_scores=out[2])
+            else:
+                s5.step5_index_score_topk(*at, s5.Workspace.create(g, n, t_cap // 8).tensor, t_cap=t_cap, sel_scores=out[2])
+        finally:
+            s5.step5_set_select_path(prev)
+        return out
+    real = seq >= 0
+    got = score(torch.ones(N, dtype=torch.bool))
+    assert status(s5) == 0
+    pad = [x[~real] for x in got]
+    assert bool((pad[0] == -1).all()) and bool((pad[1] == 0).all()) and bool((pad[2] == float("-inf")).all())
+    alone = score(real)
+    assert status(s5) == 0 and all(torch.equal(x[real], y) for x, y in zip(got, alone))
+    none = score(~real)
+    assert status(s5) == 0 and all(torch.equal(x, y) for x, y in zip(none, pad))
+    for b, p in ((-2, 0), (B, 0), (0, t_cap), (0, -1)):
+        seq2, pos2 = seq.clone(), pos.clone()
+        seq2[5], pos2[5] = b, p
+        got2 = score(torch.ones(N, dtype=torch.bool), seq2, pos2)
+        assert status(s5) == s5.DEV_RANGE, (b, p)
+        keep = real & (torch.arange(N) != 5)
+        assert all(torch.equal(x[keep], y[keep]) for x, y in zip(got2, got))
