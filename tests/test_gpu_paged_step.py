@@ -119,3 +119,84 @@ def test_scoring_of_padding(s5, path, noalloc):  # noqa: F811
         assert status(s5) == s5.DEV_RANGE, (b, p)
         keep = real & (torch.arange(N) != 5)
         assert all(torch.equal(x[keep], y[keep]) for x, y in zip(got2, got))
+
+
+def check_step(s5, c):  # noqa: F811
+    """A step's outputs against the attention over what the cache holds, and its picks against the scoring of its rows alone."""
+    real = c.rows.row_seq >= 0
+    seq, pos = c.rows.row_seq[real], c.rows.row_pos[real]
+    a = c.args
+    for x, left in (("q_rot", 5.0), ("out", 5.0), ("sel_ids", -1), ("sel_count", 0)):
+        assert bool((a[x][~real] == left).all()), x
+    if not bool(real.any()):
+        return
+    half = a["cos"].cpu(), a["sin"].cpu()
+    q_rot, ids, cnt, out, gate = (a[x][real].cpu() for x in ("q_rot", "sel_ids", "sel_count", "out", "gate"))
+    assert torch.equal(q_rot.double(), R.rotate(c.t["q"][real].cpu().double(), *half, pos.cpu().long()))
+    n = int(real.sum())
+    ids2, cnt2 = torch.empty_like(a["sel_ids"][:n]), torch.empty_like(a["sel_count"][:n])
+    s5.step5_index_score_topk(c.geom, c.t["idx_q"][real], c.t["w"][real], seq, pos, None, None, c.t["summaries"], ids2, cnt2,
+                              s5.Workspace.create(c.geom, n, c.t["summaries"].shape[2]).tensor, t_cap=c.t["idx_k"].shape[2])
+    assert torch.equal(ids2.cpu(), ids) and torch.equal(cnt2.cpu(), cnt)
+    args = (c.table.block_table.cpu(), seq.cpu(), pos.cpu(), c.geom.softmax_scale)
+    if c.e4m3:
+        want = R.attend(q_rot, R.decode(c.cache.k), R.decode(c.cache.v), c.cache.k_scales.cpu(), c.cache.v_scales.cpu(), *args,
+                        ids=ids, counts=cnt, gate=gate)
+        assert R.off(out, *want) <= 1.0
+    else:
+        want = B16.attend(q_rot, c.cache.k.cpu(), c.cache.v.cpu(), *args, ids=ids, counts=cnt, gate=gate)
+        assert B16.off(out, *want, False) <= 1.0
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("pt", [16, 64])
+def test_padded_steps(s5, e4m3, pt):  # noqa: F811
+    """Steps of six rows of which sequences take one, two or none, with sequences that start, pause, are rolled back and find no
+    pages: nothing is flagged, padding is left alone, and every output is right."""
+    c = Step(s5, e4m3=e4m3, pt=pt, seed=pt)
+    for new in ([1, 0, 2, 0, 1, 0], [0, 0, 0, 0, 0, 0], [0, 1, 2, 0, 3, 0], [1, 0, 0, 0, 0, 0], [1, 1, 1, 1, 1, 1]):
+        c.new.copy_(torch.tensor(new))
+        for x, left in (("q_rot", 5.0), ("out", 5.0), ("sel_ids", 55), ("sel_count", 55)):
+            c.args[x].fill_(left)
+        c.run()
+        assert status(s5) == 0 and c.rows.granted.tolist() == new
+        check_step(s5, c)
+        c.lengths = c.rows.ends.clone()
+    # no page left for the second, third and fourth sequence, whose next tokens need one
+    c.table.free_count.zero_()
+    held = c.table.held.tolist()
+    c.lengths.copy_(torch.tensor([c.lengths[0].item(), held[1] * pt, held[2] * pt, held[3] * pt, 100, 1]))
+    c.new.copy_(torch.tensor([1, 1, 1, 2, 1, 0]))
+    c.table.held[4] = -(-101 // pt)
+    for x, left in (("q_rot", 5.0), ("out", 5.0)):
+        c.args[x].fill_(left)
+    c.run()
+    assert status(s5) == 0 and c.rows.granted.tolist() == [1, 0, 0, 0, 1, 0]
+    check_step(s5, c)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_captured_planned_step(s5, e4m3):  # noqa: F811
+    """The whole step in a graph that goes on from the one before, replayed past the ends of pages and regions, against the
+    same steps called one after another: the same bits."""
+    steps = [Step(s5, e4m3=e4m3, pt=16, seed=3) for _ in range(2)]
+    for c in steps:
+        c.rows.ends = c.lengths
+        c.run()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        steps[0].run()
+    for i in range(20):
+        for c in steps:
+            c.t["q"].copy_(normal(torch.Generator().manual_seed(i), *c.t["q"].shape))
+            c.new.copy_(torch.tensor([1, i % 2, 2, 0, 1, 0]))
+        graph.replay()
+        steps[1].run()
+        for x in ("q_rot", "out", "sel_ids", "sel_count"):
+            assert torch.equal(*(c.args[x] for c in steps)), (i, x)
+        assert all(torch.equal(x, y) for x, y in zip(*(c.state() for c in steps)))
+        assert torch.equal(*(c.t["summaries"] for c in steps))
+    assert status(s5) == 0
+    assert steps[0].lengths.tolist() == [321, 10, 119, 0, 1022, 0]
+    check_step(s5, steps[0])
