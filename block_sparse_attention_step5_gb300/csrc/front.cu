@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kFrontThreads) front_kernel(FrontParams p) {
     }
     const int b = p.row_seq[n], pos = p.row_pos[n];
     if (b < 0 || b >= p.B || pos < 0 || pos >= p.t_cap) {
-        if (tid == 0) raise_status(p.status, kDevRange);
+        if (tid == 0 && b != -1) raise_status(p.status, kDevRange);
         return;  // the same for the whole block
     }
     // ---- k: LayerNorm with bias, z as it is, at token pos (one thread per (group, dim))

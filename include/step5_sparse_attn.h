@@ -87,7 +87,8 @@ typedef struct {
  * cache holds rotated k).  Up to 4 KV groups.  A row whose region completes reads
  * that region's other 7 tokens from the caches: rows of one call must not write into
  * one another's completing regions (decode: one row per sequence).  Out-of-range rows
- * set STEP5_DEV_RANGE and write nothing but their normalised q. */
+ * set STEP5_DEV_RANGE and write nothing but their normalised q; rows of sequence -1 are
+ * padding, the same without the flag. */
 step5_status step5_indexer_front(const step5_geometry* geom, int32_t N, int32_t B, int32_t t_cap,
                                  int32_t r_cap, const void* q_pre_bf16, const void* k_pre_bf16,
                                  const void* z_pre_bf16, const void* q_norm_w_bf16,

@@ -200,3 +200,30 @@ def test_a_captured_planned_step(s5, e4m3):  # noqa: F811
     assert status(s5) == 0
     assert steps[0].lengths.tolist() == [321, 10, 119, 0, 1022, 0]
     check_step(s5, steps[0])
+
+
+def test_front_end_of_padding(s5):  # noqa: F811
+    """The front end of a planned step's rows: padding raises no flag and writes nothing but its normalised q; a row out of range
+    is still told."""
+    c = Step(s5)
+    c.run()
+    g, N, t = c.geom, c.N, c.t
+    pre = [normal(c.gen, N, h, 64).cuda() for h in (16, 4, 4)]
+    norm = [normal(c.gen, 64).cuda() for _ in range(3)]
+    real = c.rows.row_seq >= 0
+
+    def front(rows, seq, pos):
+        q, k, z, summ = torch.full_like(pre[0][rows], 5.0), t["idx_k"].clone(), t["idx_z"].clone(), t["summaries"].clone()
+        s5.step5_indexer_front(g, *(x[rows].contiguous() for x in pre), *norm, 1e-6, seq[rows].contiguous(), pos[rows].contiguous(), None, None,
+                               q, k, z, summ)
+        return q, k, z, summ
+    every = torch.ones_like(real)
+    got = front(every, c.rows.row_seq, c.rows.row_pos)
+    assert status(s5) == 0 and bool(real.any()) and not bool(real.all())
+    alone = front(real, c.rows.row_seq, c.rows.row_pos)
+    assert status(s5) == 0 and torch.equal(got[0][real], alone[0]) and all(torch.equal(x, y) for x, y in zip(got[1:], alone[1:]))
+    for b, p in ((-2, 0), (c.B, 0), (0, -1), (0, 2048)):
+        seq, pos = c.rows.row_seq.clone(), c.rows.row_pos.clone()
+        seq[-1], pos[-1] = b, p
+        bad = front(every, seq, pos)
+        assert status(s5) == s5.DEV_RANGE and all(torch.equal(x, y) for x, y in zip(got, bad)), (b, p)
