@@ -10,8 +10,9 @@
 // little): its barrier stands between the reads of what is changed in place (held, the stack, the lengths where `ends` is
 // the same buffer) and the writes, and again between the pages put onto the stack and those taken off it.
 //
-// What it takes: 64 sequences of a token each 5.4 us, 1,024 sequences and 65,536 rows 8.9 us (by graph replay; 0.6 MB: all of it
-// latency, dependent loads and five block barriers and two of the cluster; a kernel that adds to one number takes 1.3).
+// What it takes, of steps that take pages and steps that give them back in turn: 64 sequences of a token each 5.4 us, 1,024 sequences
+// and 65,536 rows 8.9 us (by graph replay; 0.6 MB: all of it latency, dependent loads and five block barriers and two of the cluster;
+// a kernel that adds to one number takes 1.3).
 #include "paged.cuh"
 
 namespace step5 {
@@ -212,9 +213,9 @@ cudaError_t launch(const PlanParams& p, unsigned ctas, cudaStream_t stream, bool
 }  // namespace
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream, bool pdl) {
-    // One block of 256 threads, or a cluster of 8 of 1,024 (whose barriers cost more than little work spread), microseconds: 64
-    // sequences of a row each 5.0 and 5.6, of 15 rows 5.2 and 5.5, of 62 8.0 and 5.6; 256 of a row each 6.8 and 7.1, 500 7.9 and
-    // 7.5, 1,000 9.5 and 8.3, 2,048 15.1 and 9.8.
+    // One block of 256 threads, or a cluster of 8 of 1,024 (whose barriers cost more than little work spread), microseconds of steps
+    // that move no page: 64 sequences of a row each 5.0 and 5.6, of 15 rows 5.2 and 5.5, of 62 8.0 and 5.6; 256 of a row each 6.8 and
+    // 7.1, 500 7.9 and 7.5, 1,000 9.5 and 8.3, 2,048 15.1 and 9.8.
     return (int64_t)p.N + p.B <= 1024 ? launch<256>(p, 1, stream, pdl) : launch<1024>(p, 8, stream, pdl);
 }
 

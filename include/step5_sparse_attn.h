@@ -523,7 +523,7 @@ step5_status step5_sparse_attn_paged(const step5_geometry* geom, const step5_pag
  * A sequence out of range (a negative length or count, tokens past table_len * page_tokens, held_pages outside
  * [0, table_len]) or whose rows end past N keeps its pages, is granted nothing and sets STEP5_DEV_RANGE, as do a
  * free_count outside [0, num_pages], more pages given back than the stack has room for (those are lost) and page
- * numbers outside [0, num_pages] (which are moved as they are).  ends may be the same buffer as lengths; the others lie apart.
+ * numbers outside [0, num_pages) (which are moved as they are).  ends may be the same buffer as lengths; the others lie apart.
  * All pointers are device pointers; block_table is required.  N <= 2^24 rows, B <= 8192 sequences. */
 step5_status step5_paged_plan(const step5_geometry* geom, const step5_pages* pages, int32_t N, int32_t B,
                               const int32_t* lengths, const int32_t* new_tokens, int32_t* block_table,

@@ -165,3 +165,24 @@ def test_graph_of_steps(s5):  # noqa: F811
         assert not bad and rows.ends.tolist() == at and rows.row_pos.tolist() == want["row_pos"]
         assert s.gpu.block_table.tolist() == s.table and s.gpu.held.tolist() == s.held
     assert status(s5) == 0
+
+
+@pytest.mark.parametrize("B, pt, N", [(3, 16, 64), (40, 8, 300), (600, 24, 3000)])
+def test_the_stack_above_its_top(s5, B, pt, N):  # noqa: F811
+    """Entries of the stack past the pages that lay on it and those given back stay as they were."""
+    rng = random.Random(B)
+    table_len = 20
+    num = 3 * B * table_len
+    order = list(range(num))
+    rng.shuffle(order)
+    lengths = [rng.randint(0, table_len * pt // 2) for _ in range(B)]
+    s = Slots(s5, num, pt, table_len, [-(-n // pt) for n in lengths], order, free=B * table_len)
+    s.gpu.free_pages[len(s.free):] = torch.arange(-1000, -1000 - num + len(s.free), -1, dtype=torch.int32, device="cuda")
+    for _ in range(4):
+        lengths = [0 if rng.random() < 0.3 else rng.randint(0, n) for n in lengths]
+        new = [rng.randint(0, min(table_len * pt - n, 2 * N // B // 2)) for n in lengths]
+        top, held = len(s.free), list(s.held)
+        want, above = s.step(N, lengths, new)
+        given = sum(max(0, a - b) for a, b in zip(held, s.held))
+        assert s.gpu.free_pages.tolist()[top + given:] == above[top + given:]
+        lengths = want["ends"]
