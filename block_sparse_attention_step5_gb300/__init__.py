@@ -172,8 +172,12 @@ def _check(fn: str, status: int):
         raise Step5Error(fn, status)
 
 
-def _run(fn: str, *args):
-    _check(fn, getattr(load(), fn)(*args))
+def _run(call):
+    """Makes a call that has been checked and laid out: the C function's name and its arguments."""
+    fn, args = call
+    st = getattr(load(), fn)(*args)
+    if st:
+        raise Step5Error(fn, st)
 
 
 def step5_status_string(status: int) -> str:
@@ -250,8 +254,8 @@ def step5_region_summarize(geom, idx_k, idx_z, cos, sin, region_begin, region_en
                            summaries, summaries_f32=None, max_regions_per_seq=None, stream=None):
     """idx_k/idx_z [B][G][t_cap][64] bf16, cos/sin [t_cap][rope/2] bf16 (or None),
     region_begin/end [B] int32, summaries [B][G][r_cap][64] uint8 (written)."""
-    _run(*_summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summaries, summaries_f32,
-                          max_regions_per_seq, stream))
+    _run(_summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summaries, summaries_f32,
+                         max_regions_per_seq, stream))
 
 
 def _summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summaries, summaries_f32, max_regions_per_seq,
@@ -260,17 +264,17 @@ def _summarize_call(geom, idx_k, idx_z, cos, sin, region_begin, region_end, summ
     r_cap = summaries.shape[2]
     if max_regions_per_seq is None:
         max_regions_per_seq = r_cap
-    return ("step5_region_summarize", ctypes.byref(Geometry.of(geom)), B, t_cap, r_cap, int(max_regions_per_seq), _ptr(idx_k),
-            _ptr(idx_z), _ptr(cos), _ptr(sin), _ptr(region_begin), _ptr(region_end), _ptr(summaries), _ptr(summaries_f32),
-            _stream(stream))
+    return "step5_region_summarize", (
+        ctypes.byref(Geometry.of(geom)), B, t_cap, r_cap, int(max_regions_per_seq), _ptr(idx_k), _ptr(idx_z), _ptr(cos), _ptr(sin),
+        _ptr(region_begin), _ptr(region_end), _ptr(summaries), _ptr(summaries_f32), _stream(stream))
 
 
 def step5_index_score_topk(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids,
                            sel_count, workspace, t_cap, scores=None, sel_scores=None, stream=None):
     """idx_q [N][idx_heads][64] bf16, w [N][idx_heads] fp32, row_seq/row_pos [N] int32,
     summaries [B][G][r_cap][64] uint8; writes sel_ids [N][G][top_k], sel_count [N][G]."""
-    _run(*_score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, sel_count, workspace, t_cap, scores,
-                      sel_scores, stream))
+    _run(_score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, sel_count, workspace, t_cap, scores,
+                     sel_scores, stream))
 
 
 def _score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, sel_count, workspace, t_cap, scores, sel_scores,
@@ -278,9 +282,10 @@ def _score_call(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids, 
     N = idx_q.shape[0]
     B, _, r_cap, _ = summaries.shape
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return ("step5_index_score_topk", ctypes.byref(Geometry.of(geom)), N, B, int(t_cap), r_cap, _ptr(idx_q), _ptr(w),
-            _ptr(row_seq), _ptr(row_pos), _ptr(cos), _ptr(sin), _ptr(summaries), _ptr(sel_ids), _ptr(sel_count), _ptr(scores),
-            _ptr(sel_scores), _ptr(workspace), ws_bytes, _stream(stream))
+    return "step5_index_score_topk", (
+        ctypes.byref(Geometry.of(geom)), N, B, int(t_cap), r_cap, _ptr(idx_q), _ptr(w), _ptr(row_seq), _ptr(row_pos), _ptr(cos),
+        _ptr(sin), _ptr(summaries), _ptr(sel_ids), _ptr(sel_count), _ptr(scores), _ptr(sel_scores), _ptr(workspace), ws_bytes,
+        _stream(stream))
 
 
 def step5_index_score_topk_noalloc(geom, idx_q, w, row_seq, row_pos, cos, sin, summaries, sel_ids,
@@ -687,9 +692,9 @@ def _append_call(fn: str, e4m3: bool, geom, k, v, cache: PagedCache, row_seq, ro
         sp = _arg("sin", sin, torch.bfloat16, table, dev)
         t_cap, half = table
     rows = (N,)
-    return (fn, g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
-            _arg("row_seq", row_seq, torch.int32, rows, dev), _arg("row_pos", row_pos, torch.int32, rows, dev), cp, sp, qo,
-            *cache._pools, st)
+    return fn, (g, cache._pages, N, cache.B, 2 * half, t_cap, qp, qs, kp, ks, vp, vs,
+                _arg("row_seq", row_seq, torch.int32, rows, dev), _arg("row_pos", row_pos, torch.int32, rows, dev), cp, sp, qo,
+                *cache._pools, st)
 
 
 def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
@@ -698,14 +703,14 @@ def step5_kv_append(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, s
     writes it and v into the bf16 cache at (row_seq, row_pos) [N] int32; with q
     [N][Hq][128], its rotation into q_out.  q, k and v may be slices of one [N][heads][128]
     tensor (rows apart, heads together)."""
-    _run(*_append_call("step5_kv_append", False, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
+    _run(_append_call("step5_kv_append", False, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
 
 
 def step5_kv_append_e4m3(geom, k, v, cache: PagedCache, row_seq, row_pos, cos=None, sin=None, q=None, q_out=None,
                          stream=None):
     """step5_kv_append into an e4m3 cache: codes and the power-of-two scale of each region
     and group.  A sequence's rows stand together at ascending positions (see the header)."""
-    _run(*_append_call("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
+    _run(_append_call("step5_kv_append_e4m3", True, geom, k, v, cache, row_seq, row_pos, cos, sin, q, q_out, stream))
 
 
 def _attend_call(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_pos, out, ws, gate, stream, window=None,
@@ -726,10 +731,10 @@ def _attend_call(fn: str, e4m3: bool, geom, q, cache: PagedCache, row_seq, row_p
     else:
         before, after = (window,), ()
     rows = (_arg("q", q, torch.bfloat16, shape, dev),) if e4m3 else _rows("q", q, Hq, g.head_dim, dev, N)
-    return (fn, g, cache._pages, N, cache.B, *before, *rows, *cache._pools, _arg("row_seq", row_seq, torch.int32, (N,), dev),
-            _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
-            None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
-            _arg("out", out, torch.bfloat16, shape, dev), None if w is None else w.data_ptr(), 0 if w is None else w.nbytes, st)
+    return fn, (g, cache._pages, N, cache.B, *before, *rows, *cache._pools, _arg("row_seq", row_seq, torch.int32, (N,), dev),
+                _arg("row_pos", row_pos, torch.int32, (N,), dev), *after,
+                None if gate is None else _arg("gate", gate, torch.bfloat16, (N, Hq), dev),
+                _arg("out", out, torch.bfloat16, shape, dev), None if w is None else w.data_ptr(), 0 if w is None else w.nbytes, st)
 
 
 def _window(window) -> int:
@@ -741,32 +746,32 @@ def step5_paged_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, out, wor
     """Causal attention of rows q [N][Hq][128] bf16 at (row_seq, row_pos) over the e4m3
     cache's tokens max(0, pos - window + 1) .. pos (window 0: all) -> out, with the per-head
     sigmoid gate [N][Hq] when given."""
-    _run(*_attend_call("step5_paged_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                       window=_window(window)))
+    _run(_attend_call("step5_paged_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                      window=_window(window)))
 
 
 def step5_paged_attn(geom, q, cache: PagedCache, row_seq, row_pos, out, workspace, window: int = 0, gate=None,
                      stream=None):
     """step5_paged_attn_e4m3 over the bf16 cache.  q may be a slice of one [N][heads][128]
     tensor (rows apart, heads together)."""
-    _run(*_attend_call("step5_paged_attn", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                       window=_window(window)))
+    _run(_attend_call("step5_paged_attn", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                      window=_window(window)))
 
 
 def step5_sparse_attn_e4m3(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                            gate=None, stream=None):
     """step5_sparse_attn over the e4m3 cache: the picked regions sel_ids [N][G][top_k],
     sel_count [N][G] and the row's own region."""
-    _run(*_attend_call("step5_sparse_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                       sel_ids=sel_ids, sel_count=sel_count))
+    _run(_attend_call("step5_sparse_attn_e4m3", True, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                      sel_ids=sel_ids, sel_count=sel_count))
 
 
 def step5_sparse_attn_paged(geom, q, cache: PagedCache, row_seq, row_pos, sel_ids, sel_count, out, workspace,
                             gate=None, stream=None):
     """step5_sparse_attn over the bf16 cache's pages, as step5_sparse_attn_e4m3 over the e4m3
     ones.  q as in step5_paged_attn."""
-    _run(*_attend_call("step5_sparse_attn_paged", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
-                       sel_ids=sel_ids, sel_count=sel_count))
+    _run(_attend_call("step5_sparse_attn_paged", False, geom, q, cache, row_seq, row_pos, out, workspace, gate, stream,
+                      sel_ids=sel_ids, sel_count=sel_count))
 
 
 class _Int32s:
@@ -908,13 +913,13 @@ def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws:
                          t["idx_k"].shape[2], None, None, stream),
              _attend_call(attend, cache.e4m3, geom, q_rot, cache, seq, pos, out, paged_ws, gate, stream, sel_ids=sel_ids,
                           sel_count=sel_count))
-    if plan is not None:  # (the other calls' checks first: 16 us of the host, once a step)
+    if plan is not None:  # (the other calls' checks first: 11 us of the host, once a step)
         prev = step5_set_check_only(1)
         try:
             for call in calls:
-                _run(*call)
+                _run(call)
         finally:
             step5_set_check_only(prev)
         step5_paged_plan(*plan, stream=stream, geom=geom)
     for call in calls:
-        _run(*call)
+        _run(call)
