@@ -874,13 +874,17 @@ def _check_indexers(g, t: dict, rows: dict):
     N, B, G, D = t["q"].shape[0], rows["sum_begin"].shape[0], g.num_kv_groups, g.idx_dim
     length = lambda name: t[name].shape[2] if isinstance(t[name], torch.Tensor) and t[name].dim() == 4 else -1
     t_cap, r_cap = length("idx_k"), length("summaries")
-    bf16 = torch.bfloat16
-    for name, dtype, want in (("sum_end", torch.int32, (B,)), ("idx_k", bf16, (B, G, t_cap, D)), ("idx_z", bf16, (B, G, t_cap, D)),
-                              ("summaries", torch.uint8, (B, G, r_cap, D)), ("idx_q", bf16, (N, g.idx_heads, D)),
-                              ("w", torch.float32, (N, g.idx_heads))):
-        x = (rows if name == "sum_end" else t)[name]
+    bf16, i32 = torch.bfloat16, torch.int32
+    for name, dtype, want in (("sum_begin", i32, (B,)), ("sum_end", i32, (B,)), ("idx_k", bf16, (B, G, t_cap, D)),
+                              ("idx_z", bf16, (B, G, t_cap, D)), ("summaries", torch.uint8, (B, G, r_cap, D)),
+                              ("idx_q", bf16, (N, g.idx_heads, D)), ("w", torch.float32, (N, g.idx_heads))):
+        x = (rows if name in rows else t)[name]
         if not isinstance(x, torch.Tensor) or x.dtype != dtype or tuple(x.shape) != want:
             raise ValueError(f"{name} must be {dtype} {want}, of the step's {N} rows and {B} sequences")
+    for name in ("cos", "sin"):
+        x = t[name]
+        if x is not None and (x.dtype != bf16 or x.dim() != 2 or x.shape[0] < t_cap or x.shape[1] != g.rope_dims // 2):
+            raise ValueError(f"{name} of the indexer must be {bf16} {(t_cap, g.rope_dims // 2)}, or longer")
 
 
 def decode_step_paged(geom, t: dict, cache: PagedCache, ws: Workspace, paged_ws: PagedWorkspace, k, v, sel_ids,
