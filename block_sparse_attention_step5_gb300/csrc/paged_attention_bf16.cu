@@ -27,7 +27,7 @@
 //   16 rows of 16K to 32K        120 to 135 us (by lengths and GPU)  806 MB, 6.0 to 6.7 TB/s: HBM
 //   8 x 4 rows behind 6K to 8K    31 us  117 MB in copies of 2 KB (pages of 24 tokens), 1.5 us a tile at their rate, start and join
 //   one row of 512 picks         9.6 us  latency, as the short row
-//   16 rows of 512 picks          29 us  135 MB in copies of 2 KB out of HBM, 4.6 TB/s
+//   16 rows of 512 picks          29 us  start and join (10 us), and 135 MB in copies of 2 KB out of HBM (1,024 picks 50 us, 2,048 88: 6.7 to 7 TB/s)
 //   2,048 rows of 512 picks    1,298 us  17.2 GB of copies of 2 KB out of L2, 13.2 TB/s of the 13.7 that L2 gives copies of any size
 #include "paged_items.cuh"
 
