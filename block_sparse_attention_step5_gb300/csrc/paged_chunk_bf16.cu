@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t all_ones(uint32_t u) { return ((u & 0x7fff7f
 // Adds to 64 values of each lane's head row (bf16 at out, or fp32 in groups of 8 at state) what is not finite in their dims, from
 // dim d0 on, among the noted tokens and those first .. last of its sequence b (-1: none).  The warp looks through 32 tokens at a
 // time, a token a lane, for the dims with +infinity and -infinity (NaN: both).  Rarely run, and apart from the code that is.  304
-// blocks of two sequences, 16,000 tokens each, 0.52 ms: with seven such values at both ends and in the middle 0.62, with one sequence
+// blocks of two sequences, 16,000 tokens each, 0.53 ms: with seven such values at both ends and in the middle 0.61, with one sequence
 // of nothing else 8.9.
 __device__ __noinline__ void add_not_finite(const PagedAttnParams& p, const Cleared& cl, int b, int g, int d0, int first, int last,
                                             uint16_t* out, float* state) {
